@@ -1,0 +1,132 @@
+// Appending the new rows' keys and values to a paged cache.
+//
+//   K[slot(b, pos)][h] = cast(new_k[t][h]),  pos = len[b] - (start[b+1] - t)
+//
+// and V alike; an 8-bit cache stores clamp(new / scale[h], -448, 448) rounded
+// once to E4M3.  One workgroup takes one row t for both K and V: 2 H D values,
+// eight to a thread and step.  The row's sequence is found by counting the
+// starts that are not after t, one start a thread, so that finding it costs
+// one load's latency whatever B is (a binary search: log2 B dependent loads).
+
+#include "qgemv_kv.h"
+#include "qgemv_device.h"
+
+namespace qgemv {
+
+namespace {
+
+typedef float f32x8_t __attribute__((ext_vector_type(8)));
+
+template <int SRC>
+__device__ __forceinline__ f32x8_t load8(const uint8_t *p) {
+  f32x8_t r;
+  if constexpr (SRC == QGEMV_F32) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p);
+    const f32x4_t b = *reinterpret_cast<const f32x4_t *>(p + 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[i] = a[i];
+      r[4 + i] = b[i];
+    }
+  } else {
+    const u32x4_t a = *reinterpret_cast<const u32x4_t *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (SRC == QGEMV_BF16) {
+        r[2 * i] = __builtin_bit_cast(float, a[i] << 16);
+        r[2 * i + 1] = __builtin_bit_cast(float, a[i] & 0xFFFF0000u);
+      } else {
+        r[2 * i] = half_bits_to_float(a[i] & 0xFFFFu);
+        r[2 * i + 1] = half_bits_to_float(a[i] >> 16);
+      }
+    }
+  }
+  return r;
+}
+
+// One rounding, to nearest even.  E4M3 has no infinity: values are limited to
+// +-448 first (two compares, which a NaN passes unchanged).
+template <int DST>
+__device__ __forceinline__ void store8(uint8_t *p, f32x8_t x, float scale) {
+  if constexpr (DST == QGEMV_E4M3) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = x[i] / scale;
+      v = v > 448.0f ? 448.0f : v;
+      x[i] = v < -448.0f ? -448.0f : v;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int d = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
+      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], d, true);
+    }
+    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+  } else {
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DST == QGEMV_BF16) {
+        o[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
+               (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16;
+      } else {
+        o[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[2 * i]) |
+               (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[2 * i + 1]) << 16;
+      }
+    }
+    *reinterpret_cast<u32x4_t *>(p) = o;
+  }
+}
+
+template <int SRC, int DST>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
+  const int t = blockIdx.x;
+  int seq = 0;
+  for (int base = 0; base < a.B; base += 256) {
+    const int b = base + (int)threadIdx.x;
+    seq += __syncthreads_count(b < a.B && a.start[b + 1] <= t);
+  }
+  if (seq >= a.B || t < a.start[0]) return;  // no sequence's row
+  const int64_t pos = (int64_t)a.len[seq] - ((int64_t)a.start[seq + 1] - t);
+  if (pos < 0 || pos >= (int64_t)a.c.width * a.c.page) return;
+  const int idx = page_of(a.c, (int)pos);
+  const int id = a.c.table[(int64_t)seq * a.c.width + idx];
+  if (id < 0 || id >= a.c.pages) return;
+  const int64_t slot = id * a.c.stride_page + ((int)pos - idx * a.c.page) * a.c.stride_slot;
+  constexpr int SB = SRC == QGEMV_F32 ? 4 : 2, DB = DST == QGEMV_E4M3 ? 1 : 2;
+  const int per_head = a.c.D / 8, n = a.c.H * per_head;
+  for (int i = threadIdx.x; i < 2 * n; i += 256) {
+    const bool is_v = i >= n;
+    const int e = is_v ? i - n : i;
+    const int h = e / per_head, d = (e - h * per_head) * 8;
+    const uint8_t *src = is_v ? a.nv + t * a.v_row + h * a.v_head : a.nk + t * a.k_row + h * a.k_head;
+    uint8_t *dst = (is_v ? a.c.v : a.c.k) + slot + h * a.c.stride_head;
+    const float scale = DST == QGEMV_E4M3 ? (is_v ? a.c.v_scale : a.c.k_scale)[h] : 1.0f;
+    store8<DST>(dst + d * DB, load8<SRC>(src + d * SB), scale);
+  }
+}
+
+template <int SRC>
+int launch_append_src(const AppendArgs &a, hipStream_t stream) {
+  const dim3 grid(a.T), block(256);
+  switch (a.c.dtype) {
+    case QGEMV_BF16: hipLaunchKernelGGL((append_kernel<SRC, QGEMV_BF16>), grid, block, 0, stream, a); break;
+    case QGEMV_F16: hipLaunchKernelGGL((append_kernel<SRC, QGEMV_F16>), grid, block, 0, stream, a); break;
+    case QGEMV_E4M3: hipLaunchKernelGGL((append_kernel<SRC, QGEMV_E4M3>), grid, block, 0, stream, a); break;
+    default: return QGEMV_EINVAL;
+  }
+  return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
+}
+
+}  // namespace
+
+int launch_append(const AppendArgs &a, hipStream_t stream) {
+  switch (a.src) {
+    case QGEMV_F32: return launch_append_src<QGEMV_F32>(a, stream);
+    case QGEMV_BF16: return launch_append_src<QGEMV_BF16>(a, stream);
+    case QGEMV_F16: return launch_append_src<QGEMV_F16>(a, stream);
+  }
+  return QGEMV_EINVAL;
+}
+
+}  // namespace qgemv

@@ -1,0 +1,633 @@
+// Attention of the new rows of each sequence over its paged cache.
+//
+//   s_j = scale * k_scale[h] * (q . k_j) over the tokens j that the row sees:
+//         j <= pos, and with a window W also j > pos - W or j < sinks
+//   lse = log sum_j exp(s_j),  out = v_scale[h] * sum_j exp(s_j - lse) v_j
+//
+// A key-value head's G query heads and its sequence's rows share its keys, so
+// they are one product: R = rows * G query rows against n tokens, 4 R D flops
+// for 4 D bytes of cache (16 bits).  Up to R of some hundred it is bound by
+// reading the cache, which every design choice serves.
+//
+// * A wave takes tiles of 32 tokens, up to 64 query rows (RT tiles of 16) and
+//   all of D.  S^T = K Q^T: the A operand's lane (c, g) holds 8 consecutive d
+//   of token c, so keys go from memory to the matrix units with no exchange.
+//   O^T += V^T P^T: P^T's operand lane holds 8 tokens of one query row, and
+//   the order of the tokens within the product is free, so the 4 + 4 scores
+//   that the first product leaves in a lane are that operand as they stand.
+//   V^T's lane holds 8 tokens of one d: each lane loads 8 consecutive d of
+//   those 8 tokens (whole rows of the cache per load instruction) and turns
+//   the block with byte permutes, 2 dwords an instruction.  Nothing passes
+//   through LDS, no wave waits for another.
+// * Running maximum and sum per row, in base 2.  The maximum moves only when a
+//   score passes it by more than 8 (weights stay below 2^8): most tiles then
+//   leave the output's registers alone.
+// * Keys of the next tile are loaded as soon as this tile's product has read
+//   them, values alike: while a wave computes, a whole tile is on its way.
+// * The work of a call is cut in equal ranges of granules (one tile for each
+//   wave that shares the tokens), whatever the lengths are: a workgroup walks
+//   its range over (sequence, head) items, joins its waves at the end of each
+//   item and writes the result, or its part of an item that other workgroups
+//   share, which a second kernel joins in a fixed order.
+#pragma once
+
+#include "qgemv_device.h"
+#include "qgemv_kv.h"
+
+namespace qgemv {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNegInf = -__builtin_inff();
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+template <bool BF>
+__device__ __forceinline__ f32x4_t mfma_16x16x32(u32x4_t a, u32x4_t b, f32x4_t c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// Two E4M3 bytes (bytes 2 HI, 2 HI + 1) as a pair of the product's type, exact.
+template <bool BF, bool HI>
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
+  if constexpr (BF)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+}
+
+// Two floats as a pair of the product's type, rounded to nearest even.
+template <bool BF>
+__device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
+  if constexpr (BF) {
+    const bf16x2_t v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
+           (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+  }
+}
+
+// Maximum / sum over the four lanes of a query row (lanes c, c+16, c+32, c+48).
+__device__ __forceinline__ float row_max(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                            false, false);
+  x = fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                            false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+}
+__device__ __forceinline__ float row_sum(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                            false, false);
+  x = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                            false, false);
+  return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
+}
+
+// 2^(x - m) for a maximum m of x, 0 where both are -inf.
+__device__ __forceinline__ float weight_of(float x, float m) {
+  return __builtin_amdgcn_exp2f(x - (m == kNegInf ? 0.0f : m));
+}
+
+// What one sequence asks for.
+struct SeqWork {
+  int row0, rows;   // its rows in q
+  int pos0;         // position of its first row
+  int end;          // tokens [0, end) can be seen
+  int low_tile;     // first tile of the window (0 without one)
+  int sink_tiles;   // tiles of the sinks before it
+  int tiles;        // of both
+  int granules;     // of one item
+  int items;        // (head, group of rows) items
+};
+
+__device__ __forceinline__ SeqWork seq_work(const AttendArgs &a, int b) {
+  SeqWork w;
+  const int s0 = min(max(a.start[b], 0), a.T), s1 = min(max(a.start[b + 1], s0), a.T);
+  const int len = min(max(a.len[b], 0), a.c.width * a.c.page);
+  w.row0 = s0;
+  w.rows = min(s1 - s0, a.M);
+  w.pos0 = len - (s1 - s0);
+  w.end = min(len, max(w.pos0 + w.rows, 0));
+  const int low = a.window ? max(0, w.pos0 - a.window + 1) : 0;
+  const int all = (w.end + 31) >> 5;
+  w.low_tile = low >> 5;
+  w.sink_tiles = a.window ? min(min((a.sinks >> 5) + ((a.sinks & 31) != 0), w.low_tile), all) : 0;
+  w.tiles = w.sink_tiles + max(all - w.low_tile, 0);
+  const int tw = 4 / a.chunks;
+  w.granules = max((w.tiles + tw - 1) / tw, 1);  // an item without tokens still writes its rows
+  const int item_rows = a.chunks * a.rt * 16;
+  w.items = w.rows > 0 ? a.c.H * ((w.rows * a.G + item_rows - 1) / item_rows) : 0;
+  return w;
+}
+
+// Values of one tile as they lie in memory: 8 tokens of the lane's group, E
+// consecutive d of each half of D (one half below D = 256).
+template <bool F8, int D>
+struct Tile {
+  static constexpr int KL = F8 ? D / 64 : D / 32;  // 16-byte loads of a key by one lane
+  static constexpr int VH = D == 256 ? 2 : 1;
+  static constexpr int E = D / 16 / VH;
+  static constexpr int VW = E * (F8 ? 1 : 2) / 4;  // dwords of one token's values in a half
+};
+
+template <int VW>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[VW]) {
+  if constexpr (VW == 4) {
+    const u32x4_t v = *reinterpret_cast<const u32x4_t *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v[i];
+  } else if constexpr (VW == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
+// V^T operands of d = E-chunk element e (and e + 1 for 16 bits; e .. e + 3 for
+// 8): slots (2 i, 2 i + 1) of the lane's 8 tokens in dword i.
+template <bool BF, bool F8, int VW>
+__device__ __forceinline__ void turn(const uint32_t (&v)[8][VW], int word, u32x4_t *o) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = v[2 * i][word], b = v[2 * i + 1][word];
+    if constexpr (F8) {
+      const uint32_t lo = perm_b32(b, a, 0x05010400u), hi = perm_b32(b, a, 0x07030602u);
+      o[0][i] = e4m3_pair<BF, false>(lo);
+      o[1][i] = e4m3_pair<BF, true>(lo);
+      o[2][i] = e4m3_pair<BF, false>(hi);
+      o[3][i] = e4m3_pair<BF, true>(hi);
+    } else {
+      o[0][i] = perm_b32(b, a, 0x05040100u);
+      o[1][i] = perm_b32(b, a, 0x07060302u);
+    }
+  }
+}
+
+// Whether a dword of cached values holds a NaN or an infinity.
+template <bool BF, bool F8>
+__device__ __forceinline__ bool nonfinite(uint32_t w) {
+  if constexpr (F8) {
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r |= ((w >> (8 * i)) & 0x7Fu) == 0x7Fu;
+    return r;
+  } else {
+    constexpr uint32_t x = BF ? 0x7F80u : 0x7C00u;
+    return (w & x) == x || (w >> 16 & x) == x;
+  }
+}
+
+template <bool BF, bool F8, int D, int RT, int OCC>
+__global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
+  using T = Tile<F8, D>;
+  constexpr int KL = T::KL, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
+  constexpr int CB = F8 ? 1 : 2;
+  constexpr int QS = D / 32;  // steps of the first product
+  extern __shared__ __align__(16) uint8_t lds[];
+  // [4 waves][2][32] token offsets, then the scan, then what waves hand over
+  int64_t *const ring = reinterpret_cast<int64_t *>(lds);
+  int *const scan = reinterpret_cast<int *>(lds + 2048);
+  float *const give_ml = reinterpret_cast<float *>(lds + 2048 + 64);
+  f32x4_t *const give = reinterpret_cast<f32x4_t *>(lds + 2048 + 64 + 2 * RT * 64 * 2 * 4);
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int chunk = wave & (a.chunks - 1), tw_n = 4 / a.chunks, tw = wave / a.chunks;
+
+  // ---- the range of this workgroup: granules of all items, in order
+  int b = 0, base = 0, total = 0;
+  int range0, range1;
+  {
+    int mine = 0;  // granules of this thread's sequences, 256 apart
+    for (int s = threadIdx.x; s < a.B; s += 256) {
+      const SeqWork w = seq_work(a, s);
+      mine += w.items * w.granules;
+    }
+    // B <= 256: one sequence a thread, so its inclusive scan is the plan
+    int incl = mine;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int y = __shfl_up(incl, s);
+      if (lane >= s) incl += y;
+    }
+    if (lane == 63) scan[wave] = incl;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      before += s < wave ? scan[s] : 0;
+      total += scan[s];
+    }
+    const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, a.min_granules);
+    range0 = blockIdx.x * per;
+    range1 = min(range0 + per, total);
+    if (a.B <= 256) {
+      incl += before;
+      if (mine && range0 >= incl - mine && range0 < incl) {
+        scan[4] = threadIdx.x;
+        scan[5] = incl - mine;
+      }
+      if (blockIdx.x == 0 && (int)threadIdx.x < a.B) a.plan[2 + threadIdx.x] = incl;
+    } else {
+      int carry = 0;
+      for (int s0 = 0; s0 < a.B; s0 += 256) {
+        const int s = s0 + (int)threadIdx.x;
+        int n = 0;
+        if (s < a.B) {
+          const SeqWork w = seq_work(a, s);
+          n = w.items * w.granules;
+        }
+        int in = n;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) {
+          const int y = __shfl_up(in, k);
+          if (lane >= k) in += y;
+        }
+        __syncthreads();  // the last step's sums have been read
+        if (lane == 63) scan[wave] = in;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) in += k < wave ? scan[k] : 0;
+        in += carry;
+        if (n && range0 >= in - n && range0 < in) {
+          scan[4] = s;
+          scan[5] = in - n;
+        }
+        if (blockIdx.x == 0 && s < a.B) a.plan[2 + s] = in;
+        carry += scan[0] + scan[1] + scan[2] + scan[3];
+      }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      a.plan[0] = per;
+      a.plan[1] = 0;
+    }
+    __syncthreads();
+    if (range0 >= range1) return;
+    b = __builtin_amdgcn_readfirstlane(scan[4]);
+    base = __builtin_amdgcn_readfirstlane(scan[5]);
+  }
+
+  int64_t *const my_ring = ring + wave * 64;
+
+  for (int cur = range0; cur < range1;) {
+    const SeqWork w = seq_work(a, b);
+    const int seq_granules = w.items * w.granules;
+    if (cur >= base + seq_granules) {  // past this sequence (or it has no rows)
+      base += seq_granules;
+      ++b;
+      continue;
+    }
+    const int item = (cur - base) / w.granules, first = (cur - base) - item * w.granules;
+    const int n_granules = min(w.granules - first, range1 - cur);
+    const int groups = w.items / a.c.H;
+    const int h = item / groups, group = item - h * groups;
+    cur += n_granules;
+    const bool whole = n_granules == w.granules;
+
+    const uint8_t *const kbase = a.c.k + h * a.c.stride_head;
+    const uint8_t *const vbase = a.c.v + h * a.c.stride_head;
+    const int32_t *const table = a.c.table + (int64_t)b * a.c.width;
+    const float sc = a.scale * (a.c.k_scale ? a.c.k_scale[h] : 1.0f) * kLog2e;
+    const int R = w.rows * a.G;
+    const int row_first = (group * a.chunks + chunk) * RT * 16;
+
+    // ---- the query rows, one a lane and 16-row tile; rows past R see nothing
+    int pos[RT];
+    u32x4_t qf[RT][QS];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int row = row_first + r * 16 + c;
+      const int i = row / a.G, hq = h * a.G + row - i * a.G;
+      pos[r] = row < R ? w.pos0 + i : -1;
+      const uint8_t *p = a.q + (int64_t)(w.row0 + (row < R ? i : 0)) * a.q_row + (row < R ? hq : 0) * a.q_head;
+#pragma unroll
+      for (int s = 0; s < QS; ++s) {
+        // the d of a lane's 8 slots follow the key loads
+        const int d = F8 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
+        const u32x4_t x = *reinterpret_cast<const u32x4_t *>(p + d * 2);
+        qf[r][s] = row < R ? x : u32x4_t{0, 0, 0, 0};
+      }
+    }
+
+    f32x4_t acc[RT][NE];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      m[r] = kNegInf;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) acc[r][e] = f32x4_t{0, 0, 0, 0};
+    }
+
+    const int t_end = min((first + n_granules) * tw_n, w.tiles);
+    auto tile_base = [&](int t) { return (t < w.sink_tiles ? t : t - w.sink_tiles + w.low_tile) * 32; };
+    auto load_id = [&](int t) -> int {
+      if (t >= t_end) return -1;
+      const int token = tile_base(t) + (lane & 31);
+      return token < w.end ? table[page_of(a.c, token)] : -1;
+    };
+    // offsets of a tile's tokens into the ring; bit i: token i is there
+    auto put = [&](int t, int id, int slot) -> uint32_t {
+      const int token = tile_base(t) + (lane & 31);
+      const bool ok = (uint32_t)id < (uint32_t)a.c.pages;
+      const int in_page = token - page_of(a.c, token) * a.c.page;
+      if (lane < 32) my_ring[slot * 32 + lane] = ok ? id * a.c.stride_page + in_page * a.c.stride_slot : 0;
+      return (uint32_t)__ballot(ok);
+    };
+    u32x4_t kt[2][KL];
+    uint32_t vt[VH][8][VW];
+    auto load_k = [&](int slot) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        const uint8_t *p = kbase + my_ring[slot * 32 + tt * 16 + c] + g * 16;
+#pragma unroll
+        for (int s = 0; s < KL; ++s) kt[tt][s] = *reinterpret_cast<const u32x4_t *>(p + s * 64);
+      }
+    };
+    auto load_v = [&](int slot) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t *p = vbase + my_ring[slot * 32 + (j >> 2) * 16 + g * 4 + (j & 3)] + c * (E * CB);
+#pragma unroll
+        for (int x = 0; x < VH; ++x) load_words<VW>(p + x * (128 * CB), vt[x][j]);
+      }
+    };
+
+    int t = first * tw_n + tw;
+    int slot = 0;
+    uint32_t there = 0, there_next = 0;
+    int id = -1;
+    if (t < t_end) {
+      there = put(t, load_id(t), 0);
+      id = load_id(t + tw_n);
+      load_k(0);
+      load_v(0);
+    }
+    for (; t < t_end; t += tw_n) {
+      const bool more = t + tw_n < t_end;
+      if (more) there_next = put(t + tw_n, id, slot ^ 1);
+      id = load_id(t + 2 * tw_n);
+
+      // ---- scores of 32 tokens: lane (c, g) has row c, tokens tt * 16 + 4 g + i
+      f32x4_t s[RT][2];
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r][tt] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int st = 0; st < QS; ++st) {
+          u32x4_t ka;
+          if constexpr (F8) {
+            const u32x4_t x = kt[tt][st >> 1];
+            const uint32_t x0 = x[2 * (st & 1)], x1 = x[2 * (st & 1) + 1];
+            ka = u32x4_t{e4m3_pair<BF, false>(x0), e4m3_pair<BF, true>(x0), e4m3_pair<BF, false>(x1),
+                         e4m3_pair<BF, true>(x1)};
+          } else {
+            ka = kt[tt][st];
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) s[r][tt] = mfma_16x16x32<BF>(ka, qf[r][st], s[r][tt]);
+        }
+      }
+      if (more) load_k(slot ^ 1);
+
+      const int tb = tile_base(t);
+      // whether some row does not see some token of this tile
+      const bool edge = there != 0xFFFFFFFFu || tb + 31 > w.pos0 ||
+                        (a.window && tb <= w.pos0 + w.rows - 1 - a.window && tb + 31 >= a.sinks);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[r][tt][i] *= sc;
+      if (edge) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int o = tt * 16 + g * 4 + i, j = tb + o;
+              const bool sees = (there >> o & 1) && j <= pos[r] &&
+                                (!a.window || j > pos[r] - a.window || j < a.sinks);
+              s[r][tt][i] = sees ? s[r][tt][i] : kNegInf;
+            }
+      }
+
+      // ---- weights, in place of the scores, and their pairs
+      u32x4_t pf[RT];
+      bool moves = false;
+      float top[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float x = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
+                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
+        top[r] = row_max(x);
+        moves |= top[r] > m[r] + 8.0f;
+      }
+      if (__any(moves)) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float mn = fmaxf(m[r], top[r]);
+          const float f = weight_of(m[r], mn);
+          m[r] = mn;
+          l[r] *= f;
+#pragma unroll
+          for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][e][i] *= f;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float mm = m[r] == kNegInf ? 0.0f : m[r];
+        float sum = 0.0f;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[r][tt][i] = __builtin_amdgcn_exp2f(s[r][tt][i] - mm);
+            sum += s[r][tt][i];
+          }
+        l[r] += sum;
+        // weights leave fp32 here, for the matrix product: half a step of q's
+        // type each, as much as the output's own rounding
+        pf[r] = u32x4_t{pair_of<BF>(s[r][0][0], s[r][0][1]), pair_of<BF>(s[r][0][2], s[r][0][3]),
+                        pair_of<BF>(s[r][1][0], s[r][1][1]), pair_of<BF>(s[r][1][2], s[r][1][3])};
+      }
+
+      // ---- values
+      bool odd = false;
+      if (edge) {
+        // tokens that are not there weigh 0, and 0 times what their slot holds
+        // has to be 0 too; a NaN or an infinity that only some rows see takes
+        // the way below
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool ok = there >> ((j >> 2) * 16 + g * 4 + (j & 3)) & 1;
+#pragma unroll
+          for (int x = 0; x < VH; ++x)
+#pragma unroll
+            for (int y = 0; y < VW; ++y) {
+              vt[x][j][y] = ok ? vt[x][j][y] : 0u;
+              odd |= nonfinite<BF, F8>(vt[x][j][y]);
+            }
+        }
+      }
+      constexpr int PW = F8 ? 4 : 2;  // operands of one dword column
+      if (edge && __any(odd)) {
+        // One product for each position: its tokens' values alone, added to
+        // its rows alone.
+        for (int i = 0; i < w.rows; ++i) {
+          const int at = w.pos0 + i;
+          u32x4_t mask;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int o = (x >> 1) * 16 + g * 4 + (x & 1) * 2 + y, j = tb + o;
+              const bool sees = j <= at && (!a.window || j > at - a.window || j < a.sinks);
+              bits |= sees ? 0xFFFFu << (16 * y) : 0u;
+            }
+            mask[x] = bits;
+          }
+#pragma unroll
+          for (int x = 0; x < VH; ++x)
+#pragma unroll
+            for (int y = 0; y < VW; ++y) {
+              u32x4_t o[PW];
+              turn<BF, F8, VW>(vt[x], y, o);
+#pragma unroll
+              for (int z = 0; z < PW; ++z) {
+                o[z] &= mask;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                  const f32x4_t d = mfma_16x16x32<BF>(o[z], pf[r], f32x4_t{0, 0, 0, 0});
+                  f32x4_t &to = acc[r][x * E + y * PW + z];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) to[k] = pos[r] == at ? to[k] + d[k] : to[k];
+                }
+              }
+            }
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < VH; ++x)
+#pragma unroll
+          for (int y = 0; y < VW; ++y) {
+            u32x4_t o[PW];
+            turn<BF, F8, VW>(vt[x], y, o);
+#pragma unroll
+            for (int z = 0; z < PW; ++z)
+#pragma unroll
+              for (int r = 0; r < RT; ++r)
+                acc[r][x * E + y * PW + z] = mfma_16x16x32<BF>(o[z], pf[r], acc[r][x * E + y * PW + z]);
+          }
+      }
+      if (more) load_v(slot ^ 1);
+      slot ^= 1;
+      there = there_next;
+    }
+
+    // ---- the waves that shared the tokens: the upper half gives, the lower takes
+#pragma unroll
+    for (int r = 0; r < RT; ++r) l[r] = row_sum(l[r]);
+    for (int half = tw_n >> 1; half; half >>= 1) {
+      const int seat = (tw - half) * a.chunks + chunk;  // of 2 at most
+      if (tw >= half && tw < 2 * half) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          give_ml[((seat * RT + r) * 2 + 0) * 64 + lane] = m[r];
+          give_ml[((seat * RT + r) * 2 + 1) * 64 + lane] = l[r];
+#pragma unroll
+          for (int e = 0; e < NE; ++e) give[((seat * RT + r) * NE + e) * 64 + lane] = acc[r][e];
+        }
+      }
+      __syncthreads();
+      if (tw < half) {
+        const int from = tw * a.chunks + chunk;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float m2 = give_ml[((from * RT + r) * 2 + 0) * 64 + lane];
+          const float l2 = give_ml[((from * RT + r) * 2 + 1) * 64 + lane];
+          const float mn = fmaxf(m[r], m2);
+          const float f1 = weight_of(m[r], mn), f2 = weight_of(m2, mn);
+          m[r] = mn;
+          l[r] = l[r] * f1 + l2 * f2;
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            const f32x4_t y = give[((from * RT + r) * NE + e) * 64 + lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][e][i] = acc[r][e][i] * f1 + y[i] * f2;
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- write: lane (c, g) has row c and, in each half of D, the 4 E
+    // consecutive d from 4 E g on
+    if (tw == 0) {
+      const int item_rows = a.chunks * RT * 16;
+      const float vs = a.c.v_scale ? a.c.v_scale[h] : 1.0f;
+      // a part that does not begin its item is its workgroup's first, one that
+      // begins it and does not end it is its last
+      const int64_t part = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int row = row_first + r * 16 + c;
+        if (row >= R) continue;
+        if (whole) {
+          const int i = row / a.G, hq = h * a.G + row - i * a.G;
+          const float f = l[r] == 0.0f ? 0.0f : vs / l[r];
+          uint8_t *o = a.out + (int64_t)(w.row0 + i) * a.out_row + hq * a.out_head;
+#pragma unroll
+          for (int x = 0; x < VH; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int e = 0; e < E; e += 4) {
+                uint2 y;
+                y.x = pair_of<BF>(acc[r][x * E + e][k] * f, acc[r][x * E + e + 1][k] * f);
+                y.y = pair_of<BF>(acc[r][x * E + e + 2][k] * f, acc[r][x * E + e + 3][k] * f);
+                *reinterpret_cast<uint2 *>(o + (x * 128 + (g * 4 + k) * E + e) * 2) = y;
+              }
+          if (a.lse && g == 0)
+            a.lse[(int64_t)(w.row0 + i) * (a.c.H * a.G) + hq] =
+                l[r] == 0.0f ? kNegInf : (m[r] + __builtin_log2f(l[r])) * kLn2;
+        } else {
+          const int64_t at = part * item_rows + chunk * RT * 16 + r * 16 + c;
+          float *o = a.part + at * D;
+#pragma unroll
+          for (int x = 0; x < VH; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int e = 0; e < E; e += 4)
+                *reinterpret_cast<f32x4_t *>(o + x * 128 + (g * 4 + k) * E + e) =
+                    f32x4_t{acc[r][x * E + e][k], acc[r][x * E + e + 1][k], acc[r][x * E + e + 2][k],
+                            acc[r][x * E + e + 3][k]};
+          if (g == 0) {
+            a.ml[at * 2] = m[r];
+            a.ml[at * 2 + 1] = l[r];
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace qgemv

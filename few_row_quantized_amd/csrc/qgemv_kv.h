@@ -1,0 +1,82 @@
+// Shared by the kernels of the verify step's cache operators: the arguments,
+// the page lookup and the per-sequence geometry.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qgemv_internal.h"
+
+namespace qgemv {
+
+// A paged cache as the kernels see it.  Strides are in bytes and shared by
+// keys and values; slot s of page p of head h starts at
+// p * stride_page + s * stride_slot + h * stride_head.
+struct KvView {
+  uint8_t *k, *v;
+  const int32_t *table;  // [B][width] page ids
+  const float *k_scale, *v_scale;  // [H], or null
+  int64_t stride_page, stride_slot, stride_head;
+  int pages, page, width, H, D, dtype;
+  uint32_t magic;  // token / page = (token * magic) >> shift for token < 2^31
+  int shift;
+};
+
+// ceil(2^(31 + L) / d) with L = ceil(log2 d): the quotient by an invariant
+// divisor as one multiplication, exact for every dividend below 2^31.
+inline void page_magic(int d, uint32_t *magic, int *shift) {
+  int L = 0;
+  while ((1ll << L) < d) ++L;
+  *magic = (uint32_t)(((1ull << (31 + L)) + (uint64_t)d - 1) / (uint64_t)d);
+  *shift = 31 + L;
+}
+
+__device__ __forceinline__ int page_of(const KvView &c, int token) {
+  return (int)(((uint64_t)c.magic * (uint32_t)token) >> c.shift);
+}
+
+struct AppendArgs {
+  KvView c;
+  const uint8_t *nk, *nv;
+  int64_t k_row, k_head, v_row, v_head;  // bytes
+  const int32_t *start, *len;
+  int B, T, src;
+};
+
+struct AttendArgs {
+  KvView c;
+  const uint8_t *q;
+  uint8_t *out;
+  float *lse;  // [T][Hq], or null
+  const int32_t *start, *len;
+  int32_t *plan;  // [0]: granules of a workgroup; [1 + b]: granules before sequence b; [1 + B]: all
+  float *ml;      // [2 * workgroups][rows of an item][2]: maximum and sum of a part
+  float *part;    // [2 * workgroups][rows of an item][D]: its sums
+  int64_t q_row, q_head, out_row, out_head;  // bytes
+  int B, T, M, G, window, sinks, q_dtype;
+  float scale;
+  int chunks;      // waves that share the tokens and split the rows: 1, 2 or 4
+  int rt;          // 16-row tiles of a wave
+  int workgroups;  // of the main kernel
+  int min_granules;
+  int row_splits;  // workgroups of the join for one item
+  bool joins;      // whether an item can lie in more than one workgroup
+};
+
+struct VerifyArgs {
+  const uint8_t *p, *q;  // q null: drafts without probabilities
+  int64_t p_row, q_row;  // elements
+  const int32_t *tokens;
+  const float *u;
+  const int32_t *start;
+  int32_t *out, *count;
+  double *sums;       // [B][slices * waves][2]
+  int32_t *arrived;   // [B]
+  int B, T, M, V, dtype, slices;
+};
+
+int launch_append(const AppendArgs &a, hipStream_t stream);
+int launch_attend(const AttendArgs &a, hipStream_t stream);
+int launch_verify(const VerifyArgs &a, hipStream_t stream);
+
+}  // namespace qgemv

@@ -35,9 +35,24 @@ MAX_N = 4194304
 MAX_EXPERTS = 4096
 MAX_PAIRS = 256
 
+F32 = 0
+BF16 = 1
+F16 = 2
+E4M3 = 3
+
+MAX_GROUP = 64
+MAX_CONTEXT = 1 << 30
+
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqgemv.so")
 
 _lib = None
+
+
+class _KvCacheC(ctypes.Structure):
+    """qgemv_kv_cache"""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "table", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int64) for n in ("stride_page", "stride_slot", "stride_head")]
+                + [(n, ctypes.c_int32) for n in ("pages", "page", "width", "batch", "heads", "dim", "dtype")])
 
 
 class QgemvError(RuntimeError):
@@ -75,7 +90,17 @@ def lib() -> ctypes.CDLL:
         L.qgemv_strerror.argtypes = [i]
         L.qgemv_strerror.restype = ctypes.c_char_p
         L.qgemv_version.argtypes = []
-        for name in ("qgemv_small", "qgemv_run_path", "qgemv_small_add", "qgemv_run_path_add",
+        kv, i64 = ctypes.POINTER(_KvCacheC), ctypes.c_int64
+        L.qgemv_kv_append.argtypes = [kv, vp, i64, i64, vp, i64, i64, i, vp, vp, i, vp]
+        L.qgemv_kv_attend_workspace.argtypes = [kv, i, i, i]
+        L.qgemv_kv_attend.argtypes = [kv, vp, i64, i64, vp, i64, i64, i, vp, vp, vp, i, i, i, i, i,
+                                      ctypes.c_float, vp, i64, vp]
+        L.qgemv_verify_drafts_workspace.argtypes = [i, i]
+        L.qgemv_verify_drafts.argtypes = [vp, i64, vp, i64, i, vp, vp, vp, vp, vp, i, i, i, i, vp, i64, vp]
+        L.qgemv_kv_attend_workspace.restype = i64
+        L.qgemv_verify_drafts_workspace.restype = i64
+        for name in ("qgemv_kv_append", "qgemv_kv_attend", "qgemv_verify_drafts",
+                     "qgemv_small", "qgemv_run_path", "qgemv_small_add", "qgemv_run_path_add",
                      "qgemv_small_fp", "qgemv_run_path_fp", "qgemv_select_fp", "qgemv_gather",
                      "qgemv_path_supported_fp", "qgemv_unpack_probe_fp",
                      "qgemv_select", "qgemv_path_supported",
@@ -253,3 +278,8 @@ def small(codes, scales, biases, x, bits: int, group_size: int, out=None, path="
     qgemv_run_path_add(path, codes, scales, biases, x, residual, out, M, N, K, bits, group_size,
                        stream)
     return out
+
+
+# ---------------------------------------------------------------- verify step around the products
+
+from .kv import KvCache, append, attend, attend_workspace, verify, verify_workspace  # noqa: E402,F401

@@ -294,6 +294,134 @@ int qgemv_gather(const uint8_t *codes, const uint16_t *scales, const uint16_t *b
                  const uint16_t *x, const int32_t *x_idx, const int32_t *e_idx, float *y, int P,
                  int X, int E, int N, int K, int bits, int group_size, void *stream);
 
+/*
+ * ---------------------------------------------------------------- verify step around the products
+ *
+ * What a verify step does between the quantized products: append the new
+ * rows' keys and values to a paged cache, attend from those rows over the
+ * cache, and accept or refuse the drafted tokens.
+ *
+ * Rows of several sequences lie one after another: sequence b owns the rows
+ * start[b] .. start[b+1]-1 of T (its last accepted token and the drafts after
+ * it), and len[b] counts its tokens, those rows included, so that row t is
+ * the token at position len[b] - (start[b+1] - t).  start (int32 [B+1],
+ * ascending) and len (int32 [B]) are DEVICE arrays: the host reads neither,
+ * and every value that comes from them or from the page table is checked on
+ * the device before it forms an address.
+ *
+ * Element types of these entry points.
+ */
+#define QGEMV_F32 0
+#define QGEMV_BF16 1
+#define QGEMV_F16 2
+#define QGEMV_E4M3 3 /* OCP FP8 E4M3, no infinity */
+
+#define QGEMV_MAX_GROUP 64         /* query heads on one key-value head          */
+#define QGEMV_MAX_CONTEXT (1 << 30) /* tokens of one sequence (page * width)      */
+
+/*
+ * A paged cache: page p holds `page` slots, each with a key and a value of
+ * `dim` elements for each of `heads` heads.  The token at position j of
+ * sequence b lies in slot j % page of page table[b * width + j / page].
+ * Slot s, head h of page p starts at byte p * stride_page + s * stride_slot +
+ * h * stride_head of k and of v (the same strides for both), so a cache
+ * [page][slot][head][dim] and one [page][head][slot][dim] are both described.
+ *   dtype    QGEMV_BF16, QGEMV_F16, or QGEMV_E4M3 with k_scale and v_scale
+ *            (fp32 [heads], DEVICE; the key is the stored value times its
+ *            head's scale; NULL otherwise).
+ *   Requirements (else QGEMV_EINVAL / QGEMV_EALIGN): dim 64, 128 or 256;
+ *   heads, pages, page, width and batch at least 1; page * width at most
+ *   QGEMV_MAX_CONTEXT; strides positive multiples of 16; k and v 16-byte,
+ *   table and scales 4-byte aligned.
+ * A table entry outside [0, pages) is a page that is not there: a row
+ * appended to it is dropped, and its tokens are seen by no row.  A token past
+ * the table's width is treated alike.
+ */
+typedef struct qgemv_kv_cache {
+  void *k, *v;
+  const int32_t *table;
+  const float *k_scale, *v_scale;
+  int64_t stride_page, stride_slot, stride_head;
+  int32_t pages, page, width, batch, heads, dim, dtype;
+} qgemv_kv_cache;
+
+/*
+ * qgemv_kv_append -- K[slot of row t][h] = cast(new_k[t][h]), and V alike, for
+ * the T rows of all sequences.
+ *   new_k, new_v  [T][heads][dim] of src_dtype (QGEMV_F32, QGEMV_BF16 or
+ *           QGEMV_F16; the products' fp32 output can be passed as it is);
+ *           row and head strides in elements, dim contiguous.
+ * A value is rounded once, to nearest even.  For an E4M3 cache it is divided
+ * by its head's scale (one fp32 rounding) and limited to +-448 first.  NaN
+ * stays NaN.  Rows with a negative position are dropped.  Two rows that are
+ * given the same slot leave either's value there.
+ * T = 0 does nothing.  Strides must be multiples of 16 bytes and pointers
+ * 16-byte aligned (QGEMV_EALIGN).
+ */
+int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_row, int64_t k_head,
+                    const void *new_v, int64_t v_row, int64_t v_head, int src_dtype,
+                    const int32_t *start, const int32_t *len, int T, void *stream);
+
+/*
+ * qgemv_kv_attend -- attention of the T new rows over the cache, for
+ * q_heads = G * heads query heads (query head hq reads key-value head hq / G):
+ *
+ *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+ *
+ * over the tokens j that the row at position pos sees: j <= pos, and where
+ * window > 0 also j > pos - window or j < sinks.  window = 0: all of them.
+ * A row that sees nothing gives 0 and -inf.  What an unseen slot holds (NaN
+ * and infinities too) does not reach a result.
+ *   q, out  [T][q_heads][dim] of q_dtype (QGEMV_BF16 or QGEMV_F16; a 16-bit
+ *           cache has the same type), row and head strides in elements, dim
+ *           contiguous, strides multiples of 16 bytes, 16-byte aligned.
+ *   lse     fp32 [T][q_heads] (natural logarithm), or NULL.
+ *   M       the largest number of rows of a sequence, 1..QGEMV_MAX_M (a
+ *           sequence's rows past M are left unwritten).
+ *   workspace  qgemv_kv_attend_workspace bytes, 16-byte aligned, contents
+ *           free; not shared by calls that may run at the same time.
+ * Scores, softmax statistics and sums are fp32.  Results are deterministic.
+ */
+int64_t qgemv_kv_attend_workspace(const qgemv_kv_cache *cache, int M, int q_heads, int T);
+int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head,
+                    void *out, int64_t out_row, int64_t out_head, int q_dtype, float *lse,
+                    const int32_t *start, const int32_t *len, int T, int M, int q_heads, int window,
+                    int sinks, float scale, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * qgemv_verify_drafts -- which drafted tokens of each sequence are accepted,
+ * and the token after them.
+ *   p       [T][V] target probabilities after row t (QGEMV_F32, QGEMV_BF16 or
+ *           QGEMV_F16), row stride p_row elements;
+ *   q       the draft model's probabilities the draft of row t was drawn
+ *           from, same type, row stride q_row; NULL where drafts have none
+ *           (each then counts as drawn with probability 1).
+ *   tokens  int32 [T], the token fed at row t: the draft checked against row
+ *           t is tokens[t+1] of the same sequence.
+ *   u       fp32 [T], uniform in [0, 1): row t's number decides on its draft,
+ *           the last row's draws the token.
+ * The draft d of row t is accepted while u[t] * q[t][d] < p[t][d].  At the
+ * first refusal, row r, weights are w = max(p[r] - q[r], 0) (q NULL: p[r]
+ * with the refused token's set to 0), or p[r] where those sum to 0; without a
+ * refusal w = p of the last row.  The token is the first i whose running sum
+ * w[0] + .. + w[i] exceeds u[last row] * sum(w); V - 1 where none does, 0
+ * where that product is NaN.  Products and sums are fp64.
+ *   out     int32 [T]: the accepted drafts of each sequence, the drawn token,
+ *           then -1; count int32 [B]: accepted drafts + 1 (0 for a sequence
+ *           without rows).
+ *   M       the largest number of rows of a sequence, 1..QGEMV_MAX_M (rows
+ *           past M are not looked at and left unwritten).
+ *   workspace  qgemv_verify_drafts_workspace bytes, 16-byte aligned, filled
+ *           with zeros once before its first use (every call leaves it fit
+ *           for the next); not shared by calls that may run at the same time.
+ * A draft outside [0, V) is refused.  Deterministic.
+ */
+int64_t qgemv_verify_drafts_workspace(int B, int V);
+int qgemv_verify_drafts(const void *p, int64_t p_row, const void *q, int64_t q_row, int dtype,
+                        const int32_t *tokens, const float *u, const int32_t *start, int32_t *out,
+                        int32_t *count, int B, int T, int M, int V, void *workspace,
+                        int64_t workspace_bytes, void *stream);
+
 /* qgemv_strerror -- static description of a status code. */
 const char *qgemv_strerror(int status);
 
