@@ -33,7 +33,8 @@ COMMON_FLAGS = [
 SOURCES = ["qgemv_api.cpp", "qgemv_dot.hip", "qgemv_dot_add.hip", "qgemv_dot8.hip", "qgemv_dot_fp.hip",
            "qgemv_mfma.hip",
            "qgemv_persist.hip", "qgemv_persist_x.hip", "qgemv_gather.hip", "qgemv_probe.hip",
-           "qgemv_kv_api.cpp", "qgemv_append.hip", "qgemv_attend.hip", "qgemv_verify.hip"]
+           "qgemv_kv_api.cpp", "qgemv_append.hip", "qgemv_attend.hip", "qgemv_attend_bf16.hip",
+           "qgemv_attend_f16.hip", "qgemv_attend_bf16_e4m3.hip", "qgemv_attend_f16_e4m3.hip", "qgemv_verify.hip"]
 
 
 def hipcc() -> str:

@@ -122,7 +122,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs &a, int b) {
   w.sink_tiles = a.window ? min(min((a.sinks >> 5) + ((a.sinks & 31) != 0), w.low_tile), all) : 0;
   w.tiles = w.sink_tiles + max(all - w.low_tile, 0);
   const int tw = 4 / a.chunks;
-  w.granules = max((w.tiles + tw - 1) / tw, 1);  // an item without tokens still writes its rows
+  // an item without tokens still writes its rows
+  w.granules = max((w.tiles + tw * a.span - 1) / (tw * a.span), 1);
   const int item_rows = a.chunks * a.rt * 16;
   w.items = w.rows > 0 ? a.c.H * ((w.rows * a.G + item_rows - 1) / item_rows) : 0;
   return w;
@@ -173,18 +174,40 @@ __device__ __forceinline__ void turn(const uint32_t (&v)[8][VW], int word, u32x4
   }
 }
 
-// Whether a dword of cached values holds a NaN or an infinity.
+// The bits of a dword of cached values that belong to NaNs and infinities.
 template <bool BF, bool F8>
-__device__ __forceinline__ bool nonfinite(uint32_t w) {
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
+  uint32_t m = 0;
   if constexpr (F8) {
-    bool r = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r |= ((w >> (8 * i)) & 0x7Fu) == 0x7Fu;
-    return r;
+    for (int i = 0; i < 32; i += 8) m |= (w >> i & 0x7Fu) == 0x7Fu ? 0xFFu << i : 0u;
   } else {
     constexpr uint32_t x = BF ? 0x7F80u : 0x7C00u;
-    return (w & x) == x || (w >> 16 & x) == x;
+    m = ((w & x) == x ? 0xFFFFu : 0u) | ((w >> 16 & x) == x ? 0xFFFF0000u : 0u);
   }
+  return m;
+}
+
+// Element i of a dword of cached values.
+template <bool BF, bool F8>
+__device__ __forceinline__ float value_of(uint32_t w, int i) {
+  if constexpr (F8) return e4m3_to_float(w >> (8 * i));
+  const uint32_t h = i ? w >> 16 : w & 0xFFFFu;
+  return BF ? bf16_bits_to_float(h) : half_bits_to_float(h);
+}
+
+// Workgroups of 256 threads that a CU holds, by registers: the output takes
+// D / 4 a tile of rows, a tile of keys and values D / 2 (16 bits).
+constexpr int attend_occupancy(int D, int rt) { return D * rt <= 384 ? 2 : 1; }
+
+// Queries stay in registers (D / 8 a tile of rows) while they take less than 32.
+constexpr bool queries_in_lds(int D, int rt) { return D * rt >= 256; }
+
+constexpr size_t kLdsHead = 2048 + 64;  // token offsets and the scan
+constexpr size_t attend_lds(int D, int rt, int chunks) {
+  const size_t q = queries_in_lds(D, rt) ? (size_t)chunks * rt * D * 32 : 0;
+  const size_t give = chunks == 4 ? 0 : (size_t)2 * rt * (512 + D * 64);
+  return kLdsHead + (q > give ? q : give);
 }
 
 template <bool BF, bool F8, int D, int RT, int OCC>
@@ -193,12 +216,14 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
   constexpr int KL = T::KL, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
   constexpr int CB = F8 ? 1 : 2;
   constexpr int QS = D / 32;  // steps of the first product
+  constexpr bool QLDS = queries_in_lds(D, RT);
   extern __shared__ __align__(16) uint8_t lds[];
-  // [4 waves][2][32] token offsets, then the scan, then what waves hand over
+  // [4 waves][2][32] token offsets, the scan, then the queries and, after the
+  // tokens, in the same place what waves hand over
   int64_t *const ring = reinterpret_cast<int64_t *>(lds);
   int *const scan = reinterpret_cast<int *>(lds + 2048);
-  float *const give_ml = reinterpret_cast<float *>(lds + 2048 + 64);
-  f32x4_t *const give = reinterpret_cast<f32x4_t *>(lds + 2048 + 64 + 2 * RT * 64 * 2 * 4);
+  float *const give_ml = reinterpret_cast<float *>(lds + kLdsHead);
+  f32x4_t *const give = reinterpret_cast<f32x4_t *>(lds + kLdsHead + 2 * RT * 64 * 2 * 4);
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -229,7 +254,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       before += s < wave ? scan[s] : 0;
       total += scan[s];
     }
-    const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, a.min_granules);
+    const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
     range0 = blockIdx.x * per;
     range1 = min(range0 + per, total);
     if (a.B <= 256) {
@@ -304,7 +329,9 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
 
     // ---- the query rows, one a lane and 16-row tile; rows past R see nothing
     int pos[RT];
-    u32x4_t qf[RT][QS];
+    u32x4_t qf[QLDS ? 1 : RT][QS];
+    u32x4_t *const ql = reinterpret_cast<u32x4_t *>(lds + kLdsHead) + chunk * RT * QS * 64 + lane;
+    if constexpr (QLDS) __syncthreads();  // the last item's hand-over has been read
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const int row = row_first + r * 16 + c;
@@ -315,10 +342,16 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       for (int s = 0; s < QS; ++s) {
         // the d of a lane's 8 slots follow the key loads
         const int d = F8 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-        const u32x4_t x = *reinterpret_cast<const u32x4_t *>(p + d * 2);
-        qf[r][s] = row < R ? x : u32x4_t{0, 0, 0, 0};
+        if (QLDS && s % tw_n != tw) continue;  // the waves that share the rows split them
+        u32x4_t x = *reinterpret_cast<const u32x4_t *>(p + d * 2);
+        if (row >= R) x = u32x4_t{0, 0, 0, 0};
+        if constexpr (QLDS)
+          ql[(r * QS + s) * 64] = x;
+        else
+          qf[r][s] = x;
       }
     }
+    if constexpr (QLDS) __syncthreads();
 
     f32x4_t acc[RT][NE];
     float m[RT], l[RT];
@@ -330,7 +363,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       for (int e = 0; e < NE; ++e) acc[r][e] = f32x4_t{0, 0, 0, 0};
     }
 
-    const int t_end = min((first + n_granules) * tw_n, w.tiles);
+    const int t_end = min((first + n_granules) * tw_n * a.span, w.tiles);
     auto tile_base = [&](int t) { return (t < w.sink_tiles ? t : t - w.sink_tiles + w.low_tile) * 32; };
     auto load_id = [&](int t) -> int {
       if (t >= t_end) return -1;
@@ -343,7 +376,14 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       const bool ok = (uint32_t)id < (uint32_t)a.c.pages;
       const int in_page = token - page_of(a.c, token) * a.c.page;
       if (lane < 32) my_ring[slot * 32 + lane] = ok ? id * a.c.stride_page + in_page * a.c.stride_slot : 0;
+      // a wave's LDS accesses stay in order; this keeps the compiler from moving them
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       return (uint32_t)__ballot(ok);
+    };
+    // whether some row does not see some token of a tile
+    auto is_edge = [&](int tb, uint32_t present) {
+      return present != 0xFFFFFFFFu || tb + 31 > w.pos0 ||
+             (a.window && tb <= w.pos0 + w.rows - 1 - a.window && tb + 31 >= a.sinks);
     };
     u32x4_t kt[2][KL];
     uint32_t vt[VH][8][VW];
@@ -364,9 +404,10 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       }
     };
 
-    int t = first * tw_n + tw;
+    int t = first * tw_n * a.span + tw;
     int slot = 0;
     uint32_t there = 0, there_next = 0;
+    bool strays = false;  // values that were taken out
     int id = -1;
     if (t < t_end) {
       there = put(t, load_id(t), 0);
@@ -397,15 +438,20 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
             ka = kt[tt][st];
           }
 #pragma unroll
-          for (int r = 0; r < RT; ++r) s[r][tt] = mfma_16x16x32<BF>(ka, qf[r][st], s[r][tt]);
+          for (int r = 0; r < RT; ++r) {
+            u32x4_t qa;
+            if constexpr (QLDS)
+              qa = ql[(r * QS + st) * 64];
+            else
+              qa = qf[r][st];
+            s[r][tt] = mfma_16x16x32<BF>(ka, qa, s[r][tt]);
+          }
         }
       }
       if (more) load_k(slot ^ 1);
 
       const int tb = tile_base(t);
-      // whether some row does not see some token of this tile
-      const bool edge = there != 0xFFFFFFFFu || tb + 31 > w.pos0 ||
-                        (a.window && tb <= w.pos0 + w.rows - 1 - a.window && tb + 31 >= a.sinks);
+      const bool edge = is_edge(tb, there);
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -469,11 +515,11 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       }
 
       // ---- values
-      bool odd = false;
       if (edge) {
-        // tokens that are not there weigh 0, and 0 times what their slot holds
-        // has to be 0 too; a NaN or an infinity that only some rows see takes
-        // the way below
+        // a token that is not there, or that only some rows see, may hold
+        // anything, and 0 times a NaN or an infinity is not 0: these are taken
+        // out here and given to the rows that see them after the tiles
+        uint32_t odd = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const bool ok = there >> ((j >> 2) * 16 + g * 4 + (j & 3)) & 1;
@@ -485,64 +531,77 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
               odd |= nonfinite<BF, F8>(vt[x][j][y]);
             }
         }
+        if (__any(odd != 0)) {
+          strays = true;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int x = 0; x < VH; ++x)
+#pragma unroll
+              for (int y = 0; y < VW; ++y) vt[x][j][y] &= ~nonfinite<BF, F8>(vt[x][j][y]);
+        }
       }
       constexpr int PW = F8 ? 4 : 2;  // operands of one dword column
-      if (edge && __any(odd)) {
-        // One product for each position: its tokens' values alone, added to
-        // its rows alone.
-        for (int i = 0; i < w.rows; ++i) {
-          const int at = w.pos0 + i;
-          u32x4_t mask;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t bits = 0;
+      for (int x = 0; x < VH; ++x)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int o = (x >> 1) * 16 + g * 4 + (x & 1) * 2 + y, j = tb + o;
-              const bool sees = j <= at && (!a.window || j > at - a.window || j < a.sinks);
-              bits |= sees ? 0xFFFFu << (16 * y) : 0u;
-            }
-            mask[x] = bits;
-          }
+        for (int y = 0; y < VW; ++y) {
+          u32x4_t o[PW];
+          turn<BF, F8, VW>(vt[x], y, o);
 #pragma unroll
-          for (int x = 0; x < VH; ++x)
+          for (int z = 0; z < PW; ++z)
 #pragma unroll
-            for (int y = 0; y < VW; ++y) {
-              u32x4_t o[PW];
-              turn<BF, F8, VW>(vt[x], y, o);
-#pragma unroll
-              for (int z = 0; z < PW; ++z) {
-                o[z] &= mask;
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                  const f32x4_t d = mfma_16x16x32<BF>(o[z], pf[r], f32x4_t{0, 0, 0, 0});
-                  f32x4_t &to = acc[r][x * E + y * PW + z];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) to[k] = pos[r] == at ? to[k] + d[k] : to[k];
-                }
-              }
-            }
+            for (int r = 0; r < RT; ++r)
+              acc[r][x * E + y * PW + z] = mfma_16x16x32<BF>(o[z], pf[r], acc[r][x * E + y * PW + z]);
         }
-      } else {
-#pragma unroll
-        for (int x = 0; x < VH; ++x)
-#pragma unroll
-          for (int y = 0; y < VW; ++y) {
-            u32x4_t o[PW];
-            turn<BF, F8, VW>(vt[x], y, o);
-#pragma unroll
-            for (int z = 0; z < PW; ++z)
-#pragma unroll
-              for (int r = 0; r < RT; ++r)
-                acc[r][x * E + y * PW + z] = mfma_16x16x32<BF>(o[z], pf[r], acc[r][x * E + y * PW + z]);
-          }
-      }
       if (more) load_v(slot ^ 1);
       slot ^= 1;
       there = there_next;
     }
 
+    if (strays) {
+      // The NaNs and infinities of the tiles above, to the rows that see their
+      // tokens: lane (c, g) holds row c and, of each half of D, the 4 E
+      // consecutive d from 4 E g on.
+#pragma unroll 1
+      for (int t2 = first * tw_n * a.span + tw; t2 < t_end; t2 += tw_n) {
+        const uint32_t present = put(t2, load_id(t2), 0);
+        const int tb = tile_base(t2);
+        if (!is_edge(tb, present)) continue;
+#pragma unroll 1
+        for (int o = 0; o < 32; ++o) {
+          if (!(present >> o & 1)) continue;
+          const uint8_t *p = vbase + my_ring[o] + g * 4 * E * CB;
+          uint32_t sees[RT];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int j = tb + o;
+            sees[r] = j <= pos[r] && (!a.window || j > pos[r] - a.window || j < a.sinks) ? ~0u : 0u;
+            asm volatile("" : "+v"(sees[r]));  // a mask in a register, no select for each value
+          }
+#pragma unroll
+          for (int x = 0; x < VH; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t v[VW];
+              load_words<VW>(p + (x * 128 + k * E) * CB, v);
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                constexpr int PER = 4 / CB;
+                const uint32_t word = v[e / PER];
+                const bool is = nonfinite<BF, F8>(word) >> (e % PER * 8 * CB) & 1;
+                const uint32_t val = is ? __builtin_bit_cast(uint32_t, value_of<BF, F8>(word, e % PER)) : 0u;
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                  acc[r][x * E + e][k] += __builtin_bit_cast(float, val & sees[r]);
+              }
+            }
+        }
+      }
+    }
+
     // ---- the waves that shared the tokens: the upper half gives, the lower takes
+    if (QLDS && tw_n > 1) __syncthreads();  // the queries have been read
 #pragma unroll
     for (int r = 0; r < RT; ++r) l[r] = row_sum(l[r]);
     for (int half = tw_n >> 1; half; half >>= 1) {
@@ -628,6 +687,112 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       }
     }
   }
+}
+
+// Joins the parts of the items that several workgroups shared.  A team of D / 4
+// threads takes a row and all or every 8th of its parts, in order, with a
+// running maximum; teams of one row are joined in order through LDS.
+template <bool BF, int D>
+__global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
+  constexpr int TEAM = D / 4, TEAMS = 256 / TEAM;
+  const int item_rows = a.chunks * a.rt * 16;
+  const int groups_max = (a.M * a.G + item_rows - 1) / item_rows;
+  const int b = blockIdx.x / (a.c.H * groups_max), hg = blockIdx.x - b * (a.c.H * groups_max);
+  const SeqWork w = seq_work(a, b);
+  const int groups = w.items / a.c.H, h = hg / groups_max, group = hg - h * groups_max;
+  if (group >= groups) return;
+  const int per = a.plan[0];
+  const int g0 = a.plan[1 + b] + (h * groups + group) * w.granules, g1 = g0 + w.granules;
+  const int w0 = g0 / per, w1 = (g1 - 1) / per;
+  if (w0 == w1) return;  // written by its workgroup
+  const int rows = min(w.rows * a.G - group * item_rows, item_rows);
+  const int parts = w1 - w0 + 1;
+  const int per_row = parts >= 2 * TEAMS ? TEAMS : 1;  // teams of a row
+  const int team = threadIdx.x / TEAM, d = (threadIdx.x % TEAM) * 4;
+  const int sub = team % per_row, at_once = TEAMS / per_row;
+  __shared__ f32x4_t sums[256];
+  __shared__ float stats[TEAMS][2];
+  const float vs = a.c.v_scale ? a.c.v_scale[h] : 1.0f;
+  for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
+    const int row = r0 + team / per_row;
+    float m = kNegInf, l = 0.0f;
+    f32x4_t acc = {0, 0, 0, 0};
+    if (row < rows) {
+#pragma unroll 4
+      for (int i = sub; i < parts; i += per_row) {
+        const int64_t at = (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * item_rows + row;
+        const float m2 = a.ml[at * 2], l2 = a.ml[at * 2 + 1];
+        const f32x4_t y = *reinterpret_cast<const f32x4_t *>(a.part + at * D + d);
+        const float mn = fmaxf(m, m2), f1 = weight_of(m, mn), f2 = weight_of(m2, mn);
+        m = mn;
+        l = l * f1 + l2 * f2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = acc[k] * f1 + y[k] * f2;
+      }
+    }
+    if (per_row > 1) {  // one row in flight
+      if (d == 0) {
+        stats[team][0] = m;
+        stats[team][1] = l;
+      }
+      sums[threadIdx.x] = acc;
+      __syncthreads();
+      if (team == 0) {
+        for (int i = 1; i < per_row; ++i) {
+          const float m2 = stats[i][0], l2 = stats[i][1];
+          const f32x4_t y = sums[i * TEAM + threadIdx.x];
+          const float mn = fmaxf(m, m2), f1 = weight_of(m, mn), f2 = weight_of(m2, mn);
+          m = mn;
+          l = l * f1 + l2 * f2;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[k] = acc[k] * f1 + y[k] * f2;
+        }
+      }
+      __syncthreads();
+    }
+    if (row < rows && sub == 0) {
+      const int r = group * item_rows + row, i = r / a.G, hq = h * a.G + r - i * a.G;
+      const float f = l == 0.0f ? 0.0f : vs / l;
+      uint2 y;
+      y.x = pair_of<BF>(acc[0] * f, acc[1] * f);
+      y.y = pair_of<BF>(acc[2] * f, acc[3] * f);
+      *reinterpret_cast<uint2 *>(a.out + (int64_t)(w.row0 + i) * a.out_row + hq * a.out_head + d * 2) = y;
+      if (a.lse && d == 0)
+        a.lse[(int64_t)(w.row0 + i) * (a.c.H * a.G) + hq] =
+            l == 0.0f ? kNegInf : (m + __builtin_log2f(l)) * kLn2;
+    }
+  }
+}
+
+template <bool BF, bool F8, int D, int RT>
+int launch_attend_rt(const AttendArgs &a, hipStream_t stream) {
+  constexpr int OCC = attend_occupancy(D, RT);
+  const auto kern = attend_kernel<BF, F8, D, RT, OCC>;
+  const size_t bytes = attend_lds(D, RT, a.chunks);
+  if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
+  hipLaunchKernelGGL(kern, dim3(a.workgroups), dim3(256), bytes, stream, a);
+  if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
+  if (!a.joins) return QGEMV_OK;
+  const int item_rows = a.chunks * a.rt * 16, groups = (a.M * a.G + item_rows - 1) / item_rows;
+  hipLaunchKernelGGL((join_kernel<BF, D>), dim3(a.B * a.c.H * groups, a.row_splits), dim3(256), 0, stream, a);
+  return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
+}
+
+template <bool BF, bool F8>
+int launch_attend_t(const AttendArgs &a, hipStream_t stream) {
+  switch (a.c.D * 8 + a.rt) {
+    case 64 * 8 + 1: return launch_attend_rt<BF, F8, 64, 1>(a, stream);
+    case 64 * 8 + 2: return launch_attend_rt<BF, F8, 64, 2>(a, stream);
+    case 64 * 8 + 3: return launch_attend_rt<BF, F8, 64, 3>(a, stream);
+    case 64 * 8 + 4: return launch_attend_rt<BF, F8, 64, 4>(a, stream);
+    case 128 * 8 + 1: return launch_attend_rt<BF, F8, 128, 1>(a, stream);
+    case 128 * 8 + 2: return launch_attend_rt<BF, F8, 128, 2>(a, stream);
+    case 128 * 8 + 3: return launch_attend_rt<BF, F8, 128, 3>(a, stream);
+    case 128 * 8 + 4: return launch_attend_rt<BF, F8, 128, 4>(a, stream);
+    case 256 * 8 + 1: return launch_attend_rt<BF, F8, 256, 1>(a, stream);
+    case 256 * 8 + 2: return launch_attend_rt<BF, F8, 256, 2>(a, stream);
+  }
+  return QGEMV_EUNSUPPORTED;
 }
 
 }  // namespace qgemv

@@ -58,7 +58,7 @@ struct AttendArgs {
   int chunks;      // waves that share the tokens and split the rows: 1, 2 or 4
   int rt;          // 16-row tiles of a wave
   int workgroups;  // of the main kernel
-  int min_granules;
+  int span;        // tiles of a wave in a granule
   int row_splits;  // workgroups of the join for one item
   bool joins;      // whether an item can lie in more than one workgroup
 };
@@ -76,6 +76,9 @@ struct VerifyArgs {
 };
 
 int launch_append(const AppendArgs &a, hipStream_t stream);
+// Fills in the launch (chunks .. joins) and the workspace's layout from
+// `work`, and returns its size in bytes.
+int64_t plan_attend(AttendArgs *a, void *work);
 int launch_attend(const AttendArgs &a, hipStream_t stream);
 int launch_verify(const VerifyArgs &a, hipStream_t stream);
 

@@ -101,7 +101,14 @@ int64_t qgemv_kv_attend_workspace(const qgemv_kv_cache *cache, int M, int q_head
   int s = view_of(cache, &v);
   if (s != QGEMV_OK) return s;
   if ((s = attend_shape(cache, M, q_heads, T)) != QGEMV_OK) return s;
-  return 16;
+  AttendArgs a;
+  a.c = v;
+  a.B = cache->batch;
+  a.T = T;
+  a.M = M;
+  a.G = q_heads / cache->heads;
+  a.window = a.sinks = 0;  // the most that any window needs
+  return qgemv::plan_attend(&a, nullptr);
 }
 
 int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head,
@@ -118,9 +125,8 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
   if ((s = rows_status(start, len, T)) != QGEMV_OK) return s;
   if ((s = operand_status(q, q_row, q_head, a.c.D, q_dtype)) != QGEMV_OK) return s;
   if ((s = operand_status(out, out_row, out_head, a.c.D, q_dtype)) != QGEMV_OK) return s;
-  if (!workspace || workspace_bytes < qgemv_kv_attend_workspace(cache, M, q_heads, T)) return QGEMV_EINVAL;
+  if (!workspace) return QGEMV_EINVAL;
   if (!aligned(lse, 4) || !aligned(workspace, 16)) return QGEMV_EALIGN;
-  if (T == 0) return QGEMV_OK;
   a.q = static_cast<const uint8_t *>(q);
   a.out = static_cast<uint8_t *>(out);
   a.lse = lse;
@@ -139,6 +145,10 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
   a.sinks = sinks;
   a.q_dtype = q_dtype;
   a.scale = scale;
+  const int64_t need = qgemv::plan_attend(&a, workspace);
+  if (need < 0) return (int)need;
+  if (need > workspace_bytes) return QGEMV_EINVAL;
+  if (T == 0) return QGEMV_OK;
   return qgemv::launch_attend(a, reinterpret_cast<hipStream_t>(stream));
 }
 
