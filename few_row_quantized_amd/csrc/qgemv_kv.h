@@ -70,7 +70,7 @@ struct VerifyArgs {
   const float *u;
   const int32_t *start;
   int32_t *out, *count;
-  double *sums;       // [B][slices * waves][2]
+  double *sums;       // [B][4 * slices][2]: of what is left, of p
   int32_t *arrived;   // [B]
   int B, T, M, V, dtype, slices;
 };
@@ -80,6 +80,7 @@ int launch_append(const AppendArgs &a, hipStream_t stream);
 // `work`, and returns its size in bytes.
 int64_t plan_attend(AttendArgs *a, void *work);
 int launch_attend(const AttendArgs &a, hipStream_t stream);
+int64_t plan_verify(VerifyArgs *a, void *work);  // slices and workspace alike
 int launch_verify(const VerifyArgs &a, hipStream_t stream);
 
 }  // namespace qgemv

@@ -153,8 +153,11 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
 }
 
 int64_t qgemv_verify_drafts_workspace(int B, int V) {
-  if (B < 1 || V < 1) return QGEMV_EINVAL;
-  return 16;
+  if (B < 1 || V < 1 || V > QGEMV_MAX_VOCABULARY) return QGEMV_EINVAL;
+  VerifyArgs a;
+  a.B = B;
+  a.V = V;
+  return qgemv::plan_verify(&a, nullptr);
 }
 
 int qgemv_verify_drafts(const void *p, int64_t p_row, const void *q, int64_t q_row, int dtype,
@@ -162,10 +165,9 @@ int qgemv_verify_drafts(const void *p, int64_t p_row, const void *q, int64_t q_r
                         int32_t *count, int B, int T, int M, int V, void *workspace,
                         int64_t workspace_bytes, void *stream) {
   if (dtype != QGEMV_F32 && dtype != QGEMV_BF16 && dtype != QGEMV_F16) return QGEMV_EINVAL;
-  if (B < 1 || V < 1 || T < 0 || M < 1 || M > QGEMV_MAX_M) return QGEMV_EINVAL;
+  if (B < 1 || V < 1 || V > QGEMV_MAX_VOCABULARY || T < 0 || M < 1 || M > QGEMV_MAX_M) return QGEMV_EINVAL;
   if (!p || !tokens || !u || !start || !out || !count || !workspace) return QGEMV_EINVAL;
   if (p_row < V || (q && q_row < V)) return QGEMV_EINVAL;
-  if (workspace_bytes < qgemv_verify_drafts_workspace(B, V)) return QGEMV_EINVAL;
   const uintptr_t b = (uintptr_t)elem_bytes(dtype);
   if (!aligned(p, b) || !aligned(q, b) || !aligned(tokens, 4) || !aligned(u, 4) || !aligned(start, 4) ||
       !aligned(out, 4) || !aligned(count, 4) || !aligned(workspace, 16))
@@ -185,6 +187,7 @@ int qgemv_verify_drafts(const void *p, int64_t p_row, const void *q, int64_t q_r
   a.M = M;
   a.V = V;
   a.dtype = dtype;
+  if (qgemv::plan_verify(&a, workspace) > workspace_bytes) return QGEMV_EINVAL;
   return qgemv::launch_verify(a, reinterpret_cast<hipStream_t>(stream));
 }
 

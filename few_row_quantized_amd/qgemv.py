@@ -42,6 +42,7 @@ E4M3 = 3
 
 MAX_GROUP = 64
 MAX_CONTEXT = 1 << 30
+MAX_VOCABULARY = 1 << 24
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqgemv.so")
 

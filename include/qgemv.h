@@ -318,6 +318,7 @@ int qgemv_gather(const uint8_t *codes, const uint16_t *scales, const uint16_t *b
 
 #define QGEMV_MAX_GROUP 64         /* query heads on one key-value head          */
 #define QGEMV_MAX_CONTEXT (1 << 30) /* tokens of one sequence (page * width)      */
+#define QGEMV_MAX_VOCABULARY (1 << 24)
 
 /*
  * A paged cache: page p holds `page` slots, each with a key and a value of
