@@ -108,7 +108,20 @@ struct SeqWork {
   int items;        // (head, group of rows) items
 };
 
-__device__ __forceinline__ SeqWork seq_work(const AttendArgs &a, int b) {
+// A kernel's arguments where the launch put them.  Read through a pointer that
+// is made opaque between the parts of the kernel, so that what only one part
+// needs is loaded there and not kept in scalar registers across the tile loop.
+typedef const __attribute__((address_space(4))) AttendArgs KernArgs;
+__device__ __forceinline__ KernArgs *kern_args() {
+  return (KernArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+}
+__device__ __forceinline__ KernArgs *reload(KernArgs *p) {
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+template <class Args>
+__device__ __forceinline__ SeqWork seq_work(Args &a, int b) {
   SeqWork w;
   const int s0 = min(max(a.start[b], 0), a.T), s1 = min(max(a.start[b + 1], s0), a.T);
   const int len = min(max(a.len[b], 0), a.c.width * a.c.page);
@@ -210,8 +223,66 @@ constexpr size_t attend_lds(int D, int rt, int chunks) {
   return kLdsHead + (q > give ? q : give);
 }
 
+// The range of this workgroup: granules [cur, range1) of all items in order,
+// the first of them in sequence b, before which lie `base`.  False if there is
+// none.  Workgroup 0 writes the plan for the join.
+template <class Args>
+__device__ __forceinline__ bool attend_range(Args &a, int *scan, int *b, int *base, int *cur, int *range1) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int B = a.B;
+  int total = 0, per = 1;
+  // Steps of 256 sequences, one a thread.  The total is needed before a range
+  // can be placed: with more sequences the steps are taken twice.
+  for (int round = B <= 256; round < 2; ++round) {
+    int carry = 0;
+    for (int s0 = 0; s0 < B; s0 += 256) {
+      const int s = s0 + (int)threadIdx.x;
+      int n = 0;
+      if (s < B) {
+        const SeqWork w = seq_work(a, s);
+        n = w.items * w.granules;
+      }
+      int in = n;
+#pragma unroll
+      for (int k = 1; k < 64; k <<= 1) {
+        const int y = __shfl_up(in, k);
+        if (lane >= k) in += y;
+      }
+      if (lane == 63) scan[wave] = in;
+      __syncthreads();
+      const int n0 = scan[0], n1 = scan[1], n2 = scan[2], n3 = scan[3];
+      in += carry + (wave > 0 ? n0 : 0) + (wave > 1 ? n1 : 0) + (wave > 2 ? n2 : 0);
+      carry += n0 + n1 + n2 + n3;
+      if (B <= 256) total = carry;
+      if (round) {
+        per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+        const int at = blockIdx.x * per;
+        if (n && at >= in - n && at < in) {
+          scan[4] = s;
+          scan[5] = in - n;
+        }
+        if (blockIdx.x == 0 && s < B) a.plan[2 + s] = in;
+      }
+      __syncthreads();
+    }
+    total = carry;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.plan[0] = max(per, 1);
+    a.plan[1] = 0;
+  }
+  *cur = blockIdx.x * per;
+  *range1 = min(*cur + per, total);
+  if (*cur >= *range1) return false;
+  *b = __builtin_amdgcn_readfirstlane(scan[4]);
+  *base = __builtin_amdgcn_readfirstlane(scan[5]);
+  *range1 = __builtin_amdgcn_readfirstlane(*range1);
+  *cur = __builtin_amdgcn_readfirstlane(*cur);
+  return true;
+}
+
 template <bool BF, bool F8, int D, int RT, int OCC>
-__global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   using T = Tile<F8, D>;
   constexpr int KL = T::KL, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
   constexpr int CB = F8 ? 1 : 2;
@@ -222,91 +293,25 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
   // tokens, in the same place what waves hand over
   int64_t *const ring = reinterpret_cast<int64_t *>(lds);
   int *const scan = reinterpret_cast<int *>(lds + 2048);
+  u32x4_t *const queries = reinterpret_cast<u32x4_t *>(lds + kLdsHead);
   float *const give_ml = reinterpret_cast<float *>(lds + kLdsHead);
   f32x4_t *const give = reinterpret_cast<f32x4_t *>(lds + kLdsHead + 2 * RT * 64 * 2 * 4);
 
+  KernArgs *ap = kern_args();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int chunk = wave & (a.chunks - 1), tw_n = 4 / a.chunks, tw = wave / a.chunks;
+  const int chunks = ap->chunks;
+  const int tw_n = 4 / chunks, chunk = wave & (chunks - 1), tw = wave / chunks;
 
-  // ---- the range of this workgroup: granules of all items, in order
-  int b = 0, base = 0, total = 0;
-  int range0, range1;
-  {
-    int mine = 0;  // granules of this thread's sequences, 256 apart
-    for (int s = threadIdx.x; s < a.B; s += 256) {
-      const SeqWork w = seq_work(a, s);
-      mine += w.items * w.granules;
-    }
-    // B <= 256: one sequence a thread, so its inclusive scan is the plan
-    int incl = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int y = __shfl_up(incl, s);
-      if (lane >= s) incl += y;
-    }
-    if (lane == 63) scan[wave] = incl;
-    __syncthreads();
-    int before = 0;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      before += s < wave ? scan[s] : 0;
-      total += scan[s];
-    }
-    const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
-    range0 = blockIdx.x * per;
-    range1 = min(range0 + per, total);
-    if (a.B <= 256) {
-      incl += before;
-      if (mine && range0 >= incl - mine && range0 < incl) {
-        scan[4] = threadIdx.x;
-        scan[5] = incl - mine;
-      }
-      if (blockIdx.x == 0 && (int)threadIdx.x < a.B) a.plan[2 + threadIdx.x] = incl;
-    } else {
-      int carry = 0;
-      for (int s0 = 0; s0 < a.B; s0 += 256) {
-        const int s = s0 + (int)threadIdx.x;
-        int n = 0;
-        if (s < a.B) {
-          const SeqWork w = seq_work(a, s);
-          n = w.items * w.granules;
-        }
-        int in = n;
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) {
-          const int y = __shfl_up(in, k);
-          if (lane >= k) in += y;
-        }
-        __syncthreads();  // the last step's sums have been read
-        if (lane == 63) scan[wave] = in;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) in += k < wave ? scan[k] : 0;
-        in += carry;
-        if (n && range0 >= in - n && range0 < in) {
-          scan[4] = s;
-          scan[5] = in - n;
-        }
-        if (blockIdx.x == 0 && s < a.B) a.plan[2 + s] = in;
-        carry += scan[0] + scan[1] + scan[2] + scan[3];
-      }
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      a.plan[0] = per;
-      a.plan[1] = 0;
-    }
-    __syncthreads();
-    if (range0 >= range1) return;
-    b = __builtin_amdgcn_readfirstlane(scan[4]);
-    base = __builtin_amdgcn_readfirstlane(scan[5]);
-  }
+  int b, base, cur, range1;
+  if (!attend_range(*ap, scan, &b, &base, &cur, &range1)) return;
 
   int64_t *const my_ring = ring + wave * 64;
 
-  for (int cur = range0; cur < range1;) {
-    const SeqWork w = seq_work(a, b);
+  while (cur < range1) {
+    ap = reload(ap);
+    const SeqWork w = seq_work(*ap, b);
     const int seq_granules = w.items * w.granules;
     if (cur >= base + seq_granules) {  // past this sequence (or it has no rows)
       base += seq_granules;
@@ -315,43 +320,46 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
     }
     const int item = (cur - base) / w.granules, first = (cur - base) - item * w.granules;
     const int n_granules = min(w.granules - first, range1 - cur);
-    const int groups = w.items / a.c.H;
+    const int groups = w.items / ap->c.H;
     const int h = item / groups, group = item - h * groups;
     cur += n_granules;
-    const bool whole = n_granules == w.granules;
 
-    const uint8_t *const kbase = a.c.k + h * a.c.stride_head;
-    const uint8_t *const vbase = a.c.v + h * a.c.stride_head;
-    const int32_t *const table = a.c.table + (int64_t)b * a.c.width;
-    const float sc = a.scale * (a.c.k_scale ? a.c.k_scale[h] : 1.0f) * kLog2e;
-    const int R = w.rows * a.G;
-    const int row_first = (group * a.chunks + chunk) * RT * 16;
+    const int R = w.rows * ap->G;
+    const int row_first = (group * chunks + chunk) * RT * 16;
 
     // ---- the query rows, one a lane and 16-row tile; rows past R see nothing
     int pos[RT];
     u32x4_t qf[QLDS ? 1 : RT][QS];
-    u32x4_t *const ql = reinterpret_cast<u32x4_t *>(lds + kLdsHead) + chunk * RT * QS * 64 + lane;
-    if constexpr (QLDS) __syncthreads();  // the last item's hand-over has been read
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int row = row_first + r * 16 + c;
-      const int i = row / a.G, hq = h * a.G + row - i * a.G;
-      pos[r] = row < R ? w.pos0 + i : -1;
-      const uint8_t *p = a.q + (int64_t)(w.row0 + (row < R ? i : 0)) * a.q_row + (row < R ? hq : 0) * a.q_head;
-#pragma unroll
-      for (int s = 0; s < QS; ++s) {
+    {
+      const int G = ap->G;
+      auto query = [&](int row, int s) -> u32x4_t {
+        const int i = row / G, hq = h * G + row - i * G;
         // the d of a lane's 8 slots follow the key loads
         const int d = F8 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-        if (QLDS && s % tw_n != tw) continue;  // the waves that share the rows split them
-        u32x4_t x = *reinterpret_cast<const u32x4_t *>(p + d * 2);
-        if (row >= R) x = u32x4_t{0, 0, 0, 0};
-        if constexpr (QLDS)
-          ql[(r * QS + s) * 64] = x;
-        else
-          qf[r][s] = x;
+        u32x4_t x = {0, 0, 0, 0};
+        if (row < R) x = *reinterpret_cast<const u32x4_t *>(ap->q + (int64_t)(w.row0 + i) * ap->q_row + hq * ap->q_head + d * 2);
+        return x;
+      };
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int row = row_first + r * 16 + c;
+        pos[r] = row < R ? w.pos0 + row / G : -1;
+        if constexpr (!QLDS) {
+#pragma unroll
+          for (int s = 0; s < QS; ++s) qf[r][s] = query(row, s);
+        }
+      }
+      if constexpr (QLDS) {
+        // [wave's rows][tile][step][lane], every wave a quarter of the steps
+        __syncthreads();  // the last item's hand-over has been read
+        const int first_row = group * chunks * RT * 16;
+#pragma unroll 4
+        for (int u = wave; u < chunks * RT * QS; u += 4)
+          queries[u * 64 + lane] = query(first_row + u / QS * 16 + c, u % QS);
+        __syncthreads();
       }
     }
-    if constexpr (QLDS) __syncthreads();
+    const u32x4_t *const ql = queries + chunk * RT * QS * 64 + lane;
 
     f32x4_t acc[RT][NE];
     float m[RT], l[RT];
@@ -363,27 +371,39 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       for (int e = 0; e < NE; ++e) acc[r][e] = f32x4_t{0, 0, 0, 0};
     }
 
-    const int t_end = min((first + n_granules) * tw_n * a.span, w.tiles);
-    auto tile_base = [&](int t) { return (t < w.sink_tiles ? t : t - w.sink_tiles + w.low_tile) * 32; };
-    auto load_id = [&](int t) -> int {
-      if (t >= t_end) return -1;
-      const int token = tile_base(t) + (lane & 31);
-      return token < w.end ? table[page_of(a.c, token)] : -1;
+    ap = reload(ap);
+    const uint8_t *const kbase = ap->c.k + h * ap->c.stride_head;
+    const uint8_t *const vbase = ap->c.v + h * ap->c.stride_head;
+    const int32_t *const table = ap->c.table + (int64_t)b * ap->c.width;
+    const int64_t stride_page = ap->c.stride_page, stride_slot = ap->c.stride_slot;
+    const int page = ap->c.page, pages = ap->c.pages, shift = ap->c.shift;
+    const uint32_t magic = ap->c.magic;
+    const int window = ap->window ? ap->window : 1 << 30;  // none: as wide as any position
+    const int sinks = ap->sinks;
+    const float sc = ap->scale * (ap->c.k_scale ? ap->c.k_scale[h] : 1.0f) * kLog2e;
+    const int t_end = min((first + n_granules) * tw_n * ap->span, w.tiles);
+    int t = first * tw_n * ap->span + tw;
+
+    auto tile_base = [&](int tile) { return (tile < w.sink_tiles ? tile : tile - w.sink_tiles + w.low_tile) * 32; };
+    auto load_id = [&](int tile) -> int {
+      const int token = tile_base(tile) + (lane & 31);
+      return tile < t_end && token < w.end ? table[__umulhi(magic, 2 * token) >> shift] : -1;
     };
     // offsets of a tile's tokens into the ring; bit i: token i is there
-    auto put = [&](int t, int id, int slot) -> uint32_t {
-      const int token = tile_base(t) + (lane & 31);
-      const bool ok = (uint32_t)id < (uint32_t)a.c.pages;
-      const int in_page = token - page_of(a.c, token) * a.c.page;
-      if (lane < 32) my_ring[slot * 32 + lane] = ok ? id * a.c.stride_page + in_page * a.c.stride_slot : 0;
+    auto put = [&](int tile, int id, int slot) -> uint32_t {
+      const int token = tile_base(tile) + (lane & 31);
+      const bool ok = (uint32_t)id < (uint32_t)pages;
+      const int in_page = token - (int)(__umulhi(magic, 2 * token) >> shift) * page;
+      const int64_t at = ok ? id * stride_page + in_page * stride_slot : 0;
+      if (lane < 32) my_ring[slot * 32 + lane] = at;
       // a wave's LDS accesses stay in order; this keeps the compiler from moving them
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       return (uint32_t)__ballot(ok);
     };
     // whether some row does not see some token of a tile
     auto is_edge = [&](int tb, uint32_t present) {
-      return present != 0xFFFFFFFFu || tb + 31 > w.pos0 ||
-             (a.window && tb <= w.pos0 + w.rows - 1 - a.window && tb + 31 >= a.sinks);
+      return (present != 0xFFFFFFFFu) | (tb + 31 > w.pos0) |
+             ((tb <= w.pos0 + w.rows - 1 - window) & (tb + 31 >= sinks));
     };
     u32x4_t kt[2][KL];
     uint32_t vt[VH][8][VW];
@@ -404,7 +424,6 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       }
     };
 
-    int t = first * tw_n * a.span + tw;
     int slot = 0;
     uint32_t there = 0, there_next = 0;
     bool strays = false;  // values that were taken out
@@ -417,38 +436,43 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
     }
     for (; t < t_end; t += tw_n) {
       const bool more = t + tw_n < t_end;
-      if (more) there_next = put(t + tw_n, id, slot ^ 1);
+      there_next = put(t + tw_n, id, slot ^ 1);
       id = load_id(t + 2 * tw_n);
 
       // ---- scores of 32 tokens: lane (c, g) has row c, tokens tt * 16 + 4 g + i
       f32x4_t s[RT][2];
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r][tt] = f32x4_t{0, 0, 0, 0};
+        for (int tt = 0; tt < 2; ++tt) s[r][tt] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int st = 0; st < QS; ++st) {
-          u32x4_t ka;
+      for (int st = 0; st < QS; ++st) {
+        u32x4_t ka[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
           if constexpr (F8) {
             const u32x4_t x = kt[tt][st >> 1];
             const uint32_t x0 = x[2 * (st & 1)], x1 = x[2 * (st & 1) + 1];
-            ka = u32x4_t{e4m3_pair<BF, false>(x0), e4m3_pair<BF, true>(x0), e4m3_pair<BF, false>(x1),
-                         e4m3_pair<BF, true>(x1)};
+            ka[tt] = u32x4_t{e4m3_pair<BF, false>(x0), e4m3_pair<BF, true>(x0), e4m3_pair<BF, false>(x1),
+                             e4m3_pair<BF, true>(x1)};
           } else {
-            ka = kt[tt][st];
-          }
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            u32x4_t qa;
-            if constexpr (QLDS)
-              qa = ql[(r * QS + st) * 64];
-            else
-              qa = qf[r][st];
-            s[r][tt] = mfma_16x16x32<BF>(ka, qa, s[r][tt]);
+            ka[tt] = kt[tt][st];
           }
         }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          u32x4_t qa;
+          if constexpr (QLDS)
+            qa = ql[(r * QS + st) * 64];
+          else
+            qa = qf[r][st];
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) s[r][tt] = mfma_16x16x32<BF>(ka[tt], qa, s[r][tt]);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
       if (more) load_k(slot ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
 
       const int tb = tile_base(t);
       const bool edge = is_edge(tb, there);
@@ -459,15 +483,17 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[r][tt][i] *= sc;
       if (edge) {
+        const uint32_t mine = there >> (g * 4);
+        const int j0 = tb + g * 4;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int o = tt * 16 + g * 4 + i, j = tb + o;
-              const bool sees = (there >> o & 1) && j <= pos[r] &&
-                                (!a.window || j > pos[r] - a.window || j < a.sinks);
+              const int o = tt * 16 + i;
+              const bool sees = ((mine >> o & 1) != 0) & (o <= pos[r] - j0) &
+                                ((o > pos[r] - window - j0) | (o < sinks - j0));
               s[r][tt][i] = sees ? s[r][tt][i] : kNegInf;
             }
       }
@@ -520,14 +546,15 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
         // anything, and 0 times a NaN or an infinity is not 0: these are taken
         // out here and given to the rows that see them after the tiles
         uint32_t odd = 0;
+        const uint32_t mine = there >> (g * 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const bool ok = there >> ((j >> 2) * 16 + g * 4 + (j & 3)) & 1;
+          const uint32_t ok = 0u - (mine >> ((j >> 2) * 16 + (j & 3)) & 1u);
 #pragma unroll
           for (int x = 0; x < VH; ++x)
 #pragma unroll
             for (int y = 0; y < VW; ++y) {
-              vt[x][j][y] = ok ? vt[x][j][y] : 0u;
+              vt[x][j][y] &= ok;
               odd |= nonfinite<BF, F8>(vt[x][j][y]);
             }
         }
@@ -554,7 +581,9 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
             for (int r = 0; r < RT; ++r)
               acc[r][x * E + y * PW + z] = mfma_16x16x32<BF>(o[z], pf[r], acc[r][x * E + y * PW + z]);
         }
+      __builtin_amdgcn_sched_barrier(0);
       if (more) load_v(slot ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
       slot ^= 1;
       there = there_next;
     }
@@ -564,7 +593,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       // tokens: lane (c, g) holds row c and, of each half of D, the 4 E
       // consecutive d from 4 E g on.
 #pragma unroll 1
-      for (int t2 = first * tw_n * a.span + tw; t2 < t_end; t2 += tw_n) {
+      for (int t2 = first * tw_n * ap->span + tw; t2 < t_end; t2 += tw_n) {
         const uint32_t present = put(t2, load_id(t2), 0);
         const int tb = tile_base(t2);
         if (!is_edge(tb, present)) continue;
@@ -576,7 +605,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
             const int j = tb + o;
-            sees[r] = j <= pos[r] && (!a.window || j > pos[r] - a.window || j < a.sinks) ? ~0u : 0u;
+            sees[r] = (j <= pos[r]) & ((j > pos[r] - window) | (j < sinks)) ? ~0u : 0u;
             asm volatile("" : "+v"(sees[r]));  // a mask in a register, no select for each value
           }
 #pragma unroll
@@ -601,11 +630,12 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
     }
 
     // ---- the waves that shared the tokens: the upper half gives, the lower takes
+    ap = reload(ap);
     if (QLDS && tw_n > 1) __syncthreads();  // the queries have been read
 #pragma unroll
     for (int r = 0; r < RT; ++r) l[r] = row_sum(l[r]);
     for (int half = tw_n >> 1; half; half >>= 1) {
-      const int seat = (tw - half) * a.chunks + chunk;  // of 2 at most
+      const int seat = (tw - half) * chunks + chunk;  // of 2 at most
       if (tw >= half && tw < 2 * half) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -617,7 +647,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       }
       __syncthreads();
       if (tw < half) {
-        const int from = tw * a.chunks + chunk;
+        const int from = tw * chunks + chunk;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           const float m2 = give_ml[((from * RT + r) * 2 + 0) * 64 + lane];
@@ -640,8 +670,8 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
     // ---- write: lane (c, g) has row c and, in each half of D, the 4 E
     // consecutive d from 4 E g on
     if (tw == 0) {
-      const int item_rows = a.chunks * RT * 16;
-      const float vs = a.c.v_scale ? a.c.v_scale[h] : 1.0f;
+      const int G = ap->G;
+      const float vs = ap->c.v_scale ? ap->c.v_scale[h] : 1.0f;
       // a part that does not begin its item is its workgroup's first, one that
       // begins it and does not end it is its last
       const int64_t part = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
@@ -649,10 +679,10 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
       for (int r = 0; r < RT; ++r) {
         const int row = row_first + r * 16 + c;
         if (row >= R) continue;
-        if (whole) {
-          const int i = row / a.G, hq = h * a.G + row - i * a.G;
+        if (n_granules == w.granules) {
+          const int i = row / G, hq = h * G + row - i * G;
           const float f = l[r] == 0.0f ? 0.0f : vs / l[r];
-          uint8_t *o = a.out + (int64_t)(w.row0 + i) * a.out_row + hq * a.out_head;
+          uint8_t *o = ap->out + (int64_t)(w.row0 + i) * ap->out_row + hq * ap->out_head;
 #pragma unroll
           for (int x = 0; x < VH; ++x)
 #pragma unroll
@@ -664,12 +694,12 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
                 y.y = pair_of<BF>(acc[r][x * E + e + 2][k] * f, acc[r][x * E + e + 3][k] * f);
                 *reinterpret_cast<uint2 *>(o + (x * 128 + (g * 4 + k) * E + e) * 2) = y;
               }
-          if (a.lse && g == 0)
-            a.lse[(int64_t)(w.row0 + i) * (a.c.H * a.G) + hq] =
+          if (ap->lse && g == 0)
+            ap->lse[(int64_t)(w.row0 + i) * (ap->c.H * G) + hq] =
                 l[r] == 0.0f ? kNegInf : (m[r] + __builtin_log2f(l[r])) * kLn2;
         } else {
-          const int64_t at = part * item_rows + chunk * RT * 16 + r * 16 + c;
-          float *o = a.part + at * D;
+          const int64_t at = (part * chunks + chunk) * RT * 16 + r * 16 + c;
+          float *o = ap->part + at * D;
 #pragma unroll
           for (int x = 0; x < VH; ++x)
 #pragma unroll
@@ -680,8 +710,8 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs a) {
                     f32x4_t{acc[r][x * E + e][k], acc[r][x * E + e + 1][k], acc[r][x * E + e + 2][k],
                             acc[r][x * E + e + 3][k]};
           if (g == 0) {
-            a.ml[at * 2] = m[r];
-            a.ml[at * 2 + 1] = l[r];
+            ap->ml[at * 2] = m[r];
+            ap->ml[at * 2 + 1] = l[r];
           }
         }
       }

@@ -18,21 +18,22 @@ struct KvView {
   const float *k_scale, *v_scale;  // [H], or null
   int64_t stride_page, stride_slot, stride_head;
   int pages, page, width, H, D, dtype;
-  uint32_t magic;  // token / page = (token * magic) >> shift for token < 2^31
+  uint32_t magic;  // token / page = (2 token * magic) >> (32 + shift) for token < 2^30
   int shift;
 };
 
 // ceil(2^(31 + L) / d) with L = ceil(log2 d): the quotient by an invariant
-// divisor as one multiplication, exact for every dividend below 2^31.
+// divisor as one multiplication and a shift by 31 + L, exact for every
+// dividend below 2^31.
 inline void page_magic(int d, uint32_t *magic, int *shift) {
   int L = 0;
   while ((1ll << L) < d) ++L;
   *magic = (uint32_t)(((1ull << (31 + L)) + (uint64_t)d - 1) / (uint64_t)d);
-  *shift = 31 + L;
+  *shift = L;
 }
 
 __device__ __forceinline__ int page_of(const KvView &c, int token) {
-  return (int)(((uint64_t)c.magic * (uint32_t)token) >> c.shift);
+  return (int)(__umulhi(c.magic, 2u * (uint32_t)token) >> c.shift);
 }
 
 struct AppendArgs {
