@@ -61,6 +61,7 @@ struct AttendArgs {
   int workgroups;  // of the main kernel
   int span;        // tiles of a wave in a granule
   int row_splits;  // workgroups of the join for one item
+  int seq_items;   // items of a sequence of M rows
   bool joins;      // whether an item can lie in more than one workgroup
 };
 
@@ -71,9 +72,11 @@ struct VerifyArgs {
   const float *u;
   const int32_t *start;
   int32_t *out, *count;
-  double *sums;       // [B][4 * slices][2]: of what is left, of p
-  int32_t *arrived;   // [B]
-  int B, T, M, V, dtype, slices;
+  double *sums;       // [B][pieces][2]: of what is left, of p
+  int32_t *arrived;   // [B], where slices > 1
+  int B, T, M, V, dtype;
+  int per, pieces;    // tokens of a piece, pieces of a row
+  int each, slices;   // pieces of a wave, workgroups of a sequence
 };
 
 int launch_append(const AppendArgs &a, hipStream_t stream);

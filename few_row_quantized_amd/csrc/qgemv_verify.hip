@@ -13,14 +13,14 @@
 // there, and a sum of 10^5 probabilities leaves a token's share of the number
 // line where it is.
 //
-// One launch.  A sequence's row is cut into pieces, one a wave, 4 waves a
-// workgroup: each wave checks the drafts itself (they decide which row is
-// summed; at most 15 pairs of loads, one a lane), sums its piece and leaves
-// the sum in the workspace.  The workgroup that arrives last at the sequence's
-// counter scans the sums in order, finds the piece where the running sum
-// passes the number, scans that piece again and writes the answer; it also
-// sets the counter back to 0.  Which workgroup is last changes nothing in the
-// result.
+// One launch.  A row is cut into at most 256 pieces, whole loads of a wave, as
+// its length alone says; each wave checks the drafts itself (they decide which
+// row is summed; at most 15 pairs of loads, one a lane), sums its pieces and
+// leaves the sums in the workspace.  The workgroup that arrives last at the
+// sequence's counter scans the sums in order, finds the piece where the running
+// sum passes the number, scans that piece again and writes the answer; it also
+// sets the counter back to 0.  Neither which workgroup is last nor how many
+// share a sequence changes a result.
 
 #include "qgemv_kv.h"
 #include "qgemv_device.h"
@@ -29,7 +29,8 @@ namespace qgemv {
 
 namespace {
 
-constexpr int kMaxPieces = 256;  // of a row: the last workgroup has one thread for each
+constexpr int kMaxPieces = 256;       // of a row: the last workgroup has one thread for each
+constexpr int kMaxWorkgroups = 2048;  // all of them at once on the card, 8 on a CU
 
 template <int DT>
 __device__ __forceinline__ float prob(const uint8_t *row, int i) {
@@ -41,26 +42,25 @@ __device__ __forceinline__ float prob(const uint8_t *row, int i) {
   }
 }
 
-// 16 bytes of a row as floats.  Rows start at any element (an odd vocabulary),
-// so the load is only element-aligned; the hardware takes that.
+// 16 bytes of a row.  Rows start at any element (an odd vocabulary), so the
+// load is only element-aligned; the hardware takes that.
 template <int DT>
-struct Piece16 {
-  static constexpr int N = DT == QGEMV_F32 ? 4 : 8;
-  static __device__ __forceinline__ void load(const uint8_t *row, int i, float (&x)[N]) {
-    u32x4_t w;
-    __builtin_memcpy(&w, row + (int64_t)i * (16 / N), 16);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if constexpr (DT == QGEMV_F32) {
-        const uint32_t b = w[k];  // (a bit cast of the element itself takes the vector's first)
-        x[k] = __builtin_bit_cast(float, b);
-      } else {
-        const uint32_t b = k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu;
-        x[k] = DT == QGEMV_BF16 ? bf16_bits_to_float(b) : half_bits_to_float(b);
-      }
-    }
+__device__ __forceinline__ u32x4_t load16(const uint8_t *row, int i) {
+  u32x4_t w;
+  __builtin_memcpy(&w, row + (int64_t)i * (DT == QGEMV_F32 ? 4 : 2), 16);
+  return w;
+}
+
+// Element k of them.
+template <int DT>
+__device__ __forceinline__ float elem(u32x4_t w, int k) {
+  if constexpr (DT == QGEMV_F32) {
+    const uint32_t b = w[k];  // (a bit cast of the element itself takes the vector's first)
+    return __builtin_bit_cast(float, b);
   }
-};
+  const uint32_t b = k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu;
+  return DT == QGEMV_BF16 ? bf16_bits_to_float(b) : half_bits_to_float(b);
+}
 
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
@@ -103,9 +103,72 @@ __device__ __forceinline__ double rest_of(float p, float q) {
   return d < 0.0 ? 0.0 : d;
 }
 
+// A wave's pieces [first, last) of a row: sums of what is left of p, and of p
+// itself, into the workspace.  Loads of U steps (64 lanes of 16 bytes) are in
+// flight before the first of them is summed.
+template <int DT, bool HAS_Q>
+__device__ __forceinline__ void sum_pieces(const uint8_t *p, const uint8_t *q, int drop, int first, int last,
+                                           int per, int V, double *sums) {
+  constexpr int N = DT == QGEMV_F32 ? 4 : 8, U = HAS_Q ? 2 : 4, STEP = 64 * N;
+  const int lane = threadIdx.x & 63, v_end = min(last * per, V);
+  double left = 0.0, all = 0.0;
+  int piece = first, edge = min((first + 1) * per, V);  // where the piece ends
+  for (int v0 = first * per; v0 < v_end; v0 += U * STEP) {
+    u32x4_t x[U], y[U];
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      const int i = v0 + s * STEP + lane * N;
+      if (i + N <= v_end) {
+        x[s] = load16<DT>(p, i);
+        if (HAS_Q) y[s] = load16<DT>(q, i);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      const int at = v0 + s * STEP, i = at + lane * N;
+      double sum = 0.0, rest = 0.0;
+      if (i + N <= v_end) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float z = elem<DT>(x[s], k);
+          sum += z;
+          if (HAS_Q) rest += rest_of(z, elem<DT>(y[s], k));
+        }
+      } else {
+        for (int v = i; v < v_end; ++v) {  // at most one lane holds the row's ragged end
+          const float z = prob<DT>(p, v);
+          sum += z;
+          if (HAS_Q) rest += rest_of(z, prob<DT>(q, v));
+        }
+      }
+      if (!HAS_Q) {
+        rest = sum;
+        if (drop >= i && drop < min(i + N, v_end)) {  // without its weight, never by a difference
+          rest = 0.0;
+          for (int v = i; v < min(i + N, v_end); ++v) rest += v == drop ? 0.0 : (double)prob<DT>(p, v);
+        }
+      }
+      all += sum;
+      left += rest;
+      if (piece < last && at + STEP >= edge) {
+        // stored past this XCD's caches, as agent-scope atomics are
+        left = wave_sum(left);
+        all = wave_sum(all);
+        if (lane == 0) {
+          __hip_atomic_store(sums + piece * 2, left, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(sums + piece * 2 + 1, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        left = all = 0.0;
+        ++piece;
+        edge = min(edge + per, V);
+      }
+    }
+  }
+}
+
 template <int DT>
-__global__ __launch_bounds__(256) void verify_kernel(VerifyArgs a) {
-  constexpr int SB = DT == QGEMV_F32 ? 4 : 2, N = Piece16<DT>::N;
+__global__ __launch_bounds__(256, 8) void verify_kernel(VerifyArgs a) {
+  constexpr int SB = DT == QGEMV_F32 ? 4 : 2;
   const int b = blockIdx.x / a.slices, slice = blockIdx.x - b * a.slices;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int s0 = min(max(a.start[b], 0), a.T);
@@ -131,45 +194,25 @@ __global__ __launch_bounds__(256) void verify_kernel(VerifyArgs a) {
   const uint8_t *p = a.p + (s0 + n) * a.p_row * SB;
   const uint8_t *q = refused && a.q ? a.q + (s0 + n) * a.q_row * SB : nullptr;
 
-  // ---- this wave's piece: what is left of p, and p itself
-  const int pieces = 4 * a.slices, per = (a.V + pieces - 1) / pieces;
-  const int piece = slice * 4 + wave;
-  const int v0 = min(piece * per, a.V), v1 = min(v0 + per, a.V);
-  double left = 0.0, all = 0.0;
-  int i = v0 + lane * N;
-#pragma unroll 4
-  for (; i + N <= v1; i += 64 * N) {
-    float x[N], y[N];
-    Piece16<DT>::load(p, i, x);
-    if (q) Piece16<DT>::load(q, i, y);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      all += x[k];
-      left += q ? rest_of(x[k], y[k]) : i + k == drop ? 0.0 : (double)x[k];
-    }
-  }
-  for (; i < v1; ++i) {  // at most one lane holds the piece's ragged end
-    const float x = prob<DT>(p, i);
-    all += x;
-    left += q ? rest_of(x, prob<DT>(q, i)) : i == drop ? 0.0 : (double)x;
-  }
-  left = wave_sum(left);
-  all = wave_sum(all);
+  // ---- this wave's pieces
+  double *const sums = a.sums + (int64_t)b * a.pieces * 2;
+  const int first = (slice * 4 + wave) * a.each, last = min(first + a.each, a.pieces);
+  if (q)
+    sum_pieces<DT, true>(p, q, drop, first, last, a.per, a.V, sums);
+  else
+    sum_pieces<DT, false>(p, q, drop, first, last, a.per, a.V, sums);
 
-  // ---- leave the sums; the last workgroup of the sequence goes on.  The sums
-  // are stored past the caches of this XCD, and the counter's release and
-  // acquire order them for the workgroup that reads them.
-  double *const sums = a.sums + (int64_t)b * pieces * 2;
-  if (lane == 0) {
-    __hip_atomic_store(sums + piece * 2, left, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(sums + piece * 2 + 1, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  // ---- the last workgroup of the sequence goes on
   __shared__ double part[4];
   __shared__ int ints[4];
   if (a.slices > 1) {
+    // Every wave waits until its sums have arrived, then the count goes up.  A
+    // release on the counter would also write back this XCD's whole L2, one
+    // workgroup after the other (64 sequences of 151936 tokens: 55 us, not 23).
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
-      const int before = __hip_atomic_fetch_add(a.arrived + b, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+      const int before = __hip_atomic_fetch_add(a.arrived + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       ints[0] = before == a.slices - 1;
       if (before == a.slices - 1)
         __hip_atomic_store(a.arrived + b, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -182,7 +225,7 @@ __global__ __launch_bounds__(256) void verify_kernel(VerifyArgs a) {
     if (!last) return;
   }
 
-  const bool has = (int)threadIdx.x < pieces;
+  const bool has = (int)threadIdx.x < a.pieces;
   const double my_left =
       has ? __hip_atomic_load(sums + threadIdx.x * 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
   const double my_all =
@@ -198,22 +241,35 @@ __global__ __launch_bounds__(256) void verify_kernel(VerifyArgs a) {
   if (!(share == share)) {
     token = 0;
   } else if (share < total) {
-    const int at = min(block_first(has && run > share, ints), pieces - 1);
+    const int at = min(block_first(has && run > share, ints), a.pieces - 1);
     __shared__ double before_at;
     if ((int)threadIdx.x == at) before_at = run - (use_all ? my_all : my_left);
-    // the piece again, consecutive tokens a thread
-    const int a0 = min(at * per, a.V), a1 = min(a0 + per, a.V), each = (per + 255) / 256;
+    // the piece again, consecutive tokens a thread, four loads at a time
+    const int a0 = at * a.per, a1 = min(a0 + a.per, a.V), each = (a.per + 255) / 256;
     const int t0 = min(a0 + (int)threadIdx.x * each, a1), t1 = min(t0 + each, a1);
-    auto weight = [&](int v) -> double {
-      const float x = prob<DT>(p, v);
-      return use_all ? (double)x : q ? rest_of(x, prob<DT>(q, v)) : v == drop ? 0.0 : (double)x;
+    float x[4], y[4];
+    auto load4 = [&](int v) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(v + k, a.V - 1);
+        x[k] = prob<DT>(p, i);
+        y[k] = q ? prob<DT>(q, i) : 0.0f;
+      }
+    };
+    auto weight = [&](int v, int k) -> double {
+      return use_all ? (double)x[k] : q ? rest_of(x[k], y[k]) : v + k == drop ? 0.0 : (double)x[k];
     };
     double mine = 0.0;
     int weighted = -1;  // the last token here that has a weight
-    for (int v = t0; v < t1; ++v) {
-      const double w = weight(v);
-      mine += w;
-      if (w > 0.0) weighted = v;
+    for (int v = t0; v < t1; v += 4) {
+      load4(v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (v + k >= t1) continue;
+        const double w = weight(v, k);
+        mine += w;
+        if (w > 0.0) weighted = v + k;
+      }
     }
     double ignored;
     double upto = block_scan(mine, part, &ignored);
@@ -227,14 +283,22 @@ __global__ __launch_bounds__(256) void verify_kernel(VerifyArgs a) {
       // last of its tokens that has a weight
       if (weighted >= 0) atomicMax(&drawn, weighted);
     } else if ((int)threadIdx.x == who) {
-      double c = upto - mine;
-      int v = t0;
-      for (; v < t1 - 1; ++v) {
-        c += weight(v);
-        if (c > share) break;
-      }
       // (rounded another way: the last with a weight)
-      drawn = v == t1 - 1 && weighted >= 0 ? weighted : v;
+      double c = upto - mine;
+      int found = weighted >= 0 ? weighted : t1 - 1;
+      for (int v = t0, done = 0; v < t1 && !done; v += 4) {
+        if (t1 - t0 > 4) load4(v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (done || v + k >= t1) continue;
+          c += weight(v, k);
+          if (c > share) {
+            found = v + k;
+            done = 1;
+          }
+        }
+      }
+      drawn = found;
     }
     __syncthreads();
     if (drawn >= 0) token = drawn;
@@ -248,18 +312,21 @@ __global__ __launch_bounds__(256) void verify_kernel(VerifyArgs a) {
 }  // namespace
 
 int64_t plan_verify(VerifyArgs *a, void *work) {
-  // Pieces of at least 512 tokens (two 16-byte loads of fp32 a lane), about
-  // 1024 workgroups in all.
-  int slices = (int)(((int64_t)a->V + 2047) / 2048);
-  const int most = 1024 / a->B;
-  if (slices > most) slices = most;
-  if (slices > kMaxPieces / 4) slices = kMaxPieces / 4;
-  if (slices < 1) slices = 1;
-  a->slices = slices;
-  const int64_t sums = (int64_t)a->B * slices * 4 * 2 * 8;
-  a->sums = static_cast<double *>(work);
-  a->arrived = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(work) + sums);
-  return sums + 4 * (int64_t)a->B;
+  // The counters have a place of their own whatever B and V are, so that calls
+  // of several sizes can share a workspace: sequences of more than one
+  // workgroup are at most half of kMaxWorkgroups.
+  constexpr int64_t counters = kMaxWorkgroups / 2 * 4;
+  // Pieces are whole steps of a wave (16 bytes a lane, of the smallest type).
+  const int step = 512;
+  a->per = ((a->V + kMaxPieces - 1) / kMaxPieces + step - 1) / step * step;
+  a->pieces = (a->V + a->per - 1) / a->per;
+  int most = kMaxWorkgroups / a->B;
+  if (most < 1) most = 1;
+  a->each = (a->pieces + 4 * most - 1) / (4 * most);
+  a->slices = (a->pieces + 4 * a->each - 1) / (4 * a->each);
+  a->arrived = static_cast<int32_t *>(work);
+  a->sums = reinterpret_cast<double *>(static_cast<uint8_t *>(work) + counters);
+  return counters + (int64_t)a->B * a->pieces * 16;
 }
 
 int launch_verify(const VerifyArgs &a, hipStream_t stream) {

@@ -512,3 +512,28 @@ def test_verify_repeats_on_one_workspace():
     got = q.verify(p, d, tok, u, start, 5, workspace=work, stream=s)
     s.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_verify_calls_of_several_sizes_share_a_workspace():
+    sizes = [([5], 40000), ([2] * 300, 1500), ([4, 3, 1] * 9, 9001), ([3] * 1500, 70), ([16, 1], 300001)]
+    problems = [draft_problem(rows, V, seed=V) for rows, V in sizes]
+    need = max(q.lib().qgemv_verify_drafts_workspace(len(rows), V) for rows, V in sizes)
+    work = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for i in range(3):
+        for (rows, V), x in zip(sizes, problems):
+            args = [t.cuda() for t in x]
+            want = q.verify(*args, max(rows))
+            got = q.verify(*args, max(rows), workspace=work)
+            assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]), (i, len(rows), V)
+
+
+def test_verify_does_not_depend_on_the_other_sequences():
+    """A sequence's answer is the same alone and among others, where other
+    numbers of workgroups share it."""
+    p, d, tok, u, start = (x.cuda() for x in draft_problem([4, 2, 7, 1] * 30, 20011, seed=8))
+    out, n = q.verify(p, d, tok, u, start, 7)
+    for b in (0, 1, 2, 3, 61, 119):
+        s, e = int(start[b]), int(start[b + 1])
+        one = torch.tensor([0, e - s], dtype=torch.int32, device="cuda")
+        o, m = q.verify(p[s:e], d[s:e], tok[s:e].clone(), u[s:e].clone(), one, 7)
+        assert torch.equal(o, out[s:e]) and torch.equal(m, n[b:b + 1])
