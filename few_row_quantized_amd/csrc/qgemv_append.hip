@@ -4,9 +4,11 @@
 //
 // and V alike; an 8-bit cache stores clamp(new / scale[h], -448, 448) rounded
 // once to E4M3.  One workgroup takes one row t for both K and V: 2 H D values,
-// eight to a thread and step.  The row's sequence is found by counting the
-// starts that are not after t, one start a thread, so that finding it costs
-// one load's latency whatever B is (a binary search: log2 B dependent loads).
+// eight to a thread and step.  The first step's values are loaded before the
+// slot is known, so that reading them and finding it overlap.  The row's
+// sequence is found by counting the starts that are not after t, one start a
+// thread, so that finding it costs one load's latency whatever B is (a binary
+// search: log2 B dependent loads).
 
 #include "qgemv_kv.h"
 #include "qgemv_device.h"
@@ -80,7 +82,21 @@ __device__ __forceinline__ void store8(uint8_t *p, f32x8_t x, float scale) {
 
 template <int SRC, int DST>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
+  constexpr int SB = SRC == QGEMV_F32 ? 4 : 2, DB = DST == QGEMV_E4M3 ? 1 : 2;
   const int t = blockIdx.x;
+  const int per_head = a.c.D / 8, n = a.c.H * per_head;
+  int i = threadIdx.x, h = 0, d = 0;
+  bool is_v = false;
+  auto load = [&]() {
+    is_v = i >= n;
+    const int e = is_v ? i - n : i;
+    h = e / per_head;
+    d = (e - h * per_head) * 8;
+    return load8<SRC>((is_v ? a.nv + t * a.v_row + h * a.v_head : a.nk + t * a.k_row + h * a.k_head) + d * SB);
+  };
+  f32x8_t x = {};
+  if (i < 2 * n) x = load();
+
   int seq = 0;
   for (int base = 0; base < a.B; base += 256) {
     const int b = base + (int)threadIdx.x;
@@ -93,16 +109,12 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   const int id = a.c.table[(int64_t)seq * a.c.width + idx];
   if (id < 0 || id >= a.c.pages) return;
   const int64_t slot = id * a.c.stride_page + ((int)pos - idx * a.c.page) * a.c.stride_slot;
-  constexpr int SB = SRC == QGEMV_F32 ? 4 : 2, DB = DST == QGEMV_E4M3 ? 1 : 2;
-  const int per_head = a.c.D / 8, n = a.c.H * per_head;
-  for (int i = threadIdx.x; i < 2 * n; i += 256) {
-    const bool is_v = i >= n;
-    const int e = is_v ? i - n : i;
-    const int h = e / per_head, d = (e - h * per_head) * 8;
-    const uint8_t *src = is_v ? a.nv + t * a.v_row + h * a.v_head : a.nk + t * a.k_row + h * a.k_head;
+  while (i < 2 * n) {
     uint8_t *dst = (is_v ? a.c.v : a.c.k) + slot + h * a.c.stride_head;
     const float scale = DST == QGEMV_E4M3 ? (is_v ? a.c.v_scale : a.c.k_scale)[h] : 1.0f;
-    store8<DST>(dst + d * DB, load8<SRC>(src + d * SB), scale);
+    store8<DST>(dst + d * DB, x, scale);
+    i += 256;
+    if (i < 2 * n) x = load();
   }
 }
 
