@@ -31,13 +31,15 @@ int64_t plan_attend(AttendArgs *a, void *work) {
   a->joins = granules > 4;
   a->span = a->joins ? 1 : (int)granules;
   const int64_t items = (int64_t)a->B * a->c.H * groups;
-  if (items * granules >= (1 << 30)) return QGEMV_EUNSUPPORTED;  // counted in 32 bits on the device
+  // counted in 32 bits on the device, and threads of a grid on the host
+  if (items * granules >= (1 << 30) || items >= (1 << 24)) return QGEMV_EUNSUPPORTED;
   const int64_t most = (int64_t)attend_occupancy(D, a->rt) * device_cu_count();
-  a->workgroups = (int)std::min(most, items * (a->joins ? granules : 1));
+  a->seq_items = a->c.H * groups;
+  a->workgroups = (int)(a->joins ? std::min(most, items * granules) : items);
   a->row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(item_rows, R), 1024 / items));
   // workspace: the plan, maxima and sums, parts
   const auto up = [](int64_t n) { return (n + 255) & ~(int64_t)255; };
-  const int64_t plan_bytes = up(4 * ((int64_t)a->B + 2)), parts = 2 * most * item_rows;
+  const int64_t plan_bytes = a->joins ? up(4 * ((int64_t)a->B + 2)) : 256, parts = a->joins ? 2 * most * item_rows : 0;
   uint8_t *p = static_cast<uint8_t *>(work);
   a->plan = reinterpret_cast<int32_t *>(p);
   a->ml = reinterpret_cast<float *>(p + plan_bytes);

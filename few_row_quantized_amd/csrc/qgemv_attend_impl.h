@@ -11,19 +11,22 @@
 //
 // * A wave takes tiles of 32 tokens, up to 64 query rows (RT tiles of 16) and
 //   all of D.  S^T = K Q^T: the A operand's lane (c, g) holds 8 consecutive d
-//   of token c, so keys go from memory to the matrix units with no exchange.
+//   of token c.  Loads in that shape take 64 bytes of 16 keys at a time, half
+//   a line each, so keys are loaded in whole rows instead and pass through a
+//   stage in LDS of the wave's own, of which it reads the operands.
 //   O^T += V^T P^T: P^T's operand lane holds 8 tokens of one query row, and
 //   the order of the tokens within the product is free, so the 4 + 4 scores
 //   that the first product leaves in a lane are that operand as they stand.
 //   V^T's lane holds 8 tokens of one d: each lane loads 8 consecutive d of
 //   those 8 tokens (whole rows of the cache per load instruction) and turns
-//   the block with byte permutes, 2 dwords an instruction.  Nothing passes
-//   through LDS, no wave waits for another.
+//   the block with byte permutes, 2 dwords an instruction.  No wave waits for
+//   another.
 // * Running maximum and sum per row, in base 2.  The maximum moves only when a
 //   score passes it by more than 8 (weights stay below 2^8): most tiles then
 //   leave the output's registers alone.
 // * Keys of the next tile are loaded as soon as this tile's product has read
-//   them, values alike: while a wave computes, a whole tile is on its way.
+//   the stage, values as soon as theirs has read them: while a wave computes,
+//   a whole tile is on its way.
 // * The work of a call is cut in equal ranges of granules (one tile for each
 //   wave that shares the tokens), whatever the lengths are: a workgroup walks
 //   its range over (sequence, head) items, joins its waves at the end of each
@@ -146,24 +149,36 @@ __device__ __forceinline__ SeqWork seq_work(Args &a, int b) {
 // consecutive d of each half of D (one half below D = 256).
 template <bool F8, int D>
 struct Tile {
-  static constexpr int KL = F8 ? D / 64 : D / 32;  // 16-byte loads of a key by one lane
+  static constexpr int ROW = D * (F8 ? 1 : 2);     // bytes of a key or value
+  static constexpr int KL = ROW / 32;              // loads of a wave for the tile's keys
+  static constexpr int KC = ROW / 16;              // 16-byte chunks of a key
+  static constexpr bool NT = ROW >= 128;           // whole lines are read at once
   static constexpr int VH = D == 256 ? 2 : 1;
   static constexpr int E = D / 16 / VH;
   static constexpr int VW = E * (F8 ? 1 : 2) / 4;  // dwords of one token's values in a half
 };
 
-template <int VW>
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// A load of the cache, past the caches where it reads whole lines (NT).
+template <bool NT, class T>
+__device__ __forceinline__ T load_cache(const uint8_t *p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const T *>(p));
+  return *reinterpret_cast<const T *>(p);
+}
+
+template <bool NT, int VW>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[VW]) {
   if constexpr (VW == 4) {
-    const u32x4_t v = *reinterpret_cast<const u32x4_t *>(p);
+    const u32x4_t v = load_cache<NT, u32x4_t>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = v[i];
   } else if constexpr (VW == 2) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    w[0] = v.x;
-    w[1] = v.y;
+    const u32x2_t v = load_cache<NT, u32x2_t>(p);
+    w[0] = v[0];
+    w[1] = v[1];
   } else {
-    w[0] = *reinterpret_cast<const uint32_t *>(p);
+    w[0] = load_cache<NT, uint32_t>(p);
   }
 }
 
@@ -187,18 +202,21 @@ __device__ __forceinline__ void turn(const uint32_t (&v)[8][VW], int word, u32x4
   }
 }
 
+// The sign bits of a dword's NaNs and infinities set, of its other values not:
+// an exponent of all ones (for E4M3 also all mantissa bits) carries into them.
+template <bool BF, bool F8>
+__device__ __forceinline__ uint32_t nonfinite_signs(uint32_t w) {
+  if constexpr (F8) return (w & 0x7F7F7F7Fu) + 0x01010101u;
+  return BF ? (w & 0x7F807F80u) + 0x00800080u : (w & 0x7C007C00u) + 0x04000400u;
+}
+template <bool F8>
+constexpr uint32_t kSigns = F8 ? 0x80808080u : 0x80008000u;
+
 // The bits of a dword of cached values that belong to NaNs and infinities.
 template <bool BF, bool F8>
 __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
-  uint32_t m = 0;
-  if constexpr (F8) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8) m |= (w >> i & 0x7Fu) == 0x7Fu ? 0xFFu << i : 0u;
-  } else {
-    constexpr uint32_t x = BF ? 0x7F80u : 0x7C00u;
-    m = ((w & x) == x ? 0xFFFFu : 0u) | ((w >> 16 & x) == x ? 0xFFFF0000u : 0u);
-  }
-  return m;
+  const uint32_t t = nonfinite_signs<BF, F8>(w) & kSigns<F8>;
+  return t | (t - (t >> (F8 ? 7 : 15)));
 }
 
 // Element i of a dword of cached values.
@@ -211,16 +229,26 @@ __device__ __forceinline__ float value_of(uint32_t w, int i) {
 
 // Workgroups of 256 threads that a CU holds, by registers: the output takes
 // D / 4 a tile of rows, a tile of keys and values D / 2 (16 bits).
-constexpr int attend_occupancy(int D, int rt) { return D * rt <= 384 ? 2 : 1; }
+constexpr int attend_occupancy(int D, int rt) { return D * rt <= 128 ? 3 : D * rt <= 384 ? 2 : 1; }
 
 // Queries stay in registers (D / 8 a tile of rows) while they take less than 32.
 constexpr bool queries_in_lds(int D, int rt) { return D * rt >= 256; }
 
 constexpr size_t kLdsHead = 2048 + 64;  // token offsets and the scan
-constexpr size_t attend_lds(int D, int rt, int chunks) {
+constexpr size_t attend_lds(bool f8, int D, int rt, int chunks) {
   const size_t q = queries_in_lds(D, rt) ? (size_t)chunks * rt * D * 32 : 0;
+  const size_t keys = (size_t)4 * 32 * D * (f8 ? 1 : 2);
   const size_t give = chunks == 4 ? 0 : (size_t)2 * rt * (512 + D * 64);
-  return kLdsHead + (q > give ? q : give);
+  return kLdsHead + (q + keys > give ? q + keys : give);
+}
+
+// Where the stage of a wave's keys holds chunk `chunk` of token `token`: lanes
+// of 16 tokens that read one chunk each find it in different banks.
+template <int ROW>
+__device__ __forceinline__ int stage_at(int token, int chunk) {
+  constexpr int PER = ROW >= 256 ? 1 : 256 / ROW;  // keys side by side in the 64 banks
+  constexpr int MASK = (ROW >= 256 ? 256 : ROW) / 16 - 1;
+  return token * (ROW / 16) + (chunk ^ (token / PER & MASK));
 }
 
 // The range of this workgroup: granules [cur, range1) of all items in order,
@@ -284,13 +312,13 @@ __device__ __forceinline__ bool attend_range(Args &a, int *scan, int *b, int *ba
 template <bool BF, bool F8, int D, int RT, int OCC>
 __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   using T = Tile<F8, D>;
-  constexpr int KL = T::KL, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
+  constexpr int KL = T::KL, KC = T::KC, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
   constexpr int CB = F8 ? 1 : 2;
   constexpr int QS = D / 32;  // steps of the first product
   constexpr bool QLDS = queries_in_lds(D, RT);
   extern __shared__ __align__(16) uint8_t lds[];
-  // [4 waves][2][32] token offsets, the scan, then the queries and, after the
-  // tokens, in the same place what waves hand over
+  // [4 waves][2][32] token offsets, the scan, then the queries and the waves'
+  // keys and, after the tokens, in the same place what waves hand over
   int64_t *const ring = reinterpret_cast<int64_t *>(lds);
   int *const scan = reinterpret_cast<int *>(lds + 2048);
   u32x4_t *const queries = reinterpret_cast<u32x4_t *>(lds + kLdsHead);
@@ -304,23 +332,37 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   const int chunks = ap->chunks;
   const int tw_n = 4 / chunks, chunk = wave & (chunks - 1), tw = wave / chunks;
 
-  int b, base, cur, range1;
-  if (!attend_range(*ap, scan, &b, &base, &cur, &range1)) return;
+  // Items that no two workgroups share have a workgroup each; the others are
+  // walked in equal ranges.
+  const bool joins = ap->joins;
+  int b, base = 0, cur = 0, range1 = 1;
+  if (joins) {
+    if (!attend_range(*ap, scan, &b, &base, &cur, &range1)) return;
+  } else {
+    b = blockIdx.x / ap->seq_items;
+  }
 
   int64_t *const my_ring = ring + wave * 64;
+  u32x4_t *const stage = queries + (QLDS ? chunks * RT * QS * 64 : 0) + wave * (32 * T::KC);
 
   while (cur < range1) {
     ap = reload(ap);
     const SeqWork w = seq_work(*ap, b);
-    const int seq_granules = w.items * w.granules;
-    if (cur >= base + seq_granules) {  // past this sequence (or it has no rows)
-      base += seq_granules;
-      ++b;
-      continue;
+    const int seq_granules = w.items * w.granules, groups = w.items / ap->c.H;
+    int item, first = 0;
+    if (joins) {
+      if (cur >= base + seq_granules) {  // past this sequence (or it has no rows)
+        base += seq_granules;
+        ++b;
+        continue;
+      }
+      item = (cur - base) / w.granules;
+      first = (cur - base) - item * w.granules;
+    } else {
+      item = blockIdx.x - b * ap->seq_items;
+      if (item >= w.items) return;
     }
-    const int item = (cur - base) / w.granules, first = (cur - base) - item * w.granules;
     const int n_granules = min(w.granules - first, range1 - cur);
-    const int groups = w.items / ap->c.H;
     const int h = item / groups, group = item - h * groups;
     cur += n_granules;
 
@@ -385,14 +427,18 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     int t = first * tw_n * ap->span + tw;
 
     auto tile_base = [&](int tile) { return (tile < w.sink_tiles ? tile : tile - w.sink_tiles + w.low_tile) * 32; };
+    // No load of the loop lies in a branch: with one that may not have been
+    // issued the compiler cannot count what is in flight and waits for all.
+    // Past the last tile, ids are those of the last token, and keys and values
+    // the first slot's, a row that stays in the caches.
     auto load_id = [&](int tile) -> int {
-      const int token = tile_base(tile) + (lane & 31);
-      return tile < t_end && token < w.end ? table[__umulhi(magic, 2 * token) >> shift] : -1;
+      const int token = min(tile_base(tile) + (lane & 31), w.end - 1);
+      return table[__umulhi(magic, 2 * token) >> shift];
     };
     // offsets of a tile's tokens into the ring; bit i: token i is there
     auto put = [&](int tile, int id, int slot) -> uint32_t {
       const int token = tile_base(tile) + (lane & 31);
-      const bool ok = (uint32_t)id < (uint32_t)pages;
+      const bool ok = ((uint32_t)id < (uint32_t)pages) & (tile < t_end) & (token < w.end);
       const int in_page = token - (int)(__umulhi(magic, 2 * token) >> shift) * page;
       const int64_t at = ok ? id * stride_page + in_page * stride_slot : 0;
       if (lane < 32) my_ring[slot * 32 + lane] = at;
@@ -405,14 +451,13 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       return (present != 0xFFFFFFFFu) | (tb + 31 > w.pos0) |
              ((tb <= w.pos0 + w.rows - 1 - window) & (tb + 31 >= sinks));
     };
-    u32x4_t kt[2][KL];
+    u32x4_t kt[KL];
     uint32_t vt[VH][8][VW];
     auto load_k = [&](int slot) {
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
-        const uint8_t *p = kbase + my_ring[slot * 32 + tt * 16 + c] + g * 16;
-#pragma unroll
-        for (int s = 0; s < KL; ++s) kt[tt][s] = *reinterpret_cast<const u32x4_t *>(p + s * 64);
+      for (int s = 0; s < KL; ++s) {
+        const int token = (s * 64 + lane) / KC, chunk = lane % KC;
+        kt[s] = load_cache<T::NT, u32x4_t>(kbase + my_ring[slot * 32 + token] + chunk * 16);
       }
     };
     auto load_v = [&](int slot) {
@@ -420,7 +465,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       for (int j = 0; j < 8; ++j) {
         const uint8_t *p = vbase + my_ring[slot * 32 + (j >> 2) * 16 + g * 4 + (j & 3)] + c * (E * CB);
 #pragma unroll
-        for (int x = 0; x < VH; ++x) load_words<VW>(p + x * (128 * CB), vt[x][j]);
+        for (int x = 0; x < VH; ++x) load_words<T::NT, VW>(p + x * (128 * CB), vt[x][j]);
       }
     };
 
@@ -435,9 +480,15 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       load_v(0);
     }
     for (; t < t_end; t += tw_n) {
-      const bool more = t + tw_n < t_end;
       there_next = put(t + tw_n, id, slot ^ 1);
       id = load_id(t + 2 * tw_n);
+
+      // ---- keys to the stage
+      int at = lane;
+      asm volatile("" : "+v"(at));  // places computed anew for each tile, not kept in registers
+#pragma unroll
+      for (int s = 0; s < KL; ++s) stage[stage_at<T::ROW>((s * 64 + at) / KC, at % KC)] = kt[s];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
       // ---- scores of 32 tokens: lane (c, g) has row c, tokens tt * 16 + 4 g + i
       f32x4_t s[RT][2];
@@ -448,15 +499,16 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 #pragma unroll
       for (int st = 0; st < QS; ++st) {
         u32x4_t ka[2];
+        const int chunk = (F8 ? st >> 1 : st) * 4 + (at >> 4);
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
+          const u32x4_t x = stage[stage_at<T::ROW>(tt * 16 + (at & 15), chunk)];
           if constexpr (F8) {
-            const u32x4_t x = kt[tt][st >> 1];
             const uint32_t x0 = x[2 * (st & 1)], x1 = x[2 * (st & 1) + 1];
             ka[tt] = u32x4_t{e4m3_pair<BF, false>(x0), e4m3_pair<BF, true>(x0), e4m3_pair<BF, false>(x1),
                              e4m3_pair<BF, true>(x1)};
           } else {
-            ka[tt] = kt[tt][st];
+            ka[tt] = x;
           }
         }
 #pragma unroll
@@ -471,7 +523,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (more) load_k(slot ^ 1);
+      load_k(slot ^ 1);
       __builtin_amdgcn_sched_barrier(0);
 
       const int tb = tile_base(t);
@@ -555,17 +607,20 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 #pragma unroll
             for (int y = 0; y < VW; ++y) {
               vt[x][j][y] &= ok;
-              odd |= nonfinite<BF, F8>(vt[x][j][y]);
+              odd |= nonfinite_signs<BF, F8>(vt[x][j][y]);
             }
         }
-        if (__any(odd != 0)) {
+        if (__any((odd & kSigns<F8>) != 0)) {
           strays = true;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int x = 0; x < VH; ++x)
 #pragma unroll
-              for (int y = 0; y < VW; ++y) vt[x][j][y] &= ~nonfinite<BF, F8>(vt[x][j][y]);
+              for (int y = 0; y < VW; ++y) {
+                asm volatile("" : "+v"(vt[x][j][y]));  // nothing kept from the test for this rare part
+                vt[x][j][y] &= ~nonfinite<BF, F8>(vt[x][j][y]);
+              }
         }
       }
       constexpr int PW = F8 ? 4 : 2;  // operands of one dword column
@@ -582,7 +637,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
               acc[r][x * E + y * PW + z] = mfma_16x16x32<BF>(o[z], pf[r], acc[r][x * E + y * PW + z]);
         }
       __builtin_amdgcn_sched_barrier(0);
-      if (more) load_v(slot ^ 1);
+      load_v(slot ^ 1);
       __builtin_amdgcn_sched_barrier(0);
       slot ^= 1;
       there = there_next;
@@ -613,7 +668,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t v[VW];
-              load_words<VW>(p + (x * 128 + k * E) * CB, v);
+              load_words<false, VW>(p + (x * 128 + k * E) * CB, v);
 #pragma unroll
               for (int e = 0; e < E; ++e) {
                 constexpr int PER = 4 / CB;
@@ -631,7 +686,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 
     // ---- the waves that shared the tokens: the upper half gives, the lower takes
     ap = reload(ap);
-    if (QLDS && tw_n > 1) __syncthreads();  // the queries have been read
+    if (tw_n > 1) __syncthreads();  // the queries and keys have been read
 #pragma unroll
     for (int r = 0; r < RT; ++r) l[r] = row_sum(l[r]);
     for (int half = tw_n >> 1; half; half >>= 1) {
@@ -798,7 +853,7 @@ template <bool BF, bool F8, int D, int RT>
 int launch_attend_rt(const AttendArgs &a, hipStream_t stream) {
   constexpr int OCC = attend_occupancy(D, RT);
   const auto kern = attend_kernel<BF, F8, D, RT, OCC>;
-  const size_t bytes = attend_lds(D, RT, a.chunks);
+  const size_t bytes = attend_lds(F8, D, RT, a.chunks);
   if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
   hipLaunchKernelGGL(kern, dim3(a.workgroups), dim3(256), bytes, stream, a);
   if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
