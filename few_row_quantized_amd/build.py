@@ -1,4 +1,5 @@
-"""Build libqgemv.so in-tree with hipcc for gfx950.
+"""Build libqgemv.so in-tree with hipcc for gfx950, and the Python module
+_qgemv_torch.so (its calls on torch tensors) with the host compiler.
 
     python -m few_row_quantized_amd.build [-v]
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqgemv.so")
+MODULE = os.path.join(PKG, "_qgemv_torch.so")
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
@@ -60,11 +63,33 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _module(verbose: bool) -> None:
+    """qgemv_torch.cpp: host code alone, against torch's headers."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    tmp = MODULE + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-I", sysconfig.get_paths()["include"], *(f for i in include for f in ("-isystem", i)),
+           os.path.join(CSRC, "qgemv_torch.cpp"), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    t0 = time.time()
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{proc.stderr}")
+    os.replace(tmp, MODULE)
+    if verbose:
+        print(f"  qgemv_torch.cpp: {time.time() - t0:.1f}s\n{proc.stderr}", end="", flush=True)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     t0 = time.time()
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        module = ex.submit(_module, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        module.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     proc = subprocess.run(cmd, capture_output=True, text=True)

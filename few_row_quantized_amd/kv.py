@@ -3,9 +3,9 @@ appending the new rows' keys and values to a paged cache, attention of those
 rows over it, and acceptance of the drafted tokens.
 
 Argument marshalling only, as in :mod:`few_row_quantized_amd.qgemv`, which
-offers these names: types, shapes and strides are checked here (ValueError)
-and again by the library (:class:`QgemvError`); the contracts stand in
-include/qgemv.h.
+offers these names: types, shapes and strides are checked (ValueError) by the
+compiled module _qgemv_torch, and again by the library (:class:`QgemvError`);
+the contracts stand in include/qgemv.h.
 
 Sequence b owns rows start[b] .. start[b+1]-1 of every [T, ...] tensor (start
 int32 [B+1]) and has len[b] tokens, those rows included (len int32 [B]).  Both
@@ -14,59 +14,38 @@ stay on the device: no call reads them back.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
 
 import torch
 
 from . import qgemv as _q
 
-_TYPES = {torch.float32: _q.F32, torch.bfloat16: _q.BF16, torch.float16: _q.F16,
-          torch.float8_e4m3fn: _q.E4M3}
+_TYPES = {torch.bfloat16: _q.BF16, torch.float16: _q.F16, torch.float8_e4m3fn: _q.E4M3}
+
+_module = None
 
 
-def _strides(name: str, t, dim: int):
-    """Row and head strides of a [T, heads, dim] operand, in elements.  A
-    dimension of one element has no stride of its own: it gets a packed one."""
-    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [T, heads, {dim}] with a contiguous last dimension")
-    T, heads, _ = t.shape
-    head = t.stride(1) if heads > 1 else dim
-    return t.stride(0) if T > 1 else heads * head, head
+def _calls():
+    """The compiled calls, bound to the library on first use."""
+    global _module
+    if _module is None:
+        L = _q.lib()
+        try:
+            from . import _qgemv_torch as m
+        except ImportError as e:
+            raise RuntimeError(f"_qgemv_torch is not built ({e}); run `python -m few_row_quantized_amd.build`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.qgemv_kv_append, L.qgemv_kv_attend_workspace, L.qgemv_kv_attend, L.qgemv_verify_drafts_workspace,
+            L.qgemv_verify_drafts)), torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None)
+        _module = m
+    return _module
 
 
-def _index(name: str, t, n: int, device):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {device}")
-    return t.data_ptr()
-
-
-def _on(device, stream) -> Optional[int]:
-    """The raw stream of a call on `device`, which has to be the current one."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on the GPU, not on {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is {torch.cuda.current_device()}")
-    return _q._stream(stream)
-
-
-def _new(shape, dtype, device, stream, fill=None):
-    """A tensor for a call on `stream`, allocated there, so that its memory is
-    not still in use by another stream."""
-    if stream is not None and device.type == "cuda":
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        with torch.cuda.stream(stream):
-            return _new(shape, dtype, device, None, fill)
-    t = torch.empty(shape, dtype=dtype, device=device)
-    return t if fill is None else t.fill_(fill)
-
-
-def _work(workspace, need: int, device, stream, zeroed: bool):
-    if workspace is None:
-        return _new((need,), torch.uint8, device, stream, 0 if zeroed else None)
-    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
+def _allocating(stream, device):
+    """`stream` as the current one: what a call allocates for itself comes from
+    the stream it runs on, so that its memory is not still in use by another."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
 
 
 class KvCache:
@@ -115,25 +94,15 @@ class KvCache:
                                _q._ptr(v_scale), *strides, P, page, table.shape[1], table.shape[0], H, D,
                                _TYPES[k.dtype])
         self._ref = ctypes.byref(self._c)
+        self._address = ctypes.addressof(self._c)
 
 
 def append(cache: KvCache, new_k, new_v, start, len, stream=None) -> None:
     """Write the rows' keys and values, new_k and new_v [T, heads, dim] of
     float32, bfloat16 or float16, to their sequences' slots of the cache."""
-    dev, D = cache.device, cache.dim
-    if new_k.dtype != new_v.dtype or new_k.dtype not in _TYPES or new_k.dtype == torch.float8_e4m3fn:
-        raise ValueError(f"new_k and new_v must be float32, bfloat16 or float16, got {new_k.dtype}, {new_v.dtype}")
-    if new_k.shape != new_v.shape or new_k.shape[1] != cache.heads or new_k.device != dev or new_v.device != dev:
-        raise ValueError(f"new_k and new_v must be [T, {cache.heads}, {D}] on {dev}")
-    k_row, k_head = _strides("new_k", new_k, D)
-    v_row, v_head = _strides("new_v", new_v, D)
-    s, n = _index("start", start, cache.batch + 1, dev), _index("len", len, cache.batch, dev)
-    T = new_k.shape[0]
-    if T == 0:
-        return
-    _q._check(_q.lib().qgemv_kv_append(cache._ref, new_k.data_ptr(), k_row, k_head, new_v.data_ptr(),
-                                       v_row, v_head, _TYPES[new_k.dtype], s, n, T, _on(dev, stream)),
-              "qgemv_kv_append")
+    status = _calls().append(cache._address, cache.k, new_k, new_v, start, len, stream)
+    if status:
+        _q._check(status, "qgemv_kv_append")
 
 
 def attend_workspace(cache: KvCache, M: int, q_heads: int, T: int):
@@ -151,38 +120,13 @@ def attend(cache: KvCache, q, start, len, M: int, window: int = 0, sinks: int = 
     first `sinks`.  M: the largest number of rows of a sequence (1..16).
     scale: dim ** -0.5 unless given.  Returns out [T, q_heads, dim]; lse, a
     float32 [T, q_heads] tensor, takes the logarithm of each row's sum."""
-    dev, D = cache.device, cache.dim
-    if q.dtype not in (torch.bfloat16, torch.float16) or cache.dtype not in (q.dtype, torch.float8_e4m3fn):
-        raise ValueError(f"q of {q.dtype} over a cache of {cache.dtype} is not supported")
-    if q.device != dev:
-        raise ValueError(f"q must be on {dev}")
-    q_row, q_head = _strides("q", q, D)
-    T, heads, _ = q.shape
-    s, n = _index("start", start, cache.batch + 1, dev), _index("len", len, cache.batch, dev)
-    if out is None:
-        out = _new((T, heads, D), q.dtype, dev, stream)
-        o_row, o_head = heads * D, D
-    else:
-        if out.dtype != q.dtype or out.shape != q.shape or out.device != dev:
-            raise ValueError("out must have q's type, shape and device")
-        o_row, o_head = _strides("out", out, D)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()
-                            or lse.device != dev):
-        raise ValueError(f"lse must be a contiguous float32 [{T}, {heads}] tensor on {dev}")
-    L = _q.lib()
-    if workspace is None:
-        need = _q._check(L.qgemv_kv_attend_workspace(cache._ref, M, heads, T), "qgemv_kv_attend_workspace")
-        workspace = _work(None, need, dev, stream, False)
-    else:
-        _work(workspace, 0, dev, stream, False)
-    if T == 0:
-        return out
-    _q._check(L.qgemv_kv_attend(cache._ref, q.data_ptr(), q_row, q_head, out.data_ptr(), o_row, o_head,
-                                _TYPES[q.dtype], None if lse is None else lse.data_ptr(), s, n, T, M, heads,
-                                window, sinks, D ** -0.5 if scale is None else scale,
-                                workspace.data_ptr(), workspace.numel(), _on(dev, stream)),
-              "qgemv_kv_attend")
-    return out
+    if stream is not None and (out is None or workspace is None) and cache.k.is_cuda:
+        with _allocating(stream, cache.device):
+            return attend(cache, q, start, len, M, window, sinks, scale, out, lse, workspace)
+    r = _calls().attend(cache._address, cache.k, q, start, len, M, window, sinks, scale, out, lse, workspace, stream)
+    if type(r) is int:
+        _q._check(r, "qgemv_kv_attend")
+    return r
 
 
 def verify_workspace(p, B: int):
@@ -198,34 +142,10 @@ def verify(p, q, tokens, u, start, M: int, workspace=None, stream=None):
     [T] the token fed at each row, u float32 [T] uniform numbers.  Returns
     (out int32 [T]: each sequence's accepted drafts, its drawn token, then -1;
     count int32 [B]: how many of them are tokens)."""
-    dev = p.device
-    if p.dtype not in _TYPES or p.dtype == torch.float8_e4m3fn or p.dim() != 2 or p.shape[1] < 1:
-        raise ValueError("p must be a float32, bfloat16 or float16 [T, V] tensor")
-    T, V = p.shape
-    for name, t in (("p", p), ("q", q)):
-        if t is not None and (t.shape != p.shape or t.dtype != p.dtype or t.device != dev
-                              or (V > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{name} must be a {p.dtype} [{T}, {V}] tensor on {dev} with contiguous rows")
-    B = start.shape[0] - 1
-    if B < 1:
-        raise ValueError("start must have at least two entries")
-    s = _index("start", start, B + 1, dev)
-    k = _index("tokens", tokens, T, dev)
-    if u.dtype != torch.float32 or u.shape != (T,) or not u.is_contiguous() or u.device != dev:
-        raise ValueError(f"u must be a contiguous float32 [{T}] tensor on {dev}")
-    out = _new((T,), torch.int32, dev, stream)
-    count = _new((B,), torch.int32, dev, stream)
-    if T == 0:
-        return out, count.zero_()
-    L = _q.lib()
-    if workspace is None:
-        need = _q._check(L.qgemv_verify_drafts_workspace(B, V), "qgemv_verify_drafts_workspace")
-        workspace = _work(None, need, dev, stream, True)
-    else:
-        _work(workspace, 0, dev, stream, True)
-    _q._check(L.qgemv_verify_drafts(p.data_ptr(), p.stride(0) if T > 1 else V, None if q is None else q.data_ptr(),
-                                    0 if q is None else q.stride(0) if T > 1 else V, _TYPES[p.dtype], k,
-                                    u.data_ptr(), s, out.data_ptr(), count.data_ptr(), B, T, M, V,
-                                    workspace.data_ptr(), workspace.numel(), _on(dev, stream)),
-              "qgemv_verify_drafts")
-    return out, count
+    if stream is not None and p.is_cuda:
+        with _allocating(stream, p.device):
+            return verify(p, q, tokens, u, start, M, workspace)
+    r = _calls().verify(p, q, tokens, u, start, M, workspace, stream)
+    if type(r) is int:
+        _q._check(r, "qgemv_verify_drafts")
+    return r
