@@ -13,15 +13,15 @@ int launch_attend_f16_e4m3(const AttendArgs &a, hipStream_t stream);
 
 int64_t plan_attend(AttendArgs *a, void *work) {
   const int D = a->c.D, R = a->M * a->G;
-  // Rows of an item over waves: up to 64 (32 at D = 256, whose output takes
-  // twice the registers) in one wave, all four waves sharing the tokens;
-  // more are split over 2 or 4 waves that read the same tokens.
+  // Up to 64 rows of an item (32 at D = 256, whose output takes twice the
+  // registers) are one wave's, and the four waves of a workgroup share the
+  // tokens.  More are split over the four waves, which share the loads.
   const int rt_max = D == 256 ? 2 : 4;
-  a->chunks = 1;
-  while (a->chunks < 4 && a->chunks * rt_max * 16 < R) a->chunks *= 2;
-  const int groups = (R + a->chunks * rt_max * 16 - 1) / (a->chunks * rt_max * 16);
-  a->rt = (R + groups * a->chunks * 16 - 1) / (groups * a->chunks * 16);
-  const int item_rows = a->chunks * a->rt * 16, tw = 4 / a->chunks;
+  a->shared = R > rt_max * 16;
+  const int waves = a->shared ? 4 : 1, tw = 4 / waves;
+  const int groups = (R + waves * rt_max * 16 - 1) / (waves * rt_max * 16);
+  a->rt = (R + groups * waves * 16 - 1) / (groups * waves * 16);
+  const int item_rows = waves * a->rt * 16;
   // the longest item that the table and the window allow, in tiles
   int64_t tiles = ((int64_t)a->c.page * a->c.width + 31) / 32;
   if (a->window)

@@ -137,10 +137,10 @@ __device__ __forceinline__ SeqWork seq_work(Args &a, int b) {
   w.low_tile = low >> 5;
   w.sink_tiles = a.window ? min(min((a.sinks >> 5) + ((a.sinks & 31) != 0), w.low_tile), all) : 0;
   w.tiles = w.sink_tiles + max(all - w.low_tile, 0);
-  const int tw = 4 / a.chunks;
+  const int tw = a.shared ? 1 : 4;
   // an item without tokens still writes its rows
   w.granules = max((w.tiles + tw * a.span - 1) / (tw * a.span), 1);
-  const int item_rows = a.chunks * a.rt * 16;
+  const int item_rows = (a.shared ? 4 : 1) * a.rt * 16;
   w.items = w.rows > 0 ? a.c.H * ((w.rows * a.G + item_rows - 1) / item_rows) : 0;
   return w;
 }
@@ -153,6 +153,8 @@ struct Tile {
   static constexpr int KL = ROW / 32;              // loads of a wave for the tile's keys
   static constexpr int KC = ROW / 16;              // 16-byte chunks of a key
   static constexpr bool NT = ROW >= 128;           // whole lines are read at once
+  // a wave's 8 tokens of a shared tile: bytes of a load, loads of a row, of a wave
+  static constexpr int SB = ROW >= 128 ? 16 : 8, SC = ROW / SB, SL = SC / 8;
   static constexpr int VH = D == 256 ? 2 : 1;
   static constexpr int E = D / 16 / VH;
   static constexpr int VW = E * (F8 ? 1 : 2) / 4;  // dwords of one token's values in a half
@@ -227,19 +229,20 @@ __device__ __forceinline__ float value_of(uint32_t w, int i) {
   return BF ? bf16_bits_to_float(h) : half_bits_to_float(h);
 }
 
-// Workgroups of 256 threads that a CU holds, by registers: the output takes
-// D / 4 a tile of rows, a tile of keys and values D / 2 (16 bits).
+// Workgroups of 256 threads that a CU holds, by registers and LDS: the output
+// takes D / 4 registers a tile of rows, keys and values of a wave D / 2 (16 bits).
 constexpr int attend_occupancy(int D, int rt) { return D * rt <= 128 ? 3 : D * rt <= 384 ? 2 : 1; }
 
-// Queries stay in registers (D / 8 a tile of rows) while they take less than 32.
-constexpr bool queries_in_lds(int D, int rt) { return D * rt >= 256; }
+// Queries stay in registers (D / 8 a tile of rows) while they take less than
+// 32, or 64 where keys and values do not wait in registers.
+constexpr bool queries_in_lds(int D, int rt, bool sh) { return D * rt >= (sh ? 512 : 256); }
 
 constexpr size_t kLdsHead = 2048 + 64;  // token offsets and the scan
-constexpr size_t attend_lds(bool f8, int D, int rt, int chunks) {
-  const size_t q = queries_in_lds(D, rt) ? (size_t)chunks * rt * D * 32 : 0;
-  const size_t keys = (size_t)4 * 32 * D * (f8 ? 1 : 2);
-  const size_t give = chunks == 4 ? 0 : (size_t)2 * rt * (512 + D * 64);
-  return kLdsHead + (q + keys > give ? q + keys : give);
+constexpr size_t attend_lds(bool f8, int D, int rt, bool sh) {
+  const size_t q = queries_in_lds(D, rt, sh) ? (size_t)(sh ? 4 : 1) * rt * D * 32 : 0;
+  const size_t stage = (size_t)4 * 32 * D * (f8 ? 1 : 2);  // each wave's keys, or keys and values twice
+  const size_t give = sh ? 0 : (size_t)2 * rt * (512 + D * 64);
+  return kLdsHead + (q + stage > give ? q + stage : give);
 }
 
 // Where the stage of a wave's keys holds chunk `chunk` of token `token`: lanes
@@ -309,13 +312,14 @@ __device__ __forceinline__ bool attend_range(Args &a, int *scan, int *b, int *ba
   return true;
 }
 
-template <bool BF, bool F8, int D, int RT, int OCC>
+template <bool BF, bool F8, int D, int RT, bool SH, int OCC>
 __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   using T = Tile<F8, D>;
   constexpr int KL = T::KL, KC = T::KC, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
   constexpr int CB = F8 ? 1 : 2;
   constexpr int QS = D / 32;  // steps of the first product
-  constexpr bool QLDS = queries_in_lds(D, RT);
+  constexpr bool QLDS = queries_in_lds(D, RT, SH);
+  constexpr int CHUNKS = SH ? 4 : 1, TW = 4 / CHUNKS;  // waves that split the rows, and the tokens
   extern __shared__ __align__(16) uint8_t lds[];
   // [4 waves][2][32] token offsets, the scan, then the queries and the waves'
   // keys and, after the tokens, in the same place what waves hand over
@@ -329,8 +333,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int chunks = ap->chunks;
-  const int tw_n = 4 / chunks, chunk = wave & (chunks - 1), tw = wave / chunks;
+  const int chunk = SH ? wave : 0, tw = SH ? 0 : wave;
 
   // Items that no two workgroups share have a workgroup each; the others are
   // walked in equal ranges.
@@ -343,7 +346,8 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   }
 
   int64_t *const my_ring = ring + wave * 64;
-  u32x4_t *const stage = queries + (QLDS ? chunks * RT * QS * 64 : 0) + wave * (32 * T::KC);
+  int half = 0;  // of the shared stage: what the waves may still read, and what they write
+  u32x4_t *const stage = queries + (QLDS ? CHUNKS * RT * QS * 64 : 0) + (SH ? 0 : wave * (32 * KC));
 
   while (cur < range1) {
     ap = reload(ap);
@@ -367,7 +371,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     cur += n_granules;
 
     const int R = w.rows * ap->G;
-    const int row_first = (group * chunks + chunk) * RT * 16;
+    const int row_first = (group * CHUNKS + chunk) * RT * 16;
 
     // ---- the query rows, one a lane and 16-row tile; rows past R see nothing
     int pos[RT];
@@ -393,10 +397,10 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       }
       if constexpr (QLDS) {
         // [wave's rows][tile][step][lane], every wave a quarter of the steps
-        __syncthreads();  // the last item's hand-over has been read
-        const int first_row = group * chunks * RT * 16;
+        __syncthreads();  // the last item's queries, or hand-over, have been read
+        const int first_row = group * CHUNKS * RT * 16;
 #pragma unroll 4
-        for (int u = wave; u < chunks * RT * QS; u += 4)
+        for (int u = wave; u < CHUNKS * RT * QS; u += 4)
           queries[u * 64 + lane] = query(first_row + u / QS * 16 + c, u % QS);
         __syncthreads();
       }
@@ -423,8 +427,8 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     const int window = ap->window ? ap->window : 1 << 30;  // none: as wide as any position
     const int sinks = ap->sinks;
     const float sc = ap->scale * (ap->c.k_scale ? ap->c.k_scale[h] : 1.0f) * kLog2e;
-    const int t_end = min((first + n_granules) * tw_n * ap->span, w.tiles);
-    int t = first * tw_n * ap->span + tw;
+    const int t_end = min((first + n_granules) * TW * ap->span, w.tiles);
+    int t = first * TW * ap->span + tw;
 
     auto tile_base = [&](int tile) { return (tile < w.sink_tiles ? tile : tile - w.sink_tiles + w.low_tile) * 32; };
     // No load of the loop lies in a branch: with one that may not have been
@@ -451,9 +455,26 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       return (present != 0xFFFFFFFFu) | (tb + 31 > w.pos0) |
              ((tb <= w.pos0 + w.rows - 1 - window) & (tb + 31 >= sinks));
     };
-    u32x4_t kt[KL];
+    // this wave's share of a tile's keys and values: all of them, or 8 tokens
+    u32x4_t kt[SH ? T::SL : KL];
+    u32x4_t vs[SH ? T::SL : 1];
     uint32_t vt[VH][8][VW];
+    auto load_share = [&](const uint8_t *from, int slot, u32x4_t *to) {
+#pragma unroll
+      for (int s = 0; s < T::SL; ++s) {
+        const int at = s * 64 + lane;
+        const uint8_t *p = from + my_ring[slot * 32 + wave * 8 + at / T::SC] + at % T::SC * T::SB;
+        if constexpr (T::SB == 16) {
+          to[s] = load_cache<T::NT, u32x4_t>(p);
+        } else {
+          const u32x2_t x = load_cache<T::NT, u32x2_t>(p);
+          to[s][0] = x[0];
+          to[s][1] = x[1];
+        }
+      }
+    };
     auto load_k = [&](int slot) {
+      if constexpr (SH) return load_share(kbase, slot, kt);
 #pragma unroll
       for (int s = 0; s < KL; ++s) {
         const int token = (s * 64 + lane) / KC, chunk = lane % KC;
@@ -461,6 +482,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       }
     };
     auto load_v = [&](int slot) {
+      if constexpr (SH) return load_share(vbase, slot, vs);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint8_t *p = vbase + my_ring[slot * 32 + (j >> 2) * 16 + g * 4 + (j & 3)] + c * (E * CB);
@@ -475,20 +497,43 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     int id = -1;
     if (t < t_end) {
       there = put(t, load_id(t), 0);
-      id = load_id(t + tw_n);
+      id = load_id(t + TW);
       load_k(0);
       load_v(0);
     }
-    for (; t < t_end; t += tw_n) {
-      there_next = put(t + tw_n, id, slot ^ 1);
-      id = load_id(t + 2 * tw_n);
+    for (; t < t_end; t += TW) {
+      there_next = put(t + TW, id, slot ^ 1);
+      id = load_id(t + 2 * TW);
 
       // ---- keys to the stage
       int at = lane;
       asm volatile("" : "+v"(at));  // places computed anew for each tile, not kept in registers
+      u32x4_t *const keys = stage + (SH ? half * (64 * KC) : 0);
+      const uint8_t *const values = reinterpret_cast<const uint8_t *>(keys + 32 * KC);
+      if constexpr (SH) {
 #pragma unroll
-      for (int s = 0; s < KL; ++s) stage[stage_at<T::ROW>((s * 64 + at) / KC, at % KC)] = kt[s];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int s = 0; s < T::SL; ++s) {
+          const int token = wave * 8 + (s * 64 + at) / T::SC, part = (s * 64 + at) % T::SC;
+          if constexpr (T::SB == 16) {
+            keys[stage_at<T::ROW>(token, part)] = kt[s];
+            keys[32 * KC + token * KC + part] = vs[s];
+          } else {
+            u32x2_t *const k2 = reinterpret_cast<u32x2_t *>(keys), x = {kt[s][0], kt[s][1]}, y = {vs[s][0], vs[s][1]};
+            k2[stage_at<T::ROW>(token, part >> 1) * 2 + (part & 1)] = x;
+            k2[64 * KC + token * KC * 2 + part] = y;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(slot ^ 1);
+        load_v(slot ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+        half ^= 1;
+      } else {
+#pragma unroll
+        for (int s = 0; s < KL; ++s) keys[stage_at<T::ROW>((s * 64 + at) / KC, at % KC)] = kt[s];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
 
       // ---- scores of 32 tokens: lane (c, g) has row c, tokens tt * 16 + 4 g + i
       f32x4_t s[RT][2];
@@ -502,7 +547,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
         const int chunk = (F8 ? st >> 1 : st) * 4 + (at >> 4);
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
-          const u32x4_t x = stage[stage_at<T::ROW>(tt * 16 + (at & 15), chunk)];
+          const u32x4_t x = keys[stage_at<T::ROW>(tt * 16 + (at & 15), chunk)];
           if constexpr (F8) {
             const uint32_t x0 = x[2 * (st & 1)], x1 = x[2 * (st & 1) + 1];
             ka[tt] = u32x4_t{e4m3_pair<BF, false>(x0), e4m3_pair<BF, true>(x0), e4m3_pair<BF, false>(x1),
@@ -522,9 +567,11 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
           for (int tt = 0; tt < 2; ++tt) s[r][tt] = mfma_16x16x32<BF>(ka[tt], qa, s[r][tt]);
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
-      load_k(slot ^ 1);
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (!SH) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(slot ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 
       const int tb = tile_base(t);
       const bool edge = is_edge(tb, there);
@@ -593,6 +640,14 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       }
 
       // ---- values
+      if constexpr (SH) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint8_t *p = values + ((j >> 2) * 16 + (at >> 4) * 4 + (j & 3)) * T::ROW + (at & 15) * (E * CB);
+#pragma unroll
+          for (int x = 0; x < VH; ++x) load_words<false, VW>(p + x * (128 * CB), vt[x][j]);
+        }
+      }
       if (edge) {
         // a token that is not there, or that only some rows see, may hold
         // anything, and 0 times a NaN or an infinity is not 0: these are taken
@@ -636,9 +691,11 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
             for (int r = 0; r < RT; ++r)
               acc[r][x * E + y * PW + z] = mfma_16x16x32<BF>(o[z], pf[r], acc[r][x * E + y * PW + z]);
         }
-      __builtin_amdgcn_sched_barrier(0);
-      load_v(slot ^ 1);
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (!SH) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(slot ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       slot ^= 1;
       there = there_next;
     }
@@ -648,7 +705,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       // tokens: lane (c, g) holds row c and, of each half of D, the 4 E
       // consecutive d from 4 E g on.
 #pragma unroll 1
-      for (int t2 = first * tw_n * ap->span + tw; t2 < t_end; t2 += tw_n) {
+      for (int t2 = first * TW * ap->span + tw; t2 < t_end; t2 += TW) {
         const uint32_t present = put(t2, load_id(t2), 0);
         const int tb = tile_base(t2);
         if (!is_edge(tb, present)) continue;
@@ -686,12 +743,12 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 
     // ---- the waves that shared the tokens: the upper half gives, the lower takes
     ap = reload(ap);
-    if (tw_n > 1) __syncthreads();  // the queries and keys have been read
+    if constexpr (!SH) __syncthreads();  // the queries and keys have been read
 #pragma unroll
     for (int r = 0; r < RT; ++r) l[r] = row_sum(l[r]);
-    for (int half = tw_n >> 1; half; half >>= 1) {
-      const int seat = (tw - half) * chunks + chunk;  // of 2 at most
-      if (tw >= half && tw < 2 * half) {
+    for (int over = TW >> 1; over; over >>= 1) {
+      const int seat = tw - over;  // of 2 at most
+      if (tw >= over && tw < 2 * over) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           give_ml[((seat * RT + r) * 2 + 0) * 64 + lane] = m[r];
@@ -701,8 +758,8 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
         }
       }
       __syncthreads();
-      if (tw < half) {
-        const int from = tw * chunks + chunk;
+      if (tw < over) {
+        const int from = tw;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           const float m2 = give_ml[((from * RT + r) * 2 + 0) * 64 + lane];
@@ -753,7 +810,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
             ap->lse[(int64_t)(w.row0 + i) * (ap->c.H * G) + hq] =
                 l[r] == 0.0f ? kNegInf : (m[r] + __builtin_log2f(l[r])) * kLn2;
         } else {
-          const int64_t at = (part * chunks + chunk) * RT * 16 + r * 16 + c;
+          const int64_t at = (part * CHUNKS + chunk) * RT * 16 + r * 16 + c;
           float *o = ap->part + at * D;
 #pragma unroll
           for (int x = 0; x < VH; ++x)
@@ -780,7 +837,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 template <bool BF, int D>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   constexpr int TEAM = D / 4, TEAMS = 256 / TEAM;
-  const int item_rows = a.chunks * a.rt * 16;
+  const int item_rows = (a.shared ? 4 : 1) * a.rt * 16;
   const int groups_max = (a.M * a.G + item_rows - 1) / item_rows;
   const int b = blockIdx.x / (a.c.H * groups_max), hg = blockIdx.x - b * (a.c.H * groups_max);
   const SeqWork w = seq_work(a, b);
@@ -849,35 +906,35 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   }
 }
 
-template <bool BF, bool F8, int D, int RT>
+template <bool BF, bool F8, int D, int RT, bool SH>
 int launch_attend_rt(const AttendArgs &a, hipStream_t stream) {
   constexpr int OCC = attend_occupancy(D, RT);
-  const auto kern = attend_kernel<BF, F8, D, RT, OCC>;
-  const size_t bytes = attend_lds(F8, D, RT, a.chunks);
+  constexpr size_t bytes = attend_lds(F8, D, RT, SH);
+  const auto kern = attend_kernel<BF, F8, D, RT, SH, OCC>;
   if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
   hipLaunchKernelGGL(kern, dim3(a.workgroups), dim3(256), bytes, stream, a);
   if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
   if (!a.joins) return QGEMV_OK;
-  const int item_rows = a.chunks * a.rt * 16, groups = (a.M * a.G + item_rows - 1) / item_rows;
-  hipLaunchKernelGGL((join_kernel<BF, D>), dim3(a.B * a.c.H * groups, a.row_splits), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((join_kernel<BF, D>), dim3(a.B * a.seq_items, a.row_splits), dim3(256), 0, stream, a);
   return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
+}
+
+template <bool BF, bool F8, int D, bool SH>
+int launch_attend_d(const AttendArgs &a, hipStream_t stream) {
+  if constexpr (D < 256) {
+    if (a.rt == 3) return launch_attend_rt<BF, F8, D, 3, SH>(a, stream);
+    if (a.rt == 4) return launch_attend_rt<BF, F8, D, 4, SH>(a, stream);
+  }
+  return a.rt == 1 ? launch_attend_rt<BF, F8, D, 1, SH>(a, stream) : launch_attend_rt<BF, F8, D, 2, SH>(a, stream);
 }
 
 template <bool BF, bool F8>
 int launch_attend_t(const AttendArgs &a, hipStream_t stream) {
-  switch (a.c.D * 8 + a.rt) {
-    case 64 * 8 + 1: return launch_attend_rt<BF, F8, 64, 1>(a, stream);
-    case 64 * 8 + 2: return launch_attend_rt<BF, F8, 64, 2>(a, stream);
-    case 64 * 8 + 3: return launch_attend_rt<BF, F8, 64, 3>(a, stream);
-    case 64 * 8 + 4: return launch_attend_rt<BF, F8, 64, 4>(a, stream);
-    case 128 * 8 + 1: return launch_attend_rt<BF, F8, 128, 1>(a, stream);
-    case 128 * 8 + 2: return launch_attend_rt<BF, F8, 128, 2>(a, stream);
-    case 128 * 8 + 3: return launch_attend_rt<BF, F8, 128, 3>(a, stream);
-    case 128 * 8 + 4: return launch_attend_rt<BF, F8, 128, 4>(a, stream);
-    case 256 * 8 + 1: return launch_attend_rt<BF, F8, 256, 1>(a, stream);
-    case 256 * 8 + 2: return launch_attend_rt<BF, F8, 256, 2>(a, stream);
+  switch (a.c.D) {
+    case 64: return a.shared ? launch_attend_d<BF, F8, 64, true>(a, stream) : launch_attend_d<BF, F8, 64, false>(a, stream);
+    case 128: return a.shared ? launch_attend_d<BF, F8, 128, true>(a, stream) : launch_attend_d<BF, F8, 128, false>(a, stream);
   }
-  return QGEMV_EUNSUPPORTED;
+  return a.shared ? launch_attend_d<BF, F8, 256, true>(a, stream) : launch_attend_d<BF, F8, 256, false>(a, stream);
 }
 
 }  // namespace qgemv

@@ -56,7 +56,7 @@ struct AttendArgs {
   int64_t q_row, q_head, out_row, out_head;  // bytes
   int B, T, M, G, window, sinks, q_dtype;
   float scale;
-  int chunks;      // waves that share the tokens and split the rows: 1, 2 or 4
+  bool shared;     // the four waves split the rows and share the tokens' loads
   int rt;          // 16-row tiles of a wave
   int workgroups;  // of the main kernel
   int span;        // tiles of a wave in a granule
@@ -80,7 +80,7 @@ struct VerifyArgs {
 };
 
 int launch_append(const AppendArgs &a, hipStream_t stream);
-// Fills in the launch (chunks .. joins) and the workspace's layout from
+// Fills in the launch (shared .. joins) and the workspace's layout from
 // `work`, and returns its size in bytes.
 int64_t plan_attend(AttendArgs *a, void *work);
 int launch_attend(const AttendArgs &a, hipStream_t stream);
