@@ -73,7 +73,7 @@ struct VerifyArgs {
   const int32_t *start;
   int32_t *out, *count;
   double *sums;       // [B][pieces][2]: of what is left, of p
-  int32_t *arrived;   // [B], where slices > 1
+  int32_t *arrived;   // one for each sequence, where slices > 1
   int B, T, M, V, dtype;
   int per, pieces;    // tokens of a piece, pieces of a row
   int each, slices;   // pieces of a wave, workgroups of a sequence
