@@ -7,12 +7,14 @@ the Python layer (``few_row_quantized_amd.qgemv``) only marshals arguments.
 
 Submodules:
   qgemv      ctypes binding of the C ABI declared in include/qgemv.h
+  kv         the verify step's cache append, attention and draft acceptance on
+             torch tensors (qgemv has them too)
   synth      seeded synthetic inputs (no product arithmetic)
   accounting byte / flop counts for bandwidth figures
   build      compiles libqgemv.so with hipcc for gfx950
 """
 
-__all__ = ["qgemv", "synth", "accounting", "build"]
+__all__ = ["qgemv", "kv", "synth", "accounting", "build"]
 
 
 def __getattr__(name):

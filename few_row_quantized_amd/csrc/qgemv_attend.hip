@@ -18,6 +18,7 @@ int64_t plan_attend(AttendArgs *a, void *work) {
   // tokens.  More are split over the four waves, which share the loads.
   const int rt_max = D == 256 ? 2 : 4;
   a->shared = R > rt_max * 16;
+  a->group_magic = (65536 + a->G - 1) / a->G;
   const int waves = a->shared ? 4 : 1, tw = 4 / waves;
   const int groups = (R + waves * rt_max * 16 - 1) / (waves * rt_max * 16);
   a->rt = (R + groups * waves * 16 - 1) / (groups * waves * 16);
@@ -36,6 +37,10 @@ int64_t plan_attend(AttendArgs *a, void *work) {
   const int64_t most = (int64_t)attend_occupancy(D, a->rt) * device_cu_count();
   a->seq_items = a->c.H * groups;
   a->workgroups = (int)(a->joins ? std::min(most, items * granules) : items);
+  // ranks: workgroups of a CU, where all of them run
+  a->ranks = a->joins && a->workgroups == most ? attend_occupancy(D, a->rt) : 1;
+  a->rank_size = a->workgroups / a->ranks;
+  page_magic(a->rank_size, &a->rank_magic, &a->rank_shift);
   a->row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(item_rows, R), 1024 / items));
   // workspace: the plan, maxima and sums, parts
   const auto up = [](int64_t n) { return (n + 255) & ~(int64_t)255; };

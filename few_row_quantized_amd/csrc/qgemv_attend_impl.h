@@ -108,7 +108,8 @@ struct SeqWork {
   int sink_tiles;   // tiles of the sinks before it
   int tiles;        // of both
   int granules;     // of one item
-  int items;        // (head, group of rows) items
+  int groups;       // of rows, an item each
+  int items;        // (head, group of rows)
 };
 
 // A kernel's arguments where the launch put them.  Read through a pointer that
@@ -123,11 +124,19 @@ __device__ __forceinline__ KernArgs *reload(KernArgs *p) {
   return p;
 }
 
+// What no kernel writes: at a uniform index it takes scalar loads, which do not
+// wait for the vector loads in flight.
+template <class T>
+__device__ __forceinline__ const __attribute__((address_space(4))) T *constant(const T *p) {
+  return (const __attribute__((address_space(4))) T *)(uintptr_t)p;
+}
+
 template <class Args>
 __device__ __forceinline__ SeqWork seq_work(Args &a, int b) {
   SeqWork w;
-  const int s0 = min(max(a.start[b], 0), a.T), s1 = min(max(a.start[b + 1], s0), a.T);
-  const int len = min(max(a.len[b], 0), a.c.width * a.c.page);
+  const auto start = constant(a.start), lens = constant(a.len);
+  const int s0 = min(max(start[b], 0), a.T), s1 = min(max(start[b + 1], s0), a.T);
+  const int len = min(max(lens[b], 0), a.c.width * a.c.page);
   w.row0 = s0;
   w.rows = min(s1 - s0, a.M);
   w.pos0 = len - (s1 - s0);
@@ -137,11 +146,12 @@ __device__ __forceinline__ SeqWork seq_work(Args &a, int b) {
   w.low_tile = low >> 5;
   w.sink_tiles = a.window ? min(min((a.sinks >> 5) + ((a.sinks & 31) != 0), w.low_tile), all) : 0;
   w.tiles = w.sink_tiles + max(all - w.low_tile, 0);
-  const int tw = a.shared ? 1 : 4;
-  // an item without tokens still writes its rows
-  w.granules = max((w.tiles + tw * a.span - 1) / (tw * a.span), 1);
-  const int item_rows = (a.shared ? 4 : 1) * a.rt * 16;
-  w.items = w.rows > 0 ? a.c.H * ((w.rows * a.G + item_rows - 1) / item_rows) : 0;
+  // an item without tokens still writes its rows; one that no workgroups share
+  // is one granule
+  w.granules = !a.joins ? 1 : max(a.shared ? w.tiles : (w.tiles + 3) >> 2, 1);
+  const int item_rows = (a.shared ? 64 : 16) * a.rt, R = w.rows * a.G;
+  w.groups = R <= item_rows ? 1 : (R + item_rows - 1) / item_rows;
+  w.items = w.rows > 0 ? a.c.H * w.groups : 0;
   return w;
 }
 
@@ -254,6 +264,59 @@ __device__ __forceinline__ int stage_at(int token, int chunk) {
   return token * (ROW / 16) + (chunk ^ (token / PER & MASK));
 }
 
+// How the granules of a call lie on its workgroups: equal ranges within a rank.
+// The workgroups of a CU do not run alike: in equal ranges, of two the one that
+// came first was done in 395 us where the other took 500, of three in 95, 140
+// and 163 us (the older waves' loads go first).  So the ranks take unequal
+// shares: 64 sequences of 8k..16k tokens, 8 rows 597 -> 584 us, 300..8000
+// tokens, one row 194 -> 190; the optima are flat (within 2% from 158 to 188 of
+// 256).  Short ranges are equal: there the loads of all start at once, and a
+// granule more costs more than a share gains (one sequence of 32768, 4 granules
+// each: 36 us, 39 with shares).
+constexpr int kShareOfTwo = 176, kShareOfTwoShared = 158;  // 256ths, of the first rank
+constexpr int kShareOfThree = 108, kShareOfRest = 138;     // of the first, and of the second in what is left
+constexpr int kRankTiles = 24;                             // tiles of a range from which on
+
+struct Split {
+  int ranks, n;          // ranks of n workgroups each
+  int per0, per1, per2;  // granules of a workgroup
+};
+
+template <class Args>
+__device__ __forceinline__ Split split_of(Args &a, int total) {
+  const int ranks = a.ranks, n = a.rank_size;
+  auto per = [&](int left, int share) {  // share 256ths of what is left, over n workgroups
+    const int part = (left >> 8) * share + ((left & 255) * share >> 8);
+    return max((int)(__umulhi(a.rank_magic, 2u * (uint32_t)(part + n - 1)) >> a.rank_shift), 1);
+  };
+  const bool equal = total * (a.shared ? 1 : 4) < kRankTiles * ranks * n;
+  const int two = equal ? 128 : a.shared ? kShareOfTwoShared : kShareOfTwo;
+  Split s{ranks, n, 0, 0, 0};
+  s.per0 = per(total, ranks == 3 ? (equal ? 86 : kShareOfThree) : ranks == 2 ? two : 256);
+  total = max(total - n * s.per0, 0);
+  s.per1 = per(total, ranks == 3 ? (equal ? 128 : kShareOfRest) : 256);
+  s.per2 = per(max(total - n * s.per1, 0), 256);
+  return s;
+}
+
+// Granules [start, end) of a workgroup.
+__device__ __forceinline__ void split_range(const Split &s, int wg, int *start, int *end) {
+  const int p0 = s.per0, p1 = s.per1, p2 = s.per2;  // (selected as members they go through memory)
+  const bool r1 = wg >= s.n, r2 = wg >= 2 * s.n;
+  const int before = r2 ? p0 + p1 : r1 ? p0 : 0, per = r2 ? p2 : r1 ? p1 : p0;
+  *start = before * s.n + (wg - (r2 ? 2 * s.n : r1 ? s.n : 0)) * per;
+  *end = *start + per;
+}
+
+// The workgroup of a granule.
+__device__ __forceinline__ int split_owner(const Split &s, int granule) {
+  const int p0 = s.per0, p1 = s.per1, p2 = s.per2;
+  const int first = s.n * p0, second = first + s.n * p1;
+  const bool r1 = s.ranks > 1 && granule >= first, r2 = s.ranks > 2 && granule >= second;
+  const int at = granule - (r2 ? second : r1 ? first : 0), per = r2 ? p2 : r1 ? p1 : p0;
+  return (r2 ? 2 * s.n : r1 ? s.n : 0) + (int)((uint32_t)at / (uint32_t)per);
+}
+
 // The range of this workgroup: granules [cur, range1) of all items in order,
 // the first of them in sequence b, before which lie `base`.  False if there is
 // none.  Workgroup 0 writes the plan for the join.
@@ -261,54 +324,67 @@ template <class Args>
 __device__ __forceinline__ bool attend_range(Args &a, int *scan, int *b, int *base, int *cur, int *range1) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int B = a.B;
-  int total = 0, per = 1;
-  // Steps of 256 sequences, one a thread.  The total is needed before a range
-  // can be placed: with more sequences the steps are taken twice.
-  for (int round = B <= 256; round < 2; ++round) {
-    int carry = 0;
-    for (int s0 = 0; s0 < B; s0 += 256) {
-      const int s = s0 + (int)threadIdx.x;
-      int n = 0;
-      if (s < B) {
-        const SeqWork w = seq_work(a, s);
-        n = w.items * w.granules;
-      }
-      int in = n;
+  int total = 0;
+  int at = 0, end = 0;
+  auto place = [&]() { split_range(split_of(a, total), blockIdx.x, &at, &end); };
+  auto granules_of = [&](int s) {
+    const SeqWork w = seq_work(a, s);
+    return w.items * w.granules;
+  };
+  auto inclusive = [&](int in) {
 #pragma unroll
-      for (int k = 1; k < 64; k <<= 1) {
-        const int y = __shfl_up(in, k);
-        if (lane >= k) in += y;
-      }
-      if (lane == 63) scan[wave] = in;
-      __syncthreads();
-      const int n0 = scan[0], n1 = scan[1], n2 = scan[2], n3 = scan[3];
-      in += carry + (wave > 0 ? n0 : 0) + (wave > 1 ? n1 : 0) + (wave > 2 ? n2 : 0);
-      carry += n0 + n1 + n2 + n3;
-      if (B <= 256) total = carry;
-      if (round) {
-        per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-        const int at = blockIdx.x * per;
-        if (n && at >= in - n && at < in) {
-          scan[4] = s;
-          scan[5] = in - n;
-        }
-        if (blockIdx.x == 0 && s < B) a.plan[2 + s] = in;
-      }
-      __syncthreads();
+    for (int k = 1; k < 64; k <<= 1) {
+      const int y = __shfl_up(in, k);
+      if (lane >= k) in += y;
     }
-    total = carry;
+    return in;
+  };
+  if (B <= 64) {  // every wave by itself
+    const int n = lane < B ? granules_of(lane) : 0, in = inclusive(n);
+    total = __builtin_amdgcn_readlane(in, 63);
+    place();
+    if (blockIdx.x == 0 && wave == 0 && lane < B) a.plan[2 + lane] = in;
+    const uint64_t mine = __ballot(n && at >= in - n && at < in);
+    const int at_lane = mine ? (int)__ffsll((long long)mine) - 1 : 0;
+    *b = __builtin_amdgcn_readfirstlane(at_lane);
+    *base = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_readlane(in - n, at_lane));
+  } else {
+    // Steps of 256 sequences, one a thread.  The total is needed before a range
+    // can be placed: with more sequences the steps are taken twice.
+    for (int round = B <= 256; round < 2; ++round) {
+      int carry = 0;
+      for (int s0 = 0; s0 < B; s0 += 256) {
+        const int s = s0 + (int)threadIdx.x;
+        const int n = s < B ? granules_of(s) : 0;
+        int in = inclusive(n);
+        if (lane == 63) scan[wave] = in;
+        __syncthreads();
+        const int n0 = scan[0], n1 = scan[1], n2 = scan[2], n3 = scan[3];
+        in += carry + (wave > 0 ? n0 : 0) + (wave > 1 ? n1 : 0) + (wave > 2 ? n2 : 0);
+        carry += n0 + n1 + n2 + n3;
+        if (B <= 256) total = carry;
+        if (round) {
+          place();
+          if (n && at >= in - n && at < in) {
+            scan[4] = s;
+            scan[5] = in - n;
+          }
+          if (blockIdx.x == 0 && s < B) a.plan[2 + s] = in;
+        }
+        __syncthreads();
+      }
+      total = carry;
+    }
+    *b = __builtin_amdgcn_readfirstlane(scan[4]);
+    *base = __builtin_amdgcn_readfirstlane(scan[5]);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.plan[0] = max(per, 1);
+    a.plan[0] = total;
     a.plan[1] = 0;
   }
-  *cur = blockIdx.x * per;
-  *range1 = min(*cur + per, total);
-  if (*cur >= *range1) return false;
-  *b = __builtin_amdgcn_readfirstlane(scan[4]);
-  *base = __builtin_amdgcn_readfirstlane(scan[5]);
-  *range1 = __builtin_amdgcn_readfirstlane(*range1);
-  *cur = __builtin_amdgcn_readfirstlane(*cur);
+  if (__builtin_amdgcn_readfirstlane((int)(at >= total))) return false;
+  *cur = __builtin_amdgcn_readfirstlane(at);
+  *range1 = __builtin_amdgcn_readfirstlane(min(end, total));
   return true;
 }
 
@@ -352,7 +428,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   while (cur < range1) {
     ap = reload(ap);
     const SeqWork w = seq_work(*ap, b);
-    const int seq_granules = w.items * w.granules, groups = w.items / ap->c.H;
+    const int seq_granules = w.items * w.granules, groups = w.groups;
     int item, first = 0;
     if (joins) {
       if (cur >= base + seq_granules) {  // past this sequence (or it has no rows)
@@ -360,62 +436,18 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
         ++b;
         continue;
       }
-      item = (cur - base) / w.granules;
+      item = (int)((uint32_t)(cur - base) / (uint32_t)w.granules);
       first = (cur - base) - item * w.granules;
     } else {
       item = blockIdx.x - b * ap->seq_items;
       if (item >= w.items) return;
     }
     const int n_granules = min(w.granules - first, range1 - cur);
-    const int h = item / groups, group = item - h * groups;
+    const int h = groups == 1 ? item : (int)((uint32_t)item / (uint32_t)groups), group = item - h * groups;
     cur += n_granules;
 
     const int R = w.rows * ap->G;
     const int row_first = (group * CHUNKS + chunk) * RT * 16;
-
-    // ---- the query rows, one a lane and 16-row tile; rows past R see nothing
-    int pos[RT];
-    u32x4_t qf[QLDS ? 1 : RT][QS];
-    {
-      const int G = ap->G;
-      auto query = [&](int row, int s) -> u32x4_t {
-        const int i = row / G, hq = h * G + row - i * G;
-        // the d of a lane's 8 slots follow the key loads
-        const int d = F8 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-        u32x4_t x = {0, 0, 0, 0};
-        if (row < R) x = *reinterpret_cast<const u32x4_t *>(ap->q + (int64_t)(w.row0 + i) * ap->q_row + hq * ap->q_head + d * 2);
-        return x;
-      };
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int row = row_first + r * 16 + c;
-        pos[r] = row < R ? w.pos0 + row / G : -1;
-        if constexpr (!QLDS) {
-#pragma unroll
-          for (int s = 0; s < QS; ++s) qf[r][s] = query(row, s);
-        }
-      }
-      if constexpr (QLDS) {
-        // [wave's rows][tile][step][lane], every wave a quarter of the steps
-        __syncthreads();  // the last item's queries, or hand-over, have been read
-        const int first_row = group * CHUNKS * RT * 16;
-#pragma unroll 4
-        for (int u = wave; u < CHUNKS * RT * QS; u += 4)
-          queries[u * 64 + lane] = query(first_row + u / QS * 16 + c, u % QS);
-        __syncthreads();
-      }
-    }
-    const u32x4_t *const ql = queries + chunk * RT * QS * 64 + lane;
-
-    f32x4_t acc[RT][NE];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      m[r] = kNegInf;
-      l[r] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < NE; ++e) acc[r][e] = f32x4_t{0, 0, 0, 0};
-    }
 
     ap = reload(ap);
     const uint8_t *const kbase = ap->c.k + h * ap->c.stride_head;
@@ -426,7 +458,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     const uint32_t magic = ap->c.magic;
     const int window = ap->window ? ap->window : 1 << 30;  // none: as wide as any position
     const int sinks = ap->sinks;
-    const float sc = ap->scale * (ap->c.k_scale ? ap->c.k_scale[h] : 1.0f) * kLog2e;
+    const float sc = ap->scale * (ap->c.k_scale ? constant(ap->c.k_scale)[h] : 1.0f) * kLog2e;
     const int t_end = min((first + n_granules) * TW * ap->span, w.tiles);
     int t = first * TW * ap->span + tw;
 
@@ -436,7 +468,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     // Past the last tile, ids are those of the last token, and keys and values
     // the first slot's, a row that stays in the caches.
     auto load_id = [&](int tile) -> int {
-      const int token = min(tile_base(tile) + (lane & 31), w.end - 1);
+      const int token = min(tile_base(tile) + (lane & 31), max(w.end - 1, 0));
       return table[__umulhi(magic, 2 * token) >> shift];
     };
     // offsets of a tile's tokens into the ring; bit i: token i is there
@@ -494,13 +526,62 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     int slot = 0;
     uint32_t there = 0, there_next = 0;
     bool strays = false;  // values that were taken out
-    int id = -1;
-    if (t < t_end) {
-      there = put(t, load_id(t), 0);
-      id = load_id(t + TW);
-      load_k(0);
-      load_v(0);
+    // ---- page ids, then the query rows, then the first keys and values: all on
+    // their way together.  A lane has one row of each 16-row tile; rows past R
+    // repeat the last one and see nothing.
+    const int id0 = load_id(t);
+    int id = load_id(t + TW);
+    int pos[RT];
+    constexpr int NQ = QLDS ? CHUNKS * RT * QS / 4 : RT * QS;
+    u32x4_t qf[NQ];
+    {
+      const int G = ap->G, div = ap->group_magic;
+      auto query = [&](int row, int s) -> u32x4_t {
+        const int at = min(row, R - 1), i = at * div >> 16, hq = h * G + at - i * G;
+        // the d of a lane's 8 slots follow the key loads
+        const int d = F8 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
+        return *reinterpret_cast<const u32x4_t *>(ap->q + (int64_t)(w.row0 + i) * ap->q_row + hq * ap->q_head + d * 2);
+      };
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int row = row_first + r * 16 + c;
+        pos[r] = row < R ? w.pos0 + (row * div >> 16) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) {
+        if constexpr (QLDS)  // [wave's rows][tile][step][lane], every wave a quarter of the steps
+          qf[u] = query(group * CHUNKS * RT * 16 + (u * 4 + wave) / QS * 16 + c, (u * 4 + wave) % QS);
+        else
+          qf[u] = query(row_first + u / QS * 16 + c, u % QS);
+      }
     }
+    there = put(t, id0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_k(0);
+    load_v(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (QLDS) {
+      __syncthreads();  // the last item's queries, or hand-over, have been read
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) queries[(u * 4 + wave) * 64 + lane] = qf[u];
+      __syncthreads();
+    } else {
+      // they have arrived: no wait for them, and what came later, in the loop
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) asm volatile("" : "+v"(qf[u]));
+    }
+    const u32x4_t *const ql = queries + chunk * RT * QS * 64 + lane;
+
+    f32x4_t acc[RT][NE];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      m[r] = kNegInf;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) acc[r][e] = f32x4_t{0, 0, 0, 0};
+    }
+
     for (; t < t_end; t += TW) {
       there_next = put(t + TW, id, slot ^ 1);
       id = load_id(t + 2 * TW);
@@ -562,7 +643,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
           if constexpr (QLDS)
             qa = ql[(r * QS + st) * 64];
           else
-            qa = qf[r][st];
+            qa = qf[r * QS + st];
 #pragma unroll
           for (int tt = 0; tt < 2; ++tt) s[r][tt] = mfma_16x16x32<BF>(ka[tt], qa, s[r][tt]);
         }
@@ -783,7 +864,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     // consecutive d from 4 E g on
     if (tw == 0) {
       const int G = ap->G;
-      const float vs = ap->c.v_scale ? ap->c.v_scale[h] : 1.0f;
+      const float vs = ap->c.v_scale ? constant(ap->c.v_scale)[h] : 1.0f;
       // a part that does not begin its item is its workgroup's first, one that
       // begins it and does not end it is its last
       const int64_t part = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
@@ -841,11 +922,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   const int groups_max = (a.M * a.G + item_rows - 1) / item_rows;
   const int b = blockIdx.x / (a.c.H * groups_max), hg = blockIdx.x - b * (a.c.H * groups_max);
   const SeqWork w = seq_work(a, b);
-  const int groups = w.items / a.c.H, h = hg / groups_max, group = hg - h * groups_max;
+  const int groups = w.items ? w.groups : 0, h = hg / groups_max, group = hg - h * groups_max;
   if (group >= groups) return;
-  const int per = a.plan[0];
+  const Split split = split_of(a, a.plan[0]);
   const int g0 = a.plan[1 + b] + (h * groups + group) * w.granules, g1 = g0 + w.granules;
-  const int w0 = g0 / per, w1 = (g1 - 1) / per;
+  const int w0 = split_owner(split, g0), w1 = split_owner(split, g1 - 1);
   if (w0 == w1) return;  // written by its workgroup
   const int rows = min(w.rows * a.G - group * item_rows, item_rows);
   const int parts = w1 - w0 + 1;
@@ -854,7 +935,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   const int sub = team % per_row, at_once = TEAMS / per_row;
   __shared__ f32x4_t sums[256];
   __shared__ float stats[TEAMS][2];
-  const float vs = a.c.v_scale ? a.c.v_scale[h] : 1.0f;
+  const float vs = a.c.v_scale ? constant(a.c.v_scale)[h] : 1.0f;
   for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
     const int row = r0 + team / per_row;
     float m = kNegInf, l = 0.0f;

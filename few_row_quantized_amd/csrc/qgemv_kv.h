@@ -50,7 +50,7 @@ struct AttendArgs {
   uint8_t *out;
   float *lse;  // [T][Hq], or null
   const int32_t *start, *len;
-  int32_t *plan;  // [0]: granules of a workgroup; [1 + b]: granules before sequence b; [1 + B]: all
+  int32_t *plan;  // [0]: granules of all; [1 + b]: granules before sequence b
   float *ml;      // [2 * workgroups][rows of an item][2]: maximum and sum of a part
   float *part;    // [2 * workgroups][rows of an item][D]: its sums
   int64_t q_row, q_head, out_row, out_head;  // bytes
@@ -58,7 +58,12 @@ struct AttendArgs {
   float scale;
   bool shared;     // the four waves split the rows and share the tokens' loads
   int rt;          // 16-row tiles of a wave
+  int group_magic; // row / G = row * group_magic >> 16 for row < 1024, G <= 64
   int workgroups;  // of the main kernel
+  int ranks;       // of them, one for each workgroup of a CU
+  int rank_size;   // workgroups of a rank, and the division by them
+  uint32_t rank_magic;
+  int rank_shift;
   int span;        // tiles of a wave in a granule
   int row_splits;  // workgroups of the join for one item
   int seq_items;   // items of a sequence of M rows

@@ -283,4 +283,14 @@ def small(codes, scales, biases, x, bits: int, group_size: int, out=None, path="
 
 # ---------------------------------------------------------------- verify step around the products
 
-from .kv import KvCache, append, attend, attend_workspace, verify, verify_workspace  # noqa: E402,F401
+_KV = ("KvCache", "append", "attend", "attend_workspace", "verify", "verify_workspace")
+
+
+def __getattr__(name):
+    # from kv.py, which imports this module: on first use, so that either can
+    # be imported first
+    if name in _KV:
+        from . import kv
+        globals().update({n: getattr(kv, n) for n in _KV})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
