@@ -164,6 +164,15 @@ def test_attend_split_over_a_long_context(ct):
     parity(p, f"one sequence of 20001 {ct}")
 
 
+@pytest.mark.parametrize("M,G,seqs,n", [(5, 10, 7, 7900), (2, 2, 9, 9400), (5, 16, 9, 9400), (3, 48, 7, 7900)])
+def test_attend_long_ranges(M, G, seqs, n):
+    """Enough tokens that the workgroups of a CU take unequal shares: two and
+    three of them, with rows in one wave and over four."""
+    lens = [n + 97 * b - 41 * b * b for b in range(seqs)]
+    p = KvProblem([M] * (seqs - 1) + [1], lens, H=8, G=G, D=64, page=64, seed=n + G)
+    parity(p, f"{seqs} sequences of {n}, {M * G} rows")
+
+
 def test_attend_ragged_batch():
     g = np.random.default_rng(4)
     lens = [int(x) for x in np.exp(g.uniform(0, np.log(3000), 37))]
