@@ -9,6 +9,10 @@
 // sequence is found by counting the starts that are not after t, one start a
 // thread, so that finding it costs one load's latency whatever B is (a binary
 // search: log2 B dependent loads).
+//
+// On an MI355X: 5 rows of one request 2.8 us, as long as the shortest kernel
+// takes; 3476 rows of 256 sequences from fp32 into E4M3, 35.6 MB, 11 us (a pure
+// read of 34 MB: 9 us).
 
 #include "qgemv_kv.h"
 #include "qgemv_device.h"

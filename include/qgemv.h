@@ -414,7 +414,8 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
  *           past M are not looked at and left unwritten).
  *   workspace  qgemv_verify_drafts_workspace bytes, 16-byte aligned, filled
  *           with zeros once before its first use (every call leaves it fit
- *           for the next); not shared by calls that may run at the same time.
+ *           for the next, of any size that it has the bytes for); not shared
+ *           by calls that may run at the same time.
  * A draft outside [0, V) is refused.  Deterministic.
  */
 int64_t qgemv_verify_drafts_workspace(int B, int V);

@@ -278,6 +278,23 @@ def test_what_unseen_slots_hold_does_not_matter_within_a_tile(qt, ct):
         assert torch.isnan(out[2:].float()).all()
 
 
+@pytest.mark.parametrize("ct,D,M,G", [(BF, 64, 16, 9), (BF, 128, 9, 12), (F8, 128, 16, 6), (BF, 256, 8, 6), (F8, 256, 16, 5)])
+def test_what_unseen_slots_hold_does_not_matter_where_waves_split_the_rows(ct, D, M, G):
+    """More rows than one wave takes: the second last row's own value is NaN."""
+    p = KvProblem([M], [300], H=2, G=G, D=D, page=16, dtype=ct, seed=D + G)
+    clean = p.reference()
+    j = 300 - 2
+    vf = p.v.float()
+    vf[int(p.table[0, j // 16]), j % 16] = float("nan")
+    p.v = vf.to(ct)
+    out, lse = KvDevice(p).attend()
+    got, ref = out.clone(), dict(clean, out=clean["out"].copy(), mass=clean["mass"].copy())
+    got[M - 2:], ref["out"][M - 2:], ref["mass"][M - 2:] = 0, 0, 0
+    p.check(got, None, ref, "rows before a NaN")
+    assert torch.isnan(out[M - 2:].float()).all()
+    p.check(torch.zeros_like(out), lse, dict(clean, out=np.zeros_like(clean["out"])), "lse")
+
+
 def test_large_scores():
     # scores of some thousands: weights of 0 and 1, no overflow
     p = KvProblem([3], [200], H=2, G=2, D=128, page=16, spread=400.0)

@@ -178,3 +178,32 @@ def test_calls_without_rows():
     assert q.attend(c, torch.zeros(0, 6, 128, dtype=torch.bfloat16), start, n, 1).shape == (0, 6, 128)
     out, count = q.verify(torch.zeros(0, 9), None, torch.zeros(0, dtype=torch.int32), torch.zeros(0), start, 1)
     assert out.shape == (0,) and count.tolist() == [0, 0, 0]
+
+
+def test_arguments_of_other_kinds():
+    k, v, t = tensors()
+    c = q.KvCache(k, v, t)
+    start, n = torch.tensor([0, 1, 2, 4], dtype=torch.int32), torch.tensor([3, 4, 5], dtype=torch.int32)
+    x, new = torch.zeros(4, 6, 128, dtype=torch.bfloat16), torch.zeros(4, 2, 128)
+    for bad in (lambda: q.append(c, [1.0], new, start, n), lambda: q.append(c, new, new, [0, 1, 2, 4], n),
+                lambda: q.attend(c, None, start, n, 2), lambda: q.attend(c, x, start, n, "2"),
+                lambda: q.attend(c, x, start, n, 2, scale="1"), lambda: q.attend(c, x, start, n, 2, workspace=3),
+                lambda: q.verify(None, None, None, None, start, 2)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(ValueError):
+        q.attend(c, x, start, n, 1 << 40)
+    with pytest.raises(OverflowError):
+        q.attend(c, x, start, n, 2, window=1 << 70)
+    with pytest.raises(ValueError):
+        q.append(c, torch.zeros(8), torch.zeros(8), start, n)
+
+
+def test_either_module_can_be_imported_first():
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for first, second in (("kv", "qgemv"), ("qgemv", "kv")):
+        code = (f"from few_row_quantized_amd import {first}; from few_row_quantized_amd import {second}; "
+                "from few_row_quantized_amd import kv, qgemv; assert qgemv.attend is kv.attend")
+        subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
