@@ -343,15 +343,22 @@ __device__ __forceinline__ bool attend_range(Args &a, int *scan, int *b, int *ba
     const SeqWork w = seq_work(a, s);
     return w.items * w.granules;
   };
-  auto inclusive = [&](int in) {
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-      const int y = __shfl_up(in, k);
-      if (lane >= k) in += y;
-    }
+  auto inclusive = [&](int in) {  // sums over the lanes up to each, by DPP: shifts within 16, then broadcasts
+    in += __builtin_amdgcn_update_dpp(0, in, 0x111, 0xF, 0xF, false);
+    in += __builtin_amdgcn_update_dpp(0, in, 0x112, 0xF, 0xF, false);
+    in += __builtin_amdgcn_update_dpp(0, in, 0x114, 0xF, 0xF, false);
+    in += __builtin_amdgcn_update_dpp(0, in, 0x118, 0xF, 0xF, false);
+    in += __builtin_amdgcn_update_dpp(0, in, 0x142, 0xA, 0xF, false);  // lane 15 to lanes 16..31, 47 to 48..63
+    in += __builtin_amdgcn_update_dpp(0, in, 0x143, 0xC, 0xF, false);  // lane 31 to lanes 32..63
     return in;
   };
-  if (B <= 64) {  // every wave by itself
+  if (B == 1) {
+    total = granules_of(0);
+    place();
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[2] = total;
+    *b = 0;
+    *base = 0;
+  } else if (B <= 64) {  // every wave by itself
     const int n = lane < B ? granules_of(lane) : 0, in = inclusive(n);
     total = __builtin_amdgcn_readlane(in, 63);
     place();
