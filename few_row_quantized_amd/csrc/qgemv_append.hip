@@ -50,12 +50,19 @@ __device__ __forceinline__ f32x8_t load8(const uint8_t *p) {
   return r;
 }
 
-// One rounding, to nearest even.  E4M3 has no infinity: values are limited to
-// +-448 first (two compares, which a NaN passes unchanged).
+// Eight values in the cache's type: one rounding, to nearest even.  E4M3 has no
+// infinity: values are limited to +-448 first (two compares, which a NaN passes
+// unchanged).
 template <int DST>
-__device__ __forceinline__ void store8(uint8_t *p, f32x8_t x, float scale) {
+struct Packed {
+  static constexpr int N = DST == QGEMV_E4M3 ? 2 : 4;
+  uint32_t w[N];
+};
+
+template <int DST>
+__device__ __forceinline__ Packed<DST> pack8(f32x8_t x, float scale) {
+  Packed<DST> o;
   if constexpr (DST == QGEMV_E4M3) {
-    uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float v = x[i] / scale;
@@ -65,22 +72,32 @@ __device__ __forceinline__ void store8(uint8_t *p, f32x8_t x, float scale) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       int d = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
-      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], d, true);
+      o.w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], d, true);
     }
-    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
   } else {
-    u32x4_t o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (DST == QGEMV_BF16) {
-        o[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
-               (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16;
+        o.w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
+                 (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16;
       } else {
-        o[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[2 * i]) |
-               (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[2 * i + 1]) << 16;
+        o.w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[2 * i]) |
+                 (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[2 * i + 1]) << 16;
       }
     }
-    *reinterpret_cast<u32x4_t *>(p) = o;
+  }
+  return o;
+}
+
+template <int DST>
+__device__ __forceinline__ void store8(uint8_t *p, const Packed<DST> &o) {
+  if constexpr (DST == QGEMV_E4M3) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(o.w[0], o.w[1]);
+  } else {
+    u32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = o.w[i];
+    *reinterpret_cast<u32x4_t *>(p) = v;
   }
 }
 
@@ -88,14 +105,16 @@ template <int SRC, int DST>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   constexpr int SB = SRC == QGEMV_F32 ? 4 : 2, DB = DST == QGEMV_E4M3 ? 1 : 2;
   const int t = blockIdx.x;
-  const int per_head = a.c.D / 8, n = a.c.H * per_head;
+  const int shift = __builtin_ctz(a.c.D) - 3, n = a.c.H << shift;  // eights of a head, of a row's keys
   int i = threadIdx.x, h = 0, d = 0;
   bool is_v = false;
+  float scale = 1.0f;
   auto load = [&]() {
     is_v = i >= n;
     const int e = is_v ? i - n : i;
-    h = e / per_head;
-    d = (e - h * per_head) * 8;
+    h = e >> shift;
+    d = (e - (h << shift)) * 8;
+    if (DST == QGEMV_E4M3) scale = (is_v ? a.c.v_scale : a.c.k_scale)[h];
     return load8<SRC>((is_v ? a.nv + t * a.v_row + h * a.v_head : a.nk + t * a.k_row + h * a.k_head) + d * SB);
   };
   f32x8_t x = {};
@@ -111,14 +130,17 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   if (pos < 0 || pos >= (int64_t)a.c.width * a.c.page) return;
   const int idx = page_of(a.c, (int)pos);
   const int id = a.c.table[(int64_t)seq * a.c.width + idx];
+  // the first values in the cache's type while the page id is on its way
+  Packed<DST> o = {};
+  if (i < 2 * n) o = pack8<DST>(x, scale);
+#pragma unroll
+  for (int k = 0; k < Packed<DST>::N; ++k) asm volatile("" : "+v"(o.w[k]));
   if (id < 0 || id >= a.c.pages) return;
   const int64_t slot = id * a.c.stride_page + ((int)pos - idx * a.c.page) * a.c.stride_slot;
   while (i < 2 * n) {
-    uint8_t *dst = (is_v ? a.c.v : a.c.k) + slot + h * a.c.stride_head;
-    const float scale = DST == QGEMV_E4M3 ? (is_v ? a.c.v_scale : a.c.k_scale)[h] : 1.0f;
-    store8<DST>(dst + d * DB, x, scale);
+    store8<DST>((is_v ? a.c.v : a.c.k) + slot + h * a.c.stride_head + d * DB, o);
     i += 256;
-    if (i < 2 * n) x = load();
+    if (i < 2 * n) o = pack8<DST>(load(), scale);
   }
 }
 

@@ -12,6 +12,9 @@ using qgemv::VerifyArgs;
 
 namespace {
 
+// Of 256 threads, in a grid: its threads are counted in 32 bits.
+constexpr int kMaxWorkgroups = (1 << 24) - 1;
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int elem_bytes(int dtype) { return dtype == QGEMV_F32 ? 4 : dtype == QGEMV_E4M3 ? 1 : 2; }
@@ -81,6 +84,7 @@ int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_ro
   if ((s = operand_status(new_k, k_row, k_head, a.c.D, src_dtype)) != QGEMV_OK) return s;
   if ((s = operand_status(new_v, v_row, v_head, a.c.D, src_dtype)) != QGEMV_OK) return s;
   if (T == 0) return QGEMV_OK;
+  if (T > kMaxWorkgroups) return QGEMV_EUNSUPPORTED;
   const int64_t b = elem_bytes(src_dtype);
   a.nk = static_cast<const uint8_t *>(new_k);
   a.nv = static_cast<const uint8_t *>(new_v);
@@ -154,6 +158,7 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
 
 int64_t qgemv_verify_drafts_workspace(int B, int V) {
   if (B < 1 || V < 1 || V > QGEMV_MAX_VOCABULARY) return QGEMV_EINVAL;
+  if (B > kMaxWorkgroups) return QGEMV_EUNSUPPORTED;
   VerifyArgs a;
   a.B = B;
   a.V = V;
@@ -166,6 +171,7 @@ int qgemv_verify_drafts(const void *p, int64_t p_row, const void *q, int64_t q_r
                         int64_t workspace_bytes, void *stream) {
   if (dtype != QGEMV_F32 && dtype != QGEMV_BF16 && dtype != QGEMV_F16) return QGEMV_EINVAL;
   if (B < 1 || V < 1 || V > QGEMV_MAX_VOCABULARY || T < 0 || M < 1 || M > QGEMV_MAX_M) return QGEMV_EINVAL;
+  if (B > kMaxWorkgroups) return QGEMV_EUNSUPPORTED;
   if (!p || !tokens || !u || !start || !out || !count || !workspace) return QGEMV_EINVAL;
   if (p_row < V || (q && q_row < V)) return QGEMV_EINVAL;
   const uintptr_t b = (uintptr_t)elem_bytes(dtype);

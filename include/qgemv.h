@@ -356,8 +356,9 @@ typedef struct qgemv_kv_cache {
  * by its head's scale (one fp32 rounding) and limited to +-448 first.  NaN
  * stays NaN.  Rows with a negative position are dropped.  Two rows that are
  * given the same slot leave either's value there.
- * T = 0 does nothing.  Strides must be multiples of 16 bytes and pointers
- * 16-byte aligned (QGEMV_EALIGN).
+ * T = 0 does nothing; 2^24 rows and more are too many (QGEMV_EUNSUPPORTED).
+ * Strides must be multiples of 16 bytes and pointers 16-byte aligned
+ * (QGEMV_EALIGN).
  */
 int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_row, int64_t k_head,
                     const void *new_v, int64_t v_row, int64_t v_head, int src_dtype,
@@ -382,6 +383,9 @@ int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_ro
  *   workspace  qgemv_kv_attend_workspace bytes, 16-byte aligned, contents
  *           free; not shared by calls that may run at the same time.
  * Scores, softmax statistics and sums are fp32.  Results are deterministic.
+ * 2^24 items (sequences times key-value heads times groups of 64..256 rows) or
+ * 2^30 pieces of work, counted as if every sequence filled the table, are too
+ * many (QGEMV_EUNSUPPORTED).
  */
 int64_t qgemv_kv_attend_workspace(const qgemv_kv_cache *cache, int M, int q_heads, int T);
 int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head,
@@ -416,7 +420,9 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
  *           with zeros once before its first use (every call leaves it fit
  *           for the next, of any size that it has the bytes for); not shared
  *           by calls that may run at the same time.
- * A draft outside [0, V) is refused.  Deterministic.
+ * A draft outside [0, V) is refused.  Deterministic; a sequence's answer does
+ * not depend on the others.  2^24 sequences and more are too many
+ * (QGEMV_EUNSUPPORTED).
  */
 int64_t qgemv_verify_drafts_workspace(int B, int V);
 int qgemv_verify_drafts(const void *p, int64_t p_row, const void *q, int64_t q_row, int dtype,

@@ -91,6 +91,14 @@ def test_verify_refusals(kw, want):
     assert run_verify(**kw) == want
 
 
+def test_calls_too_large_for_a_grid_are_refused():
+    assert run_append(cache(), T=1 << 24) == q.EUNSUPPORTED
+    assert run_verify(B=1 << 24) == q.EUNSUPPORTED
+    assert q.lib().qgemv_verify_drafts_workspace(1 << 24, 100) == q.EUNSUPPORTED
+    assert run_attend(cache(batch=1 << 21)) == q.EUNSUPPORTED
+    assert run_attend(cache(batch=1 << 14, width=1 << 16)) == q.EUNSUPPORTED
+
+
 def test_workspace_sizes():
     L = q.lib()
     assert L.qgemv_kv_attend_workspace(cache(), 2, 48, 4) > 0
