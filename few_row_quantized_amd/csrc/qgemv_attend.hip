@@ -28,13 +28,21 @@ int64_t plan_attend(AttendArgs *a, void *work) {
   if (a->window)
     tiles = std::min(tiles, ((int64_t)a->window + a->M + 30) / 32 + 1 + ((int64_t)a->sinks + 31) / 32);
   const int64_t granules = (tiles + tw - 1) / tw;
-  // An item of at most 4 granules is not shared: one workgroup walks it.
-  a->joins = granules > 4;
-  a->span = a->joins ? 1 : (int)granules;
   const int64_t items = (int64_t)a->B * a->c.H * groups;
+  const int64_t most = (int64_t)attend_occupancy(D, a->rt) * device_cu_count();
+  // Whether items are shared by workgroups, or walked by one each: without parts
+  // and a second kernel, and given out as workgroups end.  They are not where
+  // they are short, up to 4 granules, or up to 32 tiles with items for a quarter
+  // of the workgroups that run at once (16 sequences of 300..1000 tokens, 30
+  // rows, 8 heads: 22.0 -> 19.4 us; 8 sequences 18.3 -> 18.8), or up to 64 with
+  // items for half of them and parts of more than 16 rows (32 sequences of
+  // 500..2000, 48 rows: 55.8 -> 44.3; 128 of 100..2000, 6 rows: 108 -> 120).
+  const int64_t walked = granules * tw;
+  a->joins = granules > 4 && !(walked <= 32 && items * 4 >= most) &&
+             !(walked <= 64 && !a->shared && a->rt > 1 && items * 2 >= most);
+  a->span = a->joins ? 1 : (int)granules;
   // counted in 32 bits on the device, and threads of a grid on the host
   if (items * granules >= (1 << 30) || items >= (1 << 24)) return QGEMV_EUNSUPPORTED;
-  const int64_t most = (int64_t)attend_occupancy(D, a->rt) * device_cu_count();
   a->seq_items = a->c.H * groups;
   a->workgroups = (int)(a->joins ? std::min(most, items * granules) : items);
   // ranks: workgroups of a CU, where all of them run

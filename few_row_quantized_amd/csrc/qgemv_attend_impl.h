@@ -38,8 +38,8 @@
 //   that shares the tokens), whatever the lengths are: a workgroup walks its
 //   range over (sequence, head) items, joins its waves at the end of each item
 //   and writes the result, or its part of an item that other workgroups share,
-//   which a second kernel joins in a fixed order.  Items of at most 4 granules
-//   have a workgroup each.
+//   which a second kernel joins in a fixed order.  Short items have a workgroup
+//   each.
 //
 // On an MI355X: 64 sequences of 8k..16k tokens, 8 heads of 128, 48 rows: 3.25 GB
 // in 572 us (5.7 TB/s; a pure read of as much: 468 us).  64 sequences of

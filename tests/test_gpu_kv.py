@@ -173,6 +173,17 @@ def test_attend_long_ranges(M, G, seqs, n):
     parity(p, f"{seqs} sequences of {n}, {M * G} rows")
 
 
+@pytest.mark.parametrize("B,M,G,n", [(60, 1, 2, 1000), (70, 2, 10, 2000), (50, 5, 16, 1000)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5)])
+def test_attend_items_of_one_workgroup_each(B, M, G, n, window, sinks):
+    """Items of up to 32 and 64 tiles that no two workgroups share, the table as
+    wide as the longest; one sequence with no token, one with fewer than rows."""
+    lens = [n - (37 * b * b) % (n - 20) for b in range(B - 2)] + [0, 1]
+    p = KvProblem([1 + b % M for b in range(B)], lens, H=4, G=G, D=64, page=8, window=window, sinks=sinks, seed=n + G,
+                  extra_width=0)
+    parity(p, f"{B} sequences, {M * G} rows")
+
+
 def test_attend_ragged_batch():
     g = np.random.default_rng(4)
     lens = [int(x) for x in np.exp(g.uniform(0, np.log(3000), 37))]
