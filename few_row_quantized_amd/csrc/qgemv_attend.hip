@@ -13,23 +13,28 @@ int launch_attend_f16_e4m3(const AttendArgs &a, hipStream_t stream);
 
 int64_t plan_attend(AttendArgs *a, void *work) {
   const int D = a->c.D, R = a->M * a->G;
+  const bool f8 = a->c.dtype == QGEMV_E4M3;
+  // the longest item that the table and the window allow, in tiles
+  int64_t tiles = ((int64_t)a->c.page * a->c.width + 31) / 32;
+  if (a->window)
+    tiles = std::min(tiles, ((int64_t)a->window + a->M + 30) / 32 + 1 + ((int64_t)a->sinks + 31) / 32);
   // Up to 64 rows of an item (32 at D = 256, whose output takes twice the
   // registers) are one wave's, and the four waves of a workgroup share the
-  // tokens.  More are split over the four waves, which share the loads.
+  // tokens.  More are split over the four waves, which share the loads; so are
+  // 49 to 64 at D = 128 and 16 bits where no wave has more than one tile, since
+  // such a wave has the CU's registers for itself (95 sequences of 81..85
+  // tokens 26 -> 11 us; of 200..1000 tokens 34.0 and 34.4).
   const int rt_max = D == 256 ? 2 : 4;
-  a->shared = R > rt_max * 16;
+  a->shared = R > rt_max * 16 || (R > 48 && D == 128 && !f8 && tiles <= 4);
   a->group_magic = (65536 + a->G - 1) / a->G;
   const int waves = a->shared ? 4 : 1, tw = 4 / waves;
   const int groups = (R + waves * rt_max * 16 - 1) / (waves * rt_max * 16);
   a->rt = (R + groups * waves * 16 - 1) / (groups * waves * 16);
   const int item_rows = waves * a->rt * 16;
-  // the longest item that the table and the window allow, in tiles
-  int64_t tiles = ((int64_t)a->c.page * a->c.width + 31) / 32;
-  if (a->window)
-    tiles = std::min(tiles, ((int64_t)a->window + a->M + 30) / 32 + 1 + ((int64_t)a->sinks + 31) / 32);
   const int64_t granules = (tiles + tw - 1) / tw;
   const int64_t items = (int64_t)a->B * a->c.H * groups;
-  const int64_t most = (int64_t)attend_occupancy(D, a->rt) * device_cu_count();
+  const int occupancy = attend_occupancy(f8, D, a->rt, a->shared);
+  const int64_t most = (int64_t)occupancy * device_cu_count();
   // Whether items are shared by workgroups, or walked by one each: without parts
   // and a second kernel, and given out as workgroups end.  They are not where
   // they are short, up to 4 granules, or up to 32 tiles with items for a quarter
@@ -46,7 +51,7 @@ int64_t plan_attend(AttendArgs *a, void *work) {
   a->seq_items = a->c.H * groups;
   a->workgroups = (int)(a->joins ? std::min(most, items * granules) : items);
   // ranks: workgroups of a CU, where all of them run
-  a->ranks = a->joins && a->workgroups == most ? attend_occupancy(D, a->rt) : 1;
+  a->ranks = a->joins && a->workgroups == most ? occupancy : 1;
   a->rank_size = a->workgroups / a->ranks;
   page_magic(a->rank_size, &a->rank_magic, &a->rank_shift);
   a->row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(item_rows, R), 1024 / items));

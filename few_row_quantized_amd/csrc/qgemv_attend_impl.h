@@ -253,7 +253,11 @@ __device__ __forceinline__ float value_of(uint32_t w, int i) {
 
 // Workgroups of 256 threads that a CU holds, by registers and LDS: the output
 // takes D / 4 registers a tile of rows, keys and values of a wave D / 2 (16 bits).
-constexpr int attend_occupancy(int D, int rt) { return D * rt <= 128 ? 3 : D * rt <= 384 ? 2 : 1; }
+// With 64 rows at D = 128 they fit two workgroups only from an 8-bit cache (32
+// sequences of 4000..12000 tokens: 225 -> 147 us; 16 bits would spill: 236 -> 328).
+constexpr int attend_occupancy(bool f8, int D, int rt, bool sh) {
+  return D * rt <= 128 ? 3 : D * rt <= 384 || (D == 128 && f8 && !sh) ? 2 : 1;
+}
 
 // Queries stay in registers (D / 8 a tile of rows) while they take less than
 // 32, or 64 where keys and values do not wait in registers.
@@ -1008,7 +1012,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
 
 template <bool BF, bool F8, int D, int RT, bool SH>
 int launch_attend_rt(const AttendArgs &a, hipStream_t stream) {
-  constexpr int OCC = attend_occupancy(D, RT);
+  constexpr int OCC = attend_occupancy(F8, D, RT, SH);
   constexpr size_t bytes = attend_lds(F8, D, RT, SH);
   const auto kern = attend_kernel<BF, F8, D, RT, SH, OCC>;
   if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;

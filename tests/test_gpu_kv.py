@@ -184,6 +184,14 @@ def test_attend_items_of_one_workgroup_each(B, M, G, n, window, sinks):
     parity(p, f"{B} sequences, {M * G} rows")
 
 
+@pytest.mark.parametrize("ct", [BF, F8])
+@pytest.mark.parametrize("lens", [[16, 31, 32, 33, 97, 128], [129, 20, 64], [5000, 300]])
+def test_attend_64_rows(ct, lens):
+    p = KvProblem([16] * (len(lens) - 1) + [13], lens, H=3, G=4, D=128, page=16, dtype=ct, seed=sum(lens), poison=True,
+                  extra_width=0)
+    parity(p, f"64 rows, {lens} {ct}")
+
+
 def test_attend_ragged_batch():
     g = np.random.default_rng(4)
     lens = [int(x) for x in np.exp(g.uniform(0, np.log(3000), 37))]
