@@ -11,7 +11,7 @@
 // search: log2 B dependent loads).
 //
 // On an MI355X: 5 rows of one request 2.8 us, as long as the shortest kernel
-// takes; 3476 rows of 256 sequences from fp32 into E4M3, 35.6 MB, 11 us (a pure
+// takes; 3476 rows of 256 sequences from fp32 into E4M3, 35.6 MB, 10 us (a pure
 // read of 34 MB: 9 us).
 
 #include "qgemv_kv.h"
