@@ -67,6 +67,8 @@ class Generation:
 
     def __init__(self, model, prompts, drafts=3, cache=torch.bfloat16, window=0, sinks=0, page=16, longest=1024,
                  temperature=0.05, seed=1):
+        if len(prompts) * (drafts + 1) > 16:
+            raise ValueError("the rows of a step, drafts + 1 a sequence, are at most 16 in all")
         self.m, self.window, self.sinks, self.temperature = model, window, sinks, temperature
         self.tokens = [list(p) for p in prompts]
         self.cached = [0] * len(prompts)  # tokens whose keys and values are in the cache
