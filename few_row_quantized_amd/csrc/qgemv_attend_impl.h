@@ -148,12 +148,14 @@ __device__ __forceinline__ SeqWork seq_work(Args &a, int b) {
   SeqWork w;
   const auto start = constant(a.start), lens = constant(a.len);
   const int s0 = min(max(start[b], 0), a.T), s1 = min(max(start[b + 1], s0), a.T);
-  const int len = min(max(lens[b], 0), a.c.width * a.c.page);
+  // the rows' positions follow the length itself, what they can see the table:
+  // past its end there are rows, but no tokens
+  const int len = min(max(lens[b], 0), QGEMV_MAX_CONTEXT);
   w.row0 = s0;
   w.rows = min(s1 - s0, a.M);
   w.pos0 = len - (s1 - s0);
-  w.end = min(len, max(w.pos0 + w.rows, 0));
-  const int low = a.window ? max(0, w.pos0 - a.window + 1) : 0;
+  w.end = min(a.c.width * a.c.page, max(w.pos0 + w.rows, 0));
+  const int low = a.window ? min(max(0, w.pos0 - a.window + 1), w.end) : 0;
   const int all = (w.end + 31) >> 5;
   w.low_tile = low >> 5;
   w.sink_tiles = a.window ? min(min((a.sinks >> 5) + ((a.sinks & 31) != 0), w.low_tile), all) : 0;

@@ -307,7 +307,8 @@ int qgemv_gather(const uint8_t *codes, const uint16_t *scales, const uint16_t *b
  * the token at position len[b] - (start[b+1] - t).  start (int32 [B+1],
  * ascending) and len (int32 [B]) are DEVICE arrays: the host reads neither,
  * and every value that comes from them or from the page table is checked on
- * the device before it forms an address.
+ * the device before it forms an address.  A length below 0 counts as 0, one
+ * past QGEMV_MAX_CONTEXT as that.
  *
  * Element types of these entry points.
  */
@@ -336,7 +337,9 @@ int qgemv_gather(const uint8_t *codes, const uint16_t *scales, const uint16_t *b
  *   table and scales 4-byte aligned.
  * A table entry outside [0, pages) is a page that is not there: a row
  * appended to it is dropped, and its tokens are seen by no row.  A token past
- * the table's width is treated alike.
+ * the table's width is treated alike: where a sequence's length passes the
+ * table, its rows keep their positions, those past the table's end are not
+ * stored and see what of their range is there.
  */
 typedef struct qgemv_kv_cache {
   void *k, *v;

@@ -1,0 +1,86 @@
+"""GPU tests of the cache append, the attention and the draft acceptance at
+borders: the table's end, starts out of order, sums that round, weights far
+below the largest, a stream given by its address."""
+import numpy as np
+import pytest
+import torch
+
+from few_row_quantized_amd import qgemv as q
+
+from gpu_util import say
+from kv_util import KvDevice, KvProblem
+
+pytestmark = pytest.mark.gpu
+BF, HF, F8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu(require_gpu):
+    torch.cuda.init()
+    yield
+
+
+# ---------------------------------------------------------------- lengths past the table
+
+def past_the_table(rows, lens, over, **kw):
+    """A problem whose sequences b have over[b] tokens more than the pages that
+    were laid out for them; the table is as wide as the longest."""
+    p = KvProblem(rows, lens, extra_width=0, **kw)
+    p.lens = [n + x for n, x in zip(lens, over)]
+    p.len = torch.tensor(p.lens, dtype=torch.int32)
+    p.poison()
+    return p
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3, 0), (5, 2), (40, 0), (64, 33), (5000, 4)])
+@pytest.mark.parametrize("qt,ct,D,G", [(BF, BF, 128, 2), (HF, F8, 64, 3), (BF, BF, 128, 20)])
+def test_rows_past_the_tables_end(qt, ct, D, G, window, sinks):
+    """Rows stand at len - rows and on, whether or not the table reaches there:
+    the first of them may fit (and see themselves), the others see what is
+    there.  One sequence ends before the table's end, with pages missing."""
+    say(f"attend past the table {qt} {ct} D={D} G={G} window={window} sinks={sinks}")
+    p = past_the_table([5, 5, 2, 4, 3], [96, 96, 96, 96, 40], [4, 1, 2, 90, 20], H=2, G=G, D=D, page=16, q_dtype=qt,
+                       dtype=ct, window=window, sinks=sinks, seed=window + G)
+    p.check(*KvDevice(p).attend(), label="past the table")
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1000, 5)])
+@pytest.mark.parametrize("G", [4, 20])
+def test_rows_past_the_end_of_a_long_table(G, window, sinks):
+    say(f"attend past a long table G={G} window={window}")
+    p = past_the_table([5, 3, 4], [4800, 4800, 700], [3, 700, 0], H=2, G=G, D=64, page=16, window=window, sinks=sinks,
+                       seed=G)
+    p.check(*KvDevice(p).attend(), label="past a long table")
+
+
+@pytest.mark.parametrize("G", [2, 20])
+def test_lengths_far_past_the_table(G):
+    """Up to the largest int32: all of the table without a window, with one the
+    sinks, or nothing."""
+    for window, sinks in ((0, 0), (7, 0), (7, 40), (2 ** 30, 0), (2 ** 31 - 1, 3)):
+        say(f"attend far past the table G={G} window={window}")
+        p = past_the_table([2, 3], [64, 50], [500, 500], H=1, G=G, D=64, page=16, window=min(window, 2 ** 29), sinks=sinks)
+        p.window = window
+        d = KvDevice(p)
+        ref = p.reference()
+        far = (10 ** 9, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1) if window < 100 else ()
+        for n in (0, *far):
+            if n:
+                d.len = torch.tensor([n, n], dtype=torch.int32, device="cuda")
+            p.check(*d.attend(), ref, label=f"length {n}")
+        if window == 7 and sinks == 0:
+            assert np.isneginf(ref["lse"]).all()
+
+
+def test_a_row_appended_to_the_last_slot_sees_itself():
+    """96 slots, a length of 100, 5 rows: the first is appended to slot 95 and
+    attends up to there; the four after it are dropped and see the same."""
+    p = past_the_table([5], [96], [4], H=2, G=2, D=64, page=16, spare=0)
+    d = KvDevice(p)
+    g = torch.Generator().manual_seed(3)
+    new_k, new_v = (torch.randn((5, 2, 64), generator=g) for _ in range(2))
+    q.append(d.cache, new_k.cuda(), new_v.cuda(), d.start, d.len)
+    page, slot = int(p.table[0, 5]), 15
+    p.k[page, slot], p.v[page, slot] = new_k[0].to(BF), new_v[0].to(BF)
+    assert torch.equal(d.k.cpu(), p.k) and torch.equal(d.v.cpu(), p.v)
+    p.check(*d.attend(), label="after the append")
