@@ -129,6 +129,18 @@ __device__ __forceinline__ int block_first(bool flag, int *part) {
   return r;
 }
 
+// The highest thread whose flag is set, 0 if none is.
+__device__ __forceinline__ int block_last(bool flag, int *part) {
+  const uint64_t v = __ballot(flag);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v ? 63 - (int)__clzll((long long)v) : -1;
+  __syncthreads();
+  int r = 0;
+  for (int w = 0; w < 4; ++w)
+    if (part[w] >= 0) r = w * 64 + part[w];
+  __syncthreads();
+  return r;
+}
+
 // max(p - q, 0) that a NaN passes
 __device__ __forceinline__ double rest_of(float p, float q) {
   const double d = (double)p - (double)q;
@@ -286,9 +298,14 @@ __global__ __launch_bounds__(256, 8) void verify_kernel(VerifyArgs a) {
   if (!(share == share)) {
     token = 0;
   } else if (share < total) {
-    const int at = min(block_first(has && run > share, ints), a.pieces - 1);
+    // A running sum of the scan is rounded by the way its terms are grouped, so
+    // that it may pass the share first at a place that adds nothing: pieces,
+    // threads and tokens without a weight are never taken.
+    const double my_sum = use_all ? my_all : my_left;
+    int at = block_first(my_sum > 0.0 && run > share, ints);
+    if (at == 256) at = block_last(my_sum > 0.0, ints);
     __shared__ double before_at;
-    if ((int)threadIdx.x == at) before_at = run - (use_all ? my_all : my_left);
+    if ((int)threadIdx.x == at) before_at = run - my_sum;
     // the piece again, consecutive tokens a thread, four loads at a time
     const int a0 = at * a.per, a1 = min(a0 + a.per, a.V), each = (a.per + 255) / 256;
     const int t0 = min(a0 + (int)threadIdx.x * each, a1), t1 = min(t0 + each, a1);
@@ -319,7 +336,7 @@ __global__ __launch_bounds__(256, 8) void verify_kernel(VerifyArgs a) {
     double ignored;
     double upto = block_scan(mine, part, &ignored);
     upto += before_at;  // after the scan's barriers
-    const int who = block_first(upto > share, ints);
+    const int who = block_first(weighted >= 0 && upto > share, ints);
     __shared__ int drawn;
     if (threadIdx.x == 0) drawn = -1;
     __syncthreads();
@@ -330,14 +347,15 @@ __global__ __launch_bounds__(256, 8) void verify_kernel(VerifyArgs a) {
     } else if ((int)threadIdx.x == who) {
       // (rounded another way: the last with a weight)
       double c = upto - mine;
-      int found = weighted >= 0 ? weighted : t1 - 1;
+      int found = weighted;
       for (int v = t0, done = 0; v < t1 && !done; v += 4) {
         if (t1 - t0 > 4) load4(v);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (done || v + k >= t1) continue;
-          c += weight(v, k);
-          if (c > share) {
+          const double w = weight(v, k);
+          c += w;
+          if (w > 0.0 && c > share) {
             found = v + k;
             done = 1;
           }

@@ -413,7 +413,8 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
  * with the refused token's set to 0), or p[r] where those sum to 0; without a
  * refusal w = p of the last row.  The token is the first i whose running sum
  * w[0] + .. + w[i] exceeds u[last row] * sum(w); V - 1 where none does, 0
- * where that product is NaN.  Products and sums are fp64.
+ * where that product is NaN.  Products and sums are fp64; where their rounding
+ * decides, the token is a neighbour that has a weight, never one without.
  *   out     int32 [T]: the accepted drafts of each sequence, the drawn token,
  *           then -1; count int32 [B]: accepted drafts + 1 (0 for a sequence
  *           without rows).

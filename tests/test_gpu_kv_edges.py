@@ -84,3 +84,40 @@ def test_a_row_appended_to_the_last_slot_sees_itself():
     p.k[page, slot], p.v[page, slot] = new_k[0].to(BF), new_v[0].to(BF)
     assert torch.equal(d.k.cpu(), p.k) and torch.equal(d.v.cpu(), p.v)
     p.check(*d.attend(), label="after the append")
+
+
+# ---------------------------------------------------------------- draws at rounding borders
+
+def weights_at_a_border(V, at):
+    p = torch.zeros(1, V)
+    for i, w in at.items():
+        p[0, i] = w
+    return p
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("V,u,at", [
+    # 1/2 and twice 2^-54, which round to nothing one by one and to a step of
+    # the sum together: where a sum over no weight at all first sees both
+    (600, 0.5, {14: 0.5, 16: 2.0 ** -54, 20: 2.0 ** -54, 550: 0.5}),
+    # the same over the 512-token pieces of a row
+    (30000, 0.5, {7 * 512: 0.5, 8 * 512: 2.0 ** -54, 10 * 512: 2.0 ** -54, 40 * 512: 0.5}),
+    # four tokens a thread: the sum before them, taken back from the sum after
+    # them, is a step above the number that is looked for
+    (140000, 2.0 ** -61, {40: 0.5, 61: 0.5, 62: 2.0 ** -52, 63: 2.0 ** -53, 139000: 2.0 ** 60}),
+])
+def test_no_token_without_weight_is_drawn(dtype, V, u, at):
+    p = weights_at_a_border(V, at).to(dtype)
+    for lead in (0, 1, 2, 3, 5):  # also at other places of a thread and a load
+        x = torch.roll(p, lead, 1)
+        say(f"verify border V={V} {dtype} lead={lead}")
+        one = torch.zeros(1, dtype=torch.int32, device="cuda")
+        start = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        out, n = q.verify(x.cuda(), None, one, torch.tensor([u], device="cuda"), start, 1)
+        assert n.tolist() == [1]
+        i = int(out[0])
+        assert float(x[0, i]) > 0.0, f"token {i} has no weight (at lead {lead})"
+        # and the sum up to it is the number that is looked for, to a few steps
+        c = torch.cumsum(x[0].double(), 0)
+        share, slack = u * float(c[-1]), 16 * 2.0 ** -52 * max(u * float(c[-1]), 0.5)
+        assert float(c[i]) >= share - slack and float(c[i] - x[0, i].double()) <= share + slack
