@@ -3,6 +3,8 @@
 
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "qgemv_kv.h"
 
 using qgemv::AppendArgs;
@@ -109,10 +111,17 @@ int64_t qgemv_kv_attend_workspace(const qgemv_kv_cache *cache, int M, int q_head
   a.c = v;
   a.B = cache->batch;
   a.T = T;
-  a.M = M;
   a.G = q_heads / cache->heads;
   a.window = a.sinks = 0;  // the most that any window needs
-  return qgemv::plan_attend(&a, nullptr);
+  // Fewer rows can need more (other tiles a wave, items shared where M rows are
+  // walked whole): what the call of any M up to this one needs.
+  int64_t most = 0;
+  for (a.M = 1; a.M <= M; ++a.M) {
+    const int64_t need = qgemv::plan_attend(&a, nullptr);
+    if (need < 0) return need;
+    most = std::max(most, need);
+  }
+  return most;
 }
 
 int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head,

@@ -106,8 +106,8 @@ def append(cache: KvCache, new_k, new_v, start, len, stream=None) -> None:
 
 
 def attend_workspace(cache: KvCache, M: int, q_heads: int, T: int):
-    """Scratch memory for attend() calls of this size; one for each stream
-    that runs them."""
+    """Scratch memory for attend() calls of up to M rows a sequence and T in
+    all, of any window; one for each stream that runs them."""
     need = _q._check(_q.lib().qgemv_kv_attend_workspace(cache._ref, M, q_heads, T),
                      "qgemv_kv_attend_workspace")
     return torch.empty(need, dtype=torch.uint8, device=cache.device)

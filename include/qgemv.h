@@ -384,7 +384,9 @@ int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_ro
  *   M       the largest number of rows of a sequence, 1..QGEMV_MAX_M (a
  *           sequence's rows past M are left unwritten).
  *   workspace  qgemv_kv_attend_workspace bytes, 16-byte aligned, contents
- *           free; not shared by calls that may run at the same time.
+ *           free; not shared by calls that may run at the same time.  The size
+ *           for M rows is enough for every smaller M and every window over the
+ *           same cache.
  * Scores, softmax statistics and sums are fp32.  Results are deterministic.
  * 2^24 items (sequences times key-value heads times groups of 64..256 rows) or
  * 2^30 pieces of work, counted as if every sequence filled the table, are too

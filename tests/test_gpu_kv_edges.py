@@ -121,3 +121,20 @@ def test_no_token_without_weight_is_drawn(dtype, V, u, at):
         c = torch.cumsum(x[0].double(), 0)
         share, slack = u * float(c[-1]), 16 * 2.0 ** -52 * max(u * float(c[-1]), 0.5)
         assert float(c[i]) >= share - slack and float(c[i] - x[0, i].double()) <= share + slack
+
+
+# ---------------------------------------------------------------- one workspace for smaller calls
+
+def test_fewer_rows_on_the_workspace_of_more():
+    """Sized once for the most rows of a step, as a serving loop does: 10 rows
+    need no parts over this table, fewer do."""
+    B = 32
+    lens = [2000] + [400 - 11 * b for b in range(1, B)]
+    work = None
+    for M in (10, 8, 1, 5, 2):
+        say(f"attend M={M} on the workspace of 10")
+        p = KvProblem([M] * B, lens, H=4, G=6, D=128, page=16, seed=M, extra_width=0)
+        d = KvDevice(p)
+        if work is None:
+            work = q.attend_workspace(d.cache, 10, 24, 10 * B)
+        p.check(*d.attend(workspace=work), label=f"M={M}")

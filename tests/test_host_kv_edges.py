@@ -1,0 +1,41 @@
+"""The cache operators' host side at its borders (no GPU): workspaces for calls
+of other sizes."""
+import pytest
+
+from few_row_quantized_amd import qgemv as q
+
+from test_host_kv import cache, run_attend
+
+
+# ---------------------------------------------------------------- one workspace for smaller calls
+
+def plain_cache(batch, heads, dim, page, width, f8):
+    size = 1 if f8 else 2
+    scale = 1 << 20 if f8 else None
+    return cache(batch=batch, heads=heads, dim=dim, page=page, width=width, stride_head=dim * size,
+                 stride_slot=heads * dim * size, stride_page=page * heads * dim * size,
+                 dtype=q.E4M3 if f8 else q.BF16, k_scale=scale, v_scale=scale)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("heads,G", [(8, 6), (8, 20), (1, 64), (2, 1), (4, 12)])
+def test_a_workspace_is_enough_for_fewer_rows_and_any_window(heads, G, dim, f8):
+    """The size for M rows against the calls of up to M: a call is refused where
+    it needs more, and with no rows in all nothing is launched.  Batches and
+    table widths cross the limits between shared items and items of one
+    workgroup, and rows those between one, two and more tiles a wave."""
+    L = q.lib()
+    row = heads * G * dim
+    for batch in (1, 7, 16, 32, 64, 95, 200):
+        for width in (2, 8, 13, 63, 125, 126, 2048):
+            c = plain_cache(batch, heads, dim, 16, width, f8)
+            before = 0
+            for M in range(1, q.MAX_M + 1):
+                n = L.qgemv_kv_attend_workspace(c, M, heads * G, 0)
+                assert n >= before > -1, (batch, width, M)
+                before = n
+                for m in range(1, M + 1):
+                    for window, sinks in ((0, 0), (20, 0), (100, 4), (1900, 64)):
+                        assert run_attend(c, xr=row, xh=dim, outr=row, outh=dim, T=0, M=m, heads=heads * G,
+                                          window=window, sinks=sinks, nbytes=n) == q.OK, (batch, width, M, m, window)
