@@ -42,9 +42,12 @@ def _calls():
 
 def _allocating(stream, device):
     """`stream` as the current one: what a call allocates for itself comes from
-    the stream it runs on, so that its memory is not still in use by another."""
+    the stream it runs on, so that its memory is not still in use by another.
+    The address 0 is the default stream, for which ExternalStream would take one
+    of torch's pool that waits for nothing."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
     return torch.cuda.stream(stream)
 
 

@@ -8,7 +8,7 @@ import torch
 from few_row_quantized_amd import qgemv as q
 
 from gpu_util import say
-from kv_util import KvDevice, KvProblem
+from kv_util import KvDevice, KvProblem, draft_problem
 
 pytestmark = pytest.mark.gpu
 BF, HF, F8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
@@ -138,3 +138,27 @@ def test_fewer_rows_on_the_workspace_of_more():
         if work is None:
             work = q.attend_workspace(d.cache, 10, 24, 10 * B)
         p.check(*d.attend(workspace=work), label=f"M={M}")
+
+
+# ---------------------------------------------------------------- streams by address
+
+def test_stream_zero_is_the_default_stream():
+    """0 is the default stream's address; torch's ExternalStream(0) would be a
+    stream of its pool, which waits for nothing."""
+    from few_row_quantized_amd import kv
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        with kv._allocating(0, torch.device("cuda", 0)):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        with kv._allocating(side.cuda_stream, torch.device("cuda", 0)):
+            assert torch.cuda.current_stream().cuda_stream == side.cuda_stream
+    x = [t.cuda() for t in draft_problem([4, 2, 5], 9001, seed=3)]
+    p = KvProblem([5, 4], [3000, 500], H=4, G=6, D=128, page=16)
+    d = KvDevice(p)
+    want, want_out = q.verify(*x, 5), d.attend()[0]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = q.verify(*x, 5, stream=0)
+        out = q.attend(d.cache, d.q, d.start, d.len, p.M, scale=p.scale, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and torch.equal(out, want_out)

@@ -1,7 +1,9 @@
 """The cache operators' host side at its borders (no GPU): workspaces for calls
-of other sizes."""
+of other sizes, streams given by their address."""
 import pytest
+import torch
 
+from few_row_quantized_amd import kv
 from few_row_quantized_amd import qgemv as q
 
 from test_host_kv import cache, run_attend
@@ -39,3 +41,19 @@ def test_a_workspace_is_enough_for_fewer_rows_and_any_window(heads, G, dim, f8):
                     for window, sinks in ((0, 0), (20, 0), (100, 4), (1900, 64)):
                         assert run_attend(c, xr=row, xh=dim, outr=row, outh=dim, T=0, M=m, heads=heads * G,
                                           window=window, sinks=sinks, nbytes=n) == q.OK, (batch, width, M, m, window)
+
+
+# ---------------------------------------------------------------- streams by address
+
+def test_the_address_zero_is_the_default_stream(monkeypatch):
+    """torch.cuda.ExternalStream(0) makes a stream of torch's pool, which is
+    ordered with nothing: it is not what a call on stream 0 runs on."""
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device=None: made.append(s) or ("external", s, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: ("default", device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    on = torch.device("cuda", 0)
+    assert kv._allocating(0, on) == ("default", on) and not made
+    assert kv._allocating(4096, on) == ("external", 4096, on)
+    mine = object()
+    assert kv._allocating(mine, on) is mine
