@@ -125,8 +125,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     const int b = base + (int)threadIdx.x;
     seq += __syncthreads_count(b < a.B && a.start[b + 1] <= t);
   }
-  if (seq >= a.B || t < a.start[0]) return;  // no sequence's row
-  const int64_t pos = (int64_t)min(a.len[seq], QGEMV_MAX_CONTEXT) - ((int64_t)a.start[seq + 1] - t);
+  if (seq >= a.B || t < a.start[seq]) return;  // no sequence's row
+  // (starts are limited to T, as the attention limits them)
+  const int64_t pos = (int64_t)min(a.len[seq], QGEMV_MAX_CONTEXT) - (min(a.start[seq + 1], a.T) - t);
   if (pos < 0 || pos >= (int64_t)a.c.width * a.c.page) return;
   const int idx = page_of(a.c, (int)pos);
   const int id = a.c.table[(int64_t)seq * a.c.width + idx];

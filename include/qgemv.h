@@ -308,7 +308,9 @@ int qgemv_gather(const uint8_t *codes, const uint16_t *scales, const uint16_t *b
  * ascending) and len (int32 [B]) are DEVICE arrays: the host reads neither,
  * and every value that comes from them or from the page table is checked on
  * the device before it forms an address.  A length below 0 counts as 0, one
- * past QGEMV_MAX_CONTEXT as that.
+ * past QGEMV_MAX_CONTEXT as that; a start below 0 as 0, one past T as T, in
+ * every call alike.  Where starts descend, it is not defined which sequence has
+ * the rows between them; the append stores none of them.
  *
  * Element types of these entry points.
  */

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from few_row_quantized_amd import qgemv as q
 
 from gpu_util import say
@@ -162,3 +163,48 @@ def test_stream_zero_is_the_default_stream():
         out = q.attend(d.cache, d.q, d.start, d.len, p.M, scale=p.scale, stream=0)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got)) and torch.equal(out, want_out)
+
+
+# ---------------------------------------------------------------- starts out of order or out of range
+
+def test_starts_are_limited_alike_by_append_and_attention():
+    """start below 0 or past the rows counts as 0 or T: the rows in between are
+    placed as by starts within them, in the cache and in the attention."""
+    for start, same in (([-5, 2, 900], [0, 2, 4]), ([-1, -1, 2 ** 31 - 1], [0, 0, 4]), ([1, 9, 9], [1, 4, 4]),
+                        ([-2 ** 31, 3, 2 ** 31 - 1], [0, 3, 4])):
+        say(f"starts {start}")
+        p = KvProblem([2, 2], [40, 50], H=1, G=2, D=64, page=16)
+        g = torch.Generator().manual_seed(1)
+        new_k, new_v = (torch.randn((4, 1, 64), generator=g) for _ in range(2))
+        p.start = torch.tensor(same, dtype=torch.int32)
+        for t, i, s in oracle.append_places(p.table.numpy(), same, p.lens, p.page, p.P):
+            p.k[i, s], p.v[i, s] = new_k[t].to(BF), new_v[t].to(BF)
+        ref = p.reference()
+        p = KvProblem([2, 2], [40, 50], H=1, G=2, D=64, page=16)
+        d = KvDevice(p)
+        d.start = torch.tensor(start, dtype=torch.int32, device="cuda")
+        q.append(d.cache, new_k.cuda(), new_v.cuda(), d.start, d.len)
+        want = KvProblem([2, 2], [40, 50], H=1, G=2, D=64, page=16)
+        for t, i, s in oracle.append_places(want.table.numpy(), same, want.lens, want.page, want.P):
+            want.k[i, s], want.v[i, s] = new_k[t].to(BF), new_v[t].to(BF)
+        torch.cuda.synchronize()
+        assert torch.equal(d.k.cpu(), want.k) and torch.equal(d.v.cpu(), want.v), start
+        out = torch.zeros_like(d.q)
+        lse = torch.full((4, 2), -float("inf"), device="cuda")
+        d.attend(out=out, lse=lse, M=16)
+        p.check(out, lse, ref, label=str(start))
+
+
+def test_rows_of_descending_starts_write_nothing():
+    """Sequence 1 ends before it begins: rows 3 and 4 are no longer its own, and
+    no slot of it is written (nor any past its length)."""
+    p = KvProblem([3, 2, 3], [20, 20, 20], H=1, G=1, D=64, page=16)
+    new = torch.randn(8, 1, 64)
+    want = p.k.clone()
+    for t, b, pos in ((0, 0, 15), (1, 0, 16), (2, 0, 17), (5, 2, 17), (6, 2, 18), (7, 2, 19)):
+        want[int(p.table[b, pos // 16]), pos % 16] = new[t].to(BF)
+    d = KvDevice(p)
+    d.start = torch.tensor([0, 5, 3, 8], dtype=torch.int32, device="cuda")
+    q.append(d.cache, new.cuda(), new.cuda(), d.start, d.len)
+    torch.cuda.synchronize()
+    assert torch.equal(d.k.cpu(), want)
