@@ -28,9 +28,13 @@
 //   lies between the two halves of a stage.  With each wave reading all tokens
 //   for its rows instead, 16 sequences of 4000..9000 tokens and 192 rows took
 //   265 us, not 150.
-// * Running maximum and sum per row, in base 2.  The maximum moves only when a
-//   score passes it by more than 8 (weights stay below 2^8): most tiles then
-//   leave the output's registers alone.
+// * Running maximum and sum per row, in base 2.  The reference that weights are
+//   taken against moves only when a score passes the maximum it was set by by
+//   more than 8: most tiles then leave the output's registers alone.  For bf16
+//   it is that maximum (the largest weight is 1 to 2^8), for fp16 7 below it
+//   (2^7 to 2^15): fp16 ends at 2^16 above and at 2^-24 below, and with the largest
+//   weight near 1 a long tail of weights below 2^-25 was lost to the output
+//   while the sum counted it (65536 tokens 18 nats below one, 96 rows: all).
 // * Keys of the next tile are loaded as soon as this tile's product has read
 //   the stage, values as soon as theirs has read them: while a wave computes,
 //   a whole tile is on its way.
@@ -65,6 +69,18 @@ __device__ __forceinline__ f32x4_t mfma_16x16x32(u32x4_t a, u32x4_t b, f32x4_t c
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
                                                   __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// How far below the largest score the reference of the weights lies, in base 2.
+template <bool BF>
+constexpr float kHeadroom = BF ? 0.0f : 7.0f;
+
+// log sum exp of weights summed against reference m, from base 2.
+template <bool BF>
+__device__ __forceinline__ float log_of(float m, float l) {
+  // (both terms near the score itself, so that their rounding is no more than its)
+  constexpr float down = BF ? 1.0f : 0.0078125f;  // 2^-headroom
+  return ((m + kHeadroom<BF>) + __builtin_log2f(l * down)) * kLn2;
 }
 
 // Two E4M3 bytes (bytes 2 HI, 2 HI + 1) as a pair of the product's type, exact.
@@ -712,12 +728,13 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
         float x = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
                         fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
         top[r] = row_max(x);
-        moves |= top[r] > m[r] + 8.0f;
+        // (a difference, which is exact: m + 8 would round where scores pass 2^25)
+        moves |= top[r] - m[r] > 8.0f + kHeadroom<BF>;
       }
       if (__any(moves)) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const float mn = fmaxf(m[r], top[r]);
+          const float mn = fmaxf(m[r], top[r] - kHeadroom<BF>);
           const float f = weight_of(m[r], mn);
           m[r] = mn;
           l[r] *= f;
@@ -740,7 +757,8 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
           }
         l[r] += sum;
         // weights leave fp32 here, for the matrix product: half a step of q's
-        // type each, as much as the output's own rounding
+        // type each, as much as the output's own rounding; in fp16 half of 2^-24
+        // absolute below 2^-14, the largest weight being at least 2^7
         pf[r] = u32x4_t{pair_of<BF>(s[r][0][0], s[r][0][1]), pair_of<BF>(s[r][0][2], s[r][0][3]),
                         pair_of<BF>(s[r][1][0], s[r][1][1]), pair_of<BF>(s[r][1][2], s[r][1][3])};
       }
@@ -914,7 +932,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
               }
           if (ap->lse && g == 0)
             ap->lse[(int64_t)(w.row0 + i) * (ap->c.H * G) + hq] =
-                l[r] == 0.0f ? kNegInf : (m[r] + __builtin_log2f(l[r])) * kLn2;
+                l[r] == 0.0f ? kNegInf : log_of<BF>(m[r], l[r]);
         } else {
           const int64_t at = (part * CHUNKS + chunk) * RT * 16 + r * 16 + c;
           float *o = ap->part + at * D;
@@ -1007,7 +1025,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
       *reinterpret_cast<uint2 *>(a.out + (int64_t)(w.row0 + i) * a.out_row + hq * a.out_head + d * 2) = y;
       if (a.lse && d == 0)
         a.lse[(int64_t)(w.row0 + i) * (a.c.H * a.G) + hq] =
-            l == 0.0f ? kNegInf : (m + __builtin_log2f(l)) * kLn2;
+            l == 0.0f ? kNegInf : log_of<BF>(m, l);
     }
   }
 }

@@ -389,7 +389,11 @@ int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_ro
  *           free; not shared by calls that may run at the same time.  The size
  *           for M rows is enough for every smaller M and every window over the
  *           same cache.
- * Scores, softmax statistics and sums are fp32.  Results are deterministic.
+ * Scores, softmax statistics and sums are fp32.  The weights exp(s_j - ..) are
+ * rounded to q_dtype for the product with the values, after their fp32 sum has
+ * taken them: half a step each, relative to the weight; in fp16, weights below
+ * 2^-21 of the largest lose further bits, and those below 2^-32 count as 0
+ * beside the values.  Results are deterministic.
  * 2^24 items (sequences times key-value heads times groups of 64..256 rows) or
  * 2^30 pieces of work, counted as if every sequence filled the table, are too
  * many (QGEMV_EUNSUPPORTED).

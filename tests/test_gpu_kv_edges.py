@@ -9,7 +9,7 @@ import oracle
 from few_row_quantized_amd import qgemv as q
 
 from gpu_util import say
-from kv_util import KvDevice, KvProblem, draft_problem
+from kv_util import STEP, KvDevice, KvProblem, draft_problem
 
 pytestmark = pytest.mark.gpu
 BF, HF, F8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
@@ -208,3 +208,67 @@ def test_rows_of_descending_starts_write_nothing():
     q.append(d.cache, new.cuda(), new.cuda(), d.start, d.len)
     torch.cuda.synchronize()
     assert torch.equal(d.k.cpu(), want)
+
+
+# ---------------------------------------------------------------- fp16: weights far below the largest
+
+@pytest.mark.parametrize("ct", [HF, F8])
+@pytest.mark.parametrize("M,G", [(1, 1), (2, 3), (16, 6)])
+@pytest.mark.parametrize("B,n,nats", [(1, 131072, 18.0), (768, 65536, 18.0), (768, 20000, 17.0)])
+def test_a_long_tail_below_one_large_weight(ct, M, G, B, n, nats):
+    """The first token stands `nats` above a long, nearly uniform remainder and
+    has a value of 0: the output is what the remainder contributes.  B sequences
+    of the same pages, so that a workgroup walks long ranges.  The bound counts
+    as KvProblem.check, but for weights below fp16's normal range: half of
+    2^-24 absolute where the largest weight is at least 2^7, 2^-32 of it."""
+    say(f"attend tail {ct} M={M} G={G} B={B} n={n}")
+    p = KvProblem([M], [n], H=1, G=G, D=64, page=64, q_dtype=HF, dtype=ct, seed=n)
+    g = torch.Generator().manual_seed(n)
+    p.q.zero_()
+    p.q[:, :, 0] = 16.0  # a score is 2 k[0]
+    k, v = p.k.float(), p.v.float()
+    k[..., 0] = 0.05 * torch.randn(k.shape[:3], generator=g)
+    v.copy_(1.0 + 0.25 * torch.rand(v.shape, generator=g))
+    first = int(p.table[0, 0]), 0
+    k[first][:, 0], v[first] = nats / 2.0, 0.0
+    if ct == F8:
+        p.k_scale.fill_(1.0)
+        p.v_scale.fill_(1.0)
+    p.k, p.v = k.to(ct), v.to(ct)
+    r = p.reference()
+    d = KvDevice(p)
+    d.cache = q.KvCache(d.k, d.v, d.table.repeat(B, 1).contiguous(), d.k_scale, d.v_scale)
+    start = torch.arange(B + 1, dtype=torch.int32, device="cuda") * M
+    lse = torch.full((B * M, G), float("nan"), device="cuda")
+    out = q.attend(d.cache, d.q.repeat(B, 1, 1), start, d.len.repeat(B), M, scale=p.scale, lse=lse)
+    count = r["count"][:, None].astype(np.float64)
+    weight = 2 * (p.D + 7) * 2.0 ** -24 * r["size"] + (2 * count + 16) * 2.0 ** -24
+    u = STEP[HF]
+    tol = u * np.abs(r["out"]) + (weight + u)[..., None] * (1 + u) * r["mass"] + 2.0 ** -25 \
+        + 2.0 ** -32 * count[..., None] * r["top"]
+    assert (np.abs(r["out"]) > 4 * tol).all()  # the tail is what is looked at
+    off = np.abs(out.double().cpu().numpy().reshape(B, M, G, 64) - r["out"])
+    assert (off <= tol).all(), f"off by {(off / tol).max()} of the bound, {off.max()} of {np.abs(r['out']).max()}"
+    z = lse.double().cpu().numpy().reshape(B, M, G)
+    assert (np.abs(z - r["lse"]) <= weight + 4 * 2.0 ** -24 * np.abs(r["lse"])).all()
+
+
+@pytest.mark.parametrize("qt", [BF, HF])
+def test_weights_stay_finite_where_scores_have_wide_steps(qt):
+    """Scores past 2^27, whose fp32 steps are 16 and more: no weight passes the
+    type's range, whatever order the largest come in."""
+    for a, b in ((8, 16), (16, 8), (13, 27), (14, 28), (11, 50)):
+        for step in (4.0, 8.0, 12.0, 16.0, 20.0, 24.0, 32.0):
+            p = KvProblem([1], [129], H=1, G=1, D=64, page=16, q_dtype=qt)
+            p.scale = 1.0
+            p.q.zero_()
+            p.q[0, 0, 0], p.q[0, 0, 1] = 2.0 ** 14, 1.0
+            p.k.zero_()
+            at = lambda j: (int(p.table[0, j // 16]), j % 16)  # noqa: E731
+            for j in range(129):
+                p.k[at(j)][0, 0] = a * 2.0 ** 9 + b
+                p.k[at(j)][0, 1] = step * (j // 32)
+            say(f"attend wide steps {qt} {a} {b} {step}")
+            out, lse = KvDevice(p).attend()
+            assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+            assert out.float().abs().max() <= p.v.float().abs().max() * (1 + 2 * STEP[qt])
