@@ -69,6 +69,9 @@ class Generation:
                  temperature=0.05, seed=1):
         if len(prompts) * (drafts + 1) > 16:
             raise ValueError("the rows of a step, drafts + 1 a sequence, are at most 16 in all")
+        self.slots = -(-longest // page) * page  # of a sequence's pages
+        for b, p in enumerate(prompts):
+            self._fits(b, len(p))
         self.m, self.window, self.sinks, self.temperature = model, window, sinks, temperature
         self.tokens = [list(p) for p in prompts]
         self.cached = [0] * len(prompts)  # tokens whose keys and values are in the cache
@@ -86,6 +89,10 @@ class Generation:
         self.random = torch.Generator(device=dev).manual_seed(seed)
         while any(len(t) - 1 > c for t, c in zip(self.tokens, self.cached)):
             self._prefill()
+
+    def _fits(self, b, tokens):
+        if tokens > self.slots:
+            raise ValueError(f"sequence {b} has pages for {self.slots} tokens, not for {tokens}")
 
     def _layer(self, rows, lens):
         """Logits of the rows of all sequences; their keys and values enter the
@@ -120,8 +127,12 @@ class Generation:
         return []
 
     def step(self):
-        """One verify step of all sequences; returns how many tokens each gained."""
-        rows = [t[-1:] + self._draft(t) for t in self.tokens]
+        """One verify step of all sequences; returns how many tokens each gained.
+        Drafts end where a sequence's pages do; a sequence whose last token has no
+        place left ends the generation with a ValueError, before anything is changed."""
+        for b, c in enumerate(self.cached):
+            self._fits(b, c + 1)
+        rows = [t[-1:] + self._draft(t)[:self.slots - c - 1] for t, c in zip(self.tokens, self.cached)]
         lens = [c + len(r) for c, r in zip(self.cached, rows)]
         logits, fed, start = self._layer(rows, lens)
         p = torch.softmax(logits / self.temperature, -1)
@@ -146,7 +157,9 @@ def main():
     a.add_argument("--window", type=int, default=0)
     a = a.parse_args()
     cache = torch.bfloat16 if a.cache == "bf16" else torch.float8_e4m3fn
-    g = Generation(Decoder(), [[1, 2, 3], [70, 80], list(range(100, 140))], a.drafts, cache, a.window, min(a.window, 4))
+    prompts = [[1, 2, 3], [70, 80], list(range(100, 140))]
+    longest = max(map(len, prompts)) + a.steps * (a.drafts + 1)
+    g = Generation(Decoder(), prompts, a.drafts, cache, a.window, min(a.window, 4), longest=longest)
     gained = [g.step() for _ in range(a.steps)]
     for b, t in enumerate(g.tokens):
         n = sum(s[b] for s in gained)
