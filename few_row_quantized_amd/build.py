@@ -1,5 +1,6 @@
 """Build libqgemv.so in-tree with hipcc for gfx950, and the Python module
-_qgemv_torch.so (its calls on torch tensors) with the host compiler.
+_qgemv_torch.so (its calls on torch tensors) with the host compiler, where torch
+and such a compiler are there.
 
     python -m few_row_quantized_amd.build [-v]
 
@@ -64,12 +65,27 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def _module(verbose: bool) -> None:
-    """qgemv_torch.cpp: host code alone, against torch's headers."""
-    import torch
-    root = os.path.dirname(torch.__file__)
-    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    """qgemv_torch.cpp: host code alone, against torch's headers.  Where those or
+    the host compiler are missing there is no module, and none of an earlier
+    build stays; the C library does not need it."""
+    cxx = os.environ.get("CXX", "g++")
+    try:
+        import torch
+        root = os.path.dirname(torch.__file__)
+    except ImportError:
+        root = None
+    include = [os.path.join(root or "", "include"),
+               os.path.join(root or "", "include", "torch", "csrc", "api", "include")]
+    missing = ("torch" if root is None else "torch's headers" if not os.path.isdir(include[0])
+               else cxx if shutil.which(cxx.split()[0]) is None else None)
+    if missing:
+        if os.path.exists(MODULE):
+            os.remove(MODULE)
+        print(f"  _qgemv_torch not built: {missing} not found (the C library does without; "
+              "the verify step's Python calls need it)", flush=True)
+        return
     tmp = MODULE + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+    cmd = [*cxx.split(), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
            "-I", sysconfig.get_paths()["include"], *(f for i in include for f in ("-isystem", i)),
            os.path.join(CSRC, "qgemv_torch.cpp"), "-o", tmp,
@@ -83,21 +99,25 @@ def _module(verbose: bool) -> None:
         print(f"  qgemv_torch.cpp: {time.time() - t0:.1f}s\n{proc.stderr}", end="", flush=True)
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    t0 = time.time()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
-        module = ex.submit(_module, verbose)
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        module.result()
+def _link(objs) -> None:
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     proc = subprocess.run(cmd, capture_output=True, text=True)
     if proc.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{proc.stderr}")
     os.replace(tmp, LIB)
-    if verbose:
-        print(f"built {LIB} in {time.time() - t0:.1f}s", flush=True)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    t0 = time.time()
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        module = ex.submit(_module, verbose)
+        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        _link(objs)
+        if verbose:
+            print(f"built {LIB} in {time.time() - t0:.1f}s", flush=True)
+        module.result()  # what failed there, with the library in place
     return LIB
 
 
