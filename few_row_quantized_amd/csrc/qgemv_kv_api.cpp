@@ -16,6 +16,8 @@ namespace {
 
 // Of 256 threads, in a grid: its threads are counted in 32 bits.
 constexpr int kMaxWorkgroups = (1 << 24) - 1;
+// Values of a row's keys that the append takes: it counts them in 32 bits.
+constexpr int64_t kMaxRow = 1 << 30;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -86,7 +88,7 @@ int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_ro
   if ((s = operand_status(new_k, k_row, k_head, a.c.D, src_dtype)) != QGEMV_OK) return s;
   if ((s = operand_status(new_v, v_row, v_head, a.c.D, src_dtype)) != QGEMV_OK) return s;
   if (T == 0) return QGEMV_OK;
-  if (T > kMaxWorkgroups) return QGEMV_EUNSUPPORTED;
+  if (T > kMaxWorkgroups || (int64_t)a.c.H * a.c.D > kMaxRow) return QGEMV_EUNSUPPORTED;
   const int64_t b = elem_bytes(src_dtype);
   a.nk = static_cast<const uint8_t *>(new_k);
   a.nv = static_cast<const uint8_t *>(new_v);

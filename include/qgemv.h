@@ -361,7 +361,8 @@ typedef struct qgemv_kv_cache {
  * by its head's scale (one fp32 rounding) and limited to +-448 first.  NaN
  * stays NaN.  Rows with a negative position are dropped.  Two rows that are
  * given the same slot leave either's value there.
- * T = 0 does nothing; 2^24 rows and more are too many (QGEMV_EUNSUPPORTED).
+ * T = 0 does nothing; 2^24 rows and more, or more than 2^30 values of a row's
+ * keys, are too many (QGEMV_EUNSUPPORTED).
  * Strides must be multiples of 16 bytes and pointers 16-byte aligned
  * (QGEMV_EALIGN).
  */

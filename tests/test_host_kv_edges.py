@@ -1,12 +1,12 @@
 """The cache operators' host side at its borders (no GPU): workspaces for calls
-of other sizes, streams given by their address."""
+of other sizes, streams given by their address, rows too wide to count."""
 import pytest
 import torch
 
 from few_row_quantized_amd import kv
 from few_row_quantized_amd import qgemv as q
 
-from test_host_kv import cache, run_attend
+from test_host_kv import cache, run_append, run_attend
 
 
 # ---------------------------------------------------------------- one workspace for smaller calls
@@ -57,3 +57,13 @@ def test_the_address_zero_is_the_default_stream(monkeypatch):
     assert kv._allocating(4096, on) == ("external", 4096, on)
     mine = object()
     assert kv._allocating(mine, on) is mine
+
+
+# ---------------------------------------------------------------- rows too wide to count
+
+def test_rows_too_wide_for_the_append_are_refused():
+    """From 2^26 heads of 256 on, a row's values wrapped and nothing was stored."""
+    for heads, dim in ((1 << 26, 256), ((1 << 22) + 1, 256), (1 << 30, 64), ((1 << 31) - 1, 128)):
+        c = cache(heads=heads, dim=dim, stride_slot=1 << 45, stride_page=1 << 50, stride_head=dim * 2)
+        assert run_append(c, kh=dim, vh=dim, kr=1 << 40, vr=1 << 40) == q.EUNSUPPORTED
+        assert run_append(c, kh=dim, vh=dim, kr=1 << 40, vr=1 << 40, T=0) == q.OK
