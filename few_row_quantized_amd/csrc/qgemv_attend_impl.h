@@ -25,9 +25,8 @@
 //   another before an item's end.
 // * More rows than that (SH) are split over the four waves of a workgroup,
 //   which share every tile: each loads 8 of its tokens, and one barrier a tile
-//   lies between the two halves of a stage.  With each wave reading all tokens
-//   for its rows instead, 16 sequences of 4000..9000 tokens and 192 rows took
-//   265 us, not 150.
+//   lies between the two halves of a stage.  16 sequences of 4000..9000 tokens
+//   and 192 rows take 157 us; when each wave read all tokens for its rows, 265.
 // * Running maximum and sum per row, in base 2.  The reference that weights are
 //   taken against moves only when a score passes the maximum it was set by by
 //   more than 8: most tiles then leave the output's registers alone.  For bf16
@@ -272,7 +271,7 @@ __device__ __forceinline__ float value_of(uint32_t w, int i) {
 // Workgroups of 256 threads that a CU holds, by registers and LDS: the output
 // takes D / 4 registers a tile of rows, keys and values of a wave D / 2 (16 bits).
 // With 64 rows at D = 128 they fit two workgroups only from an 8-bit cache (32
-// sequences of 4000..12000 tokens: 225 -> 147 us; 16 bits would spill: 236 -> 328).
+// sequences of 4000..12000 tokens: 225 -> 155 us; 16 bits would spill: 236 -> 328).
 constexpr int attend_occupancy(bool f8, int D, int rt, bool sh) {
   return D * rt <= 128 ? 3 : D * rt <= 384 || (D == 128 && f8 && !sh) ? 2 : 1;
 }

@@ -395,6 +395,9 @@ int qgemv_kv_append(const qgemv_kv_cache *cache, const void *new_k, int64_t k_ro
  * taken them: half a step each, relative to the weight; in fp16, weights below
  * 2^-21 of the largest lose further bits, and those below 2^-32 count as 0
  * beside the values.  Results are deterministic.
+ * The launch follows from the sizes alone (page * width, the window, M, the
+ * batch), since lengths are on the device: over a table much wider than the
+ * sequences a call costs a few us more than over one as wide as the longest.
  * 2^24 items (sequences times key-value heads times groups of 64..256 rows) or
  * 2^30 pieces of work, counted as if every sequence filled the table, are too
  * many (QGEMV_EUNSUPPORTED).
