@@ -411,14 +411,32 @@ def measure_moe(args, capture, time_graph, name="moe30b_gateup_e128_k2048_n1536_
                       "one row's 8 pairs; interleaved rounds, median"}
 
 
+def product_sources():
+    """The files under csrc/ that the products are built from: their sources and
+    what those include, by name.  Profiles of the products do not depend on the
+    library's other operators."""
+    import re
+    from few_row_quantized_amd.build import PRODUCTS
+    csrc = os.path.join(ROOT, "few_row_quantized_amd", "csrc")
+    names, left = set(), list(PRODUCTS)
+    while left:
+        name = left.pop()
+        if name in names:
+            continue
+        names.add(name)
+        text = open(os.path.join(csrc, name), encoding="utf-8").read()
+        left += [i for i in re.findall(r'#include "([^"]+)"', text)
+                 if "/" not in i and os.path.exists(os.path.join(csrc, i))]
+    return sorted(names)
+
+
 def csrc_sha256():
-    """sha256 of the kernel sources with comments and blank lines removed: a
-    profile stays valid across edits of comments only, and goes stale with
-    any change of code."""
-    import glob
+    """sha256 of the products' kernel sources with comments and blank lines
+    removed: a profile stays valid across edits of comments only, and goes stale
+    with any change of code."""
     import hashlib
     import re
-    srcs = sorted(glob.glob(os.path.join(ROOT, "few_row_quantized_amd", "csrc", "*")))
+    srcs = [os.path.join(ROOT, "few_row_quantized_amd", "csrc", n) for n in product_sources()]
     h = hashlib.sha256()
     for f in srcs:
         text = open(f, encoding="utf-8").read()

@@ -34,11 +34,13 @@ COMMON_FLAGS = [
     "-I", os.path.join(ROOT, "include"),
 ]
 
-SOURCES = ["qgemv_api.cpp", "qgemv_dot.hip", "qgemv_dot_add.hip", "qgemv_dot8.hip", "qgemv_dot_fp.hip",
-           "qgemv_mfma.hip",
-           "qgemv_persist.hip", "qgemv_persist_x.hip", "qgemv_gather.hip", "qgemv_probe.hip",
-           "qgemv_kv_api.cpp", "qgemv_append.hip", "qgemv_attend.hip", "qgemv_attend_bf16.hip",
-           "qgemv_attend_f16.hip", "qgemv_attend_bf16_e4m3.hip", "qgemv_attend_f16_e4m3.hip", "qgemv_verify.hip"]
+# the products, and the verify step's other operators
+PRODUCTS = ["qgemv_api.cpp", "qgemv_dot.hip", "qgemv_dot_add.hip", "qgemv_dot8.hip", "qgemv_dot_fp.hip",
+            "qgemv_mfma.hip",
+            "qgemv_persist.hip", "qgemv_persist_x.hip", "qgemv_gather.hip", "qgemv_probe.hip"]
+VERIFY_STEP = ["qgemv_kv_api.cpp", "qgemv_append.hip", "qgemv_attend.hip", "qgemv_attend_bf16.hip",
+               "qgemv_attend_f16.hip", "qgemv_attend_bf16_e4m3.hip", "qgemv_attend_f16_e4m3.hip", "qgemv_verify.hip"]
+SOURCES = PRODUCTS + VERIFY_STEP
 
 
 def hipcc() -> str:
