@@ -7,8 +7,8 @@ the Python layer (``few_row_quantized_amd.qgemv``) only marshals arguments.
 
 Submodules:
   qgemv      ctypes binding of the C ABI declared in include/qgemv.h
-  kv         the verify step's cache append, attention and draft acceptance on
-             torch tensors (qgemv has them too)
+  kv         the verify step's cache append, attention, draft acceptance, routing
+             and adapters on torch tensors (qgemv has them too)
   synth      seeded synthetic inputs (no product arithmetic)
   accounting byte / flop counts for bandwidth figures
   build      compiles libqgemv.so with hipcc for gfx950

@@ -39,7 +39,9 @@ PRODUCTS = ["qgemv_api.cpp", "qgemv_dot.hip", "qgemv_dot_add.hip", "qgemv_dot8.h
             "qgemv_mfma.hip",
             "qgemv_persist.hip", "qgemv_persist_x.hip", "qgemv_gather.hip", "qgemv_probe.hip"]
 VERIFY_STEP = ["qgemv_kv_api.cpp", "qgemv_append.hip", "qgemv_attend.hip", "qgemv_attend_bf16.hip",
-               "qgemv_attend_f16.hip", "qgemv_attend_bf16_e4m3.hip", "qgemv_attend_f16_e4m3.hip", "qgemv_verify.hip"]
+               "qgemv_attend_f16.hip", "qgemv_attend_bf16_e4m3.hip", "qgemv_attend_f16_e4m3.hip", "qgemv_verify.hip",
+               "qgemv_prefix_bf16.hip", "qgemv_prefix_f16.hip", "qgemv_prefix_bf16_e4m3.hip",
+               "qgemv_prefix_f16_e4m3.hip", "qgemv_route.hip", "qgemv_adapt.hip"]
 SOURCES = PRODUCTS + VERIFY_STEP
 
 

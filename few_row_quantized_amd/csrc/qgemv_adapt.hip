@@ -1,0 +1,331 @@
+// Low-rank adapters of many requests beside a shared projection.
+//
+//   out[t] = y[t] + scale[a] * B[a] (A[a] x[t]),  a = adapter[t]
+//
+// A [n][r][K] and B [n][N][r] are small beside the projection's own weights, and
+// each that is used is read once for all rows that have it (once for every 64
+// of them): rows of one adapter, wherever they are among the T, make tiles of
+// 16, 32 or 64 and go through the matrix units together.  Two launches: the
+// first product with K cut over workgroups, whose partial sums the second adds
+// up in order.  Each wave finds the rows of its tile by itself, by ballots over
+// the adapters of all rows (512 at most in a call of the kernels).
+//
+// The sums of the first product enter the second as two parts, each in the
+// weights' type (hi + lo, 16 to 22 bits of the value); in fp16 a row is scaled
+// by a power of two first, so that its largest sum is near 2^14.
+
+#include <algorithm>
+#include <type_traits>
+
+#include "qgemv_attend_impl.h"
+
+namespace qgemv {
+
+namespace {
+
+// Rows of tile `tile`, of up to 16 RT rows of one adapter: their number, and
+// the rows themselves in rows[].  Adapters in the order of their first rows;
+// rows without one come last where `rest` asks for them (adapter -1).
+template <int NC>
+__device__ __forceinline__ int find_rows(const int32_t *adapter, int T, int n, bool rest, int tile, int size,
+                                         int lane, int *rows, int *which) {
+  int mine[NC];
+  uint64_t left[NC], none[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int t = i * 64 + lane;
+    mine[i] = t < T ? adapter[t] : -1;
+    const bool has = (uint32_t)mine[i] < (uint32_t)n;
+    left[i] = __ballot(t < T && has);
+    none[i] = __ballot(t < T && !has);
+  }
+  bool last = false;
+  while (true) {
+    int a = -1;
+    uint64_t mask[NC];
+    int count = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (!found && left[i]) {
+        a = __builtin_amdgcn_readlane(mine[i], (int)__ffsll((long long)left[i]) - 1);
+        found = true;
+      }
+    if (!found) {
+      if (last || !rest) return 0;
+      last = true;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      mask[i] = found ? __ballot(mine[i] == a) & left[i] : none[i];
+      left[i] &= ~mask[i];
+      count += __popcll(mask[i]);
+    }
+    const int tiles = (count + size - 1) / size;
+    if (tile < tiles) {
+      *which = a;
+      int rank = -tile * size;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int at = rank + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask[i] >> 32),
+                                                             __builtin_amdgcn_mbcnt_lo((uint32_t)mask[i], 0));
+        if ((mask[i] >> lane & 1) && at >= 0 && at < size) rows[at] = i * 64 + lane;
+        rank += __popcll(mask[i]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      return min(count - tile * size, size);
+    }
+    tile -= tiles;
+  }
+}
+
+// First product: part[split][t][i] = sum over the split's k of A[i][k] x[t][k].
+// The waves of a workgroup cut its K once more and add up through LDS.
+template <bool BF, int NC, int RT>
+__global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs a) {
+  __shared__ int rows[4][16 * RT];
+  __shared__ f32x4_t sums[3][RT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  int which = -1;
+  const int count =
+      __builtin_amdgcn_readfirstlane(find_rows<NC>(a.adapter, a.T, a.n, false, blockIdx.x, 16 * RT, lane, rows[wave], &which));
+  if (count == 0) return;
+  which = __builtin_amdgcn_readfirstlane(which);
+  const int steps = (a.K + 31) / 32, waves = a.splits * 4;
+  const int per = (steps + waves - 1) / waves;
+  const int s0 = (blockIdx.y * 4 + wave) * per, s1 = min(s0 + per, steps);
+  const uint8_t *xr[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) xr[i] = a.x + (int64_t)rows[wave][min(i * 16 + c, count - 1)] * a.x_row * 2;
+  const int r0 = blockIdx.z * 16;
+  const uint8_t *const ar = a.a + ((int64_t)which * a.r + min(r0 + c, a.r - 1)) * a.K * 2;
+  f32x4_t acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+  constexpr int U = 4;  // steps whose loads are on their way together
+  for (int s = s0; s < s1; s += U) {
+    u32x4_t w[U], x[U][RT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (s + u) * 32 + g * 8;
+      const bool in = (s + u < s1) & (k < a.K);
+      const int64_t at = in ? 2 * (int64_t)k : 0;
+      const uint32_t keep = in ? ~0u : 0u;
+      w[u] = *reinterpret_cast<const u32x4_t *>(ar + at) & keep;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) x[u][i] = *reinterpret_cast<const u32x4_t *>(xr[i] + at) & keep;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[i] = mfma_16x16x32<BF>(w[u], x[u][i], acc[i]);  // lane (c, g): row c, ranks 4 g ..
+  }
+  if (wave > 0)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) sums[wave - 1][i][lane] = acc[i];
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][k] += sums[w][i][lane][k];
+    if (i * 16 + c < count && r0 + g * 4 < a.r)
+      *reinterpret_cast<f32x4_t *>(a.part + ((int64_t)blockIdx.y * a.T + rows[0][i * 16 + c]) * a.r + r0 + g * 4) = acc[i];
+  }
+}
+
+typedef float f32x4_free_t __attribute__((ext_vector_type(4), aligned(4)));
+
+// Second product and the sum.  STEPS of 32 ranks; a wave takes NB tiles of 16
+// columns at a time, whose loads, and those of y, are on their way together.
+template <bool BF, int NC, int RT, int STEPS>
+__global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs a) {
+  constexpr int S = 16 * RT, NB = STEPS > 2 ? 2 : 4;
+  constexpr int W = STEPS * 32 + 8;  // values of a row in LDS: 16 bytes past whole banks
+  extern __shared__ __align__(16) uint8_t lds[];  // rows of each wave's tile, what a row's sums are scaled by, the sums
+  int(*const rows)[S] = reinterpret_cast<int(*)[S]>(lds);
+  float *const back = reinterpret_cast<float *>(lds + 16 * S);
+  uint16_t *const hi = reinterpret_cast<uint16_t *>(lds + 20 * S), *const lo = hi + S * W;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  int which = -1;
+  const int count = __builtin_amdgcn_readfirstlane(
+      find_rows<NC>(a.adapter, a.T, a.n, a.out != a.y, blockIdx.x, S, lane, rows[wave], &which));
+  if (count == 0) return;
+  which = __builtin_amdgcn_readfirstlane(which);
+  if (which >= 0) {
+    const float scale = a.scales ? a.scales[which] : 1.0f;
+    // 16 lanes a row, which cut its ranks
+    for (int i = threadIdx.x >> 4; i < S; i += 16) {
+      const float *const p = a.part + (int64_t)rows[wave][min(i, count - 1)] * a.r;
+      constexpr int Q = (STEPS + 1) / 2;  // fours of a lane
+      f32x4_t v[Q];
+      float most = 0.0f;
+#pragma unroll
+      for (int x = 0; x < Q; ++x) {
+        const int k = (x * 16 + c) * 4;
+        v[x] = f32x4_t{0, 0, 0, 0};
+        if (k < a.r)
+          for (int s = 0; s < a.splits; ++s) v[x] += *reinterpret_cast<const f32x4_t *>(p + (int64_t)s * a.T * a.r + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = fmaxf(most, __builtin_fabsf(v[x][j]));
+      }
+      int up = 0;
+      if constexpr (!BF) {  // scaled to 2^13 .. 2^14
+        auto ror = [](float x, auto by) {
+          return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(by)::value, 0xF, 0xF, true));
+        };
+        most = fmaxf(most, ror(most, std::integral_constant<int, 0x128>{}));
+        most = fmaxf(most, ror(most, std::integral_constant<int, 0x124>{}));
+        most = fmaxf(most, ror(most, std::integral_constant<int, 0x122>{}));
+        most = fmaxf(most, ror(most, std::integral_constant<int, 0x121>{}));
+        up = most > 0.0f && __builtin_isfinite(most) ? min(14 - __builtin_amdgcn_frexp_expf(most), 120) : 0;
+      }
+#pragma unroll
+      for (int x = 0; x < Q; ++x) {
+        const int k = (x * 16 + c) * 4;
+        float rest[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float value = BF ? v[x][j] : __builtin_amdgcn_ldexpf(v[x][j], up);
+          const float top = BF ? (float)(__bf16)value : (float)(_Float16)value;
+          rest[j] = __builtin_isfinite(top) ? value - top : 0.0f;
+          v[x][j] = top;
+        }
+        if (k < STEPS * 32) {
+          *reinterpret_cast<uint2 *>(hi + i * W + k) = make_uint2(pair_of<BF>(v[x][0], v[x][1]), pair_of<BF>(v[x][2], v[x][3]));
+          *reinterpret_cast<uint2 *>(lo + i * W + k) = make_uint2(pair_of<BF>(rest[0], rest[1]), pair_of<BF>(rest[2], rest[3]));
+        }
+      }
+      if (c == 0) back[i] = BF ? scale : __builtin_amdgcn_ldexpf(scale, -up);
+    }
+    __syncthreads();
+  }
+  // lane (c, g) has row c of each 16, columns n0 + 16 j + 4 g ..
+  const uint8_t *const b = a.b + (int64_t)max(which, 0) * a.N * a.r * 2;
+  const int blocks = (a.N + NB * 16 - 1) / (NB * 16);
+  for (int n = blockIdx.y * 4 + wave; n < blocks; n += gridDim.y * 4) {
+    const int n0 = n * (NB * 16);
+    f32x4_free_t y[RT][NB];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const float *const p = a.y + rows[wave][min(i * 16 + c, count - 1)] * a.y_row;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int col = n0 + j * 16 + g * 4;
+        if (col + 4 <= a.N) {
+          y[i][j] = *reinterpret_cast<const f32x4_free_t *>(p + col);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[i][j][k] = p[min(col + k, a.N - 1)];
+        }
+      }
+    }
+    if (which >= 0) {
+      u32x4_t w[NB][STEPS];
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const int k = s * 32 + g * 8;
+          const uint32_t keep = k < a.r ? ~0u : 0u;
+          w[j][s] = *reinterpret_cast<const u32x4_t *>(b + ((int64_t)min(n0 + j * 16 + c, a.N - 1) * a.r + (k < a.r ? k : 0)) * 2) & keep;
+        }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        f32x4_t acc[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const int at = (i * 16 + c) * W + s * 32 + g * 8;
+          const u32x4_t h = *reinterpret_cast<const u32x4_t *>(hi + at), l = *reinterpret_cast<const u32x4_t *>(lo + at);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[j] = mfma_16x16x32<BF>(w[j][s], h, acc[j]);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[j] = mfma_16x16x32<BF>(w[j][s], l, acc[j]);
+        }
+        const float f = back[i * 16 + c];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[i][j][k] += f * acc[j][k];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if (i * 16 + c >= count) continue;
+      float *const p = a.out + rows[wave][i * 16 + c] * a.out_row;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int col = n0 + j * 16 + g * 4;
+        if (col + 4 <= a.N) {
+          *reinterpret_cast<f32x4_free_t *>(p + col) = y[i][j];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (col + k < a.N) p[col + k] = y[i][j][k];
+        }
+      }
+    }
+  }
+}
+
+template <bool BF, int NC, int RT, int STEPS>
+int launch_adapt_up(const AdaptArgs &a, hipStream_t stream) {
+  constexpr size_t bytes = (size_t)16 * RT * (20 + 4 * (STEPS * 32 + 8));
+  constexpr int columns = STEPS > 2 ? 128 : 256;  // of a workgroup
+  const auto kern = adapt_up_kernel<BF, NC, RT, STEPS>;
+  if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
+  const int blocks = (a.N + columns - 1) / columns, want = std::max(1, 4 * device_cu_count() / a.tiles);
+  hipLaunchKernelGGL(kern, dim3(a.tiles, std::min(blocks, want)), dim3(256), bytes, stream, a);
+  return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
+}
+
+template <bool BF, int NC, int RT>
+int launch_adapt_rt(const AdaptArgs &a, hipStream_t stream) {
+  hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT>), dim3(a.tiles, a.splits, (a.r + 15) / 16), dim3(256), 0, stream, a);
+  if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
+  return a.r <= 32 ? launch_adapt_up<BF, NC, RT, 1>(a, stream)
+         : a.r <= 64 ? launch_adapt_up<BF, NC, RT, 2>(a, stream)
+         : a.r <= 128 ? launch_adapt_up<BF, NC, RT, 4>(a, stream)
+                      : launch_adapt_up<BF, NC, RT, 8>(a, stream);
+}
+
+template <bool BF, int NC>
+int launch_adapt_nc(const AdaptArgs &a, hipStream_t stream) {
+  return a.rt == 1 ? launch_adapt_rt<BF, NC, 1>(a, stream)
+         : a.rt == 2 ? launch_adapt_rt<BF, NC, 2>(a, stream)
+                     : launch_adapt_rt<BF, NC, 4>(a, stream);
+}
+
+template <bool BF>
+int launch_adapt_t(const AdaptArgs &a, hipStream_t stream) {
+  if (a.T <= 64) return launch_adapt_nc<BF, 1>(a, stream);
+  return launch_adapt_nc<BF, kAdaptRows / 64>(a, stream);
+}
+
+}  // namespace
+
+int64_t plan_adapt(AdaptArgs *a) {
+  const int each = (a->T + a->n - 1) / a->n;  // rows of an adapter, where all have as many
+  a->rt = each <= 16 ? 1 : each <= 32 ? 2 : 4;
+  const int size = 16 * a->rt;
+  // the most tiles: every adapter, and the rows without one, end in a part of one
+  a->tiles = std::min(a->T, a->T / size + std::min(a->n + 1, a->T));
+  const int ranks = (a->r + 15) / 16, steps = (a->K + 31) / 32;
+  a->splits = std::max(1, std::min({kAdaptSplits, steps / 8, 4 * device_cu_count() / (a->tiles * ranks)}));
+  // the most splits: so the size grows with T and r alone
+  return (int64_t)4 * kAdaptSplits * a->T * a->r;
+}
+
+int launch_adapt(const AdaptArgs &a, hipStream_t stream) {
+  return a.dtype == QGEMV_BF16 ? launch_adapt_t<true>(a, stream) : launch_adapt_t<false>(a, stream);
+}
+
+}  // namespace qgemv

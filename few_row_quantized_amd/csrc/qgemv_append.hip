@@ -157,7 +157,169 @@ int launch_append_src(const AppendArgs &a, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
 }
 
+// ---- with the rotation of positions on the way
+//
+//   angle(i) = position[axis(i)] * freq[i],  i < pairs
+//   (a, b) -> (a cos - b sin, a sin + b cos) of the pair i of a head's values:
+//   2 i and 2 i + 1 (interleaved), or i and pairs + i; the values after the
+//   pairs stay.  Queries and keys are turned, values are not.
+//
+// One workgroup takes a row: its angles once, for all heads, then 16 values of
+// a head to a thread and step, two pieces of eight that hold whole pairs.
+
+// cos and sin of position * freq.  The product of 31 and 24 bits is taken in
+// fp64, and turned into quarter turns there: positions reach millions of turns.
+// What is left is at most an eighth of a turn, where the series of sin and cos
+// end at their 9th and 10th power (next terms below 2^-29 and 2^-30).
+__device__ __forceinline__ float2 turn_of(int position, float freq) {
+  const double quarters = (double)position * (double)freq * 0.63661977236758134308;  // 2 / pi
+  const double whole = __builtin_rint(quarters);
+  const float x = (float)((quarters - whole) * 1.57079632679489661923);
+  const float y = x * x;
+  const float s = x + x * y * (-1.0f / 6 + y * (1.0f / 120 + y * (-1.0f / 5040 + y * (1.0f / 362880))));
+  const float c = 1.0f + y * (-0.5f + y * (1.0f / 24 + y * (-1.0f / 720 + y * (1.0f / 40320 + y * (-1.0f / 3628800)))));
+  const int q = (int)(long long)whole & 3;
+  const float u = q & 1 ? s : c, v = q & 1 ? c : s;
+  return make_float2(q == 1 || q == 2 ? -u : u, q >= 2 ? -v : v);
+}
+
+template <int DST>
+__device__ __forceinline__ void put8(uint8_t *p, f32x8_t x, float scale) {
+  store8<DST>(p, pack8<DST>(x, scale));
+}
+
+template <int SRC, int DST, int OUT>
+__global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a) {
+  constexpr int SB = SRC == QGEMV_F32 ? 4 : 2, DB = DST == QGEMV_E4M3 ? 1 : 2;
+  __shared__ float2 turns[128];
+  const int t = blockIdx.x, tid = threadIdx.x, T = a.rows.T, B = a.rows.B, pairs = a.pairs;
+  const KvView &c = a.rows.c;
+  const int shift = __builtin_ctz(c.D) - 4, per_head = 1 << shift;  // 16 values each
+  const int n = (a.q_heads + 2 * c.H) << shift;
+  // this thread's frequency and its given position, while the sequence is searched
+  float freq = 0.0f;
+  int position = 0;
+  if (tid < pairs) {
+    freq = a.freq[tid];
+    if (a.position) {
+      const int axis = a.axis ? min(max(a.axis[tid], 0), a.axes - 1) : 0;
+      position = a.position[axis * a.position_axis + t];
+    }
+  }
+  // the values of a step: two pieces of eight
+  f32x8_t x, y;
+  int h = 0, d0 = 0, d1 = 0;
+  bool turned = false;
+  auto load = [&](int i) {
+    const int u = i & (per_head - 1);
+    h = i >> shift;
+    turned = false;
+    if (h < a.q_heads + c.H && !a.interleaved) {
+      turned = u * 8 < pairs;
+      const int rest = u * 8 - pairs;
+      d0 = turned ? u * 8 : 2 * pairs + rest;
+      d1 = turned ? pairs + u * 8 : 2 * pairs + rest + (c.D / 2 - pairs);
+    } else {
+      d0 = u * 8;
+      d1 = c.D / 2 + u * 8;
+    }
+    const int hk = h - a.q_heads, hv = hk - c.H;
+    const uint8_t *p = hk < 0 ? a.q + t * a.q_row + h * a.q_head
+                       : hv < 0 ? a.rows.nk + t * a.rows.k_row + hk * a.rows.k_head
+                                : a.rows.nv + t * a.rows.v_row + hv * a.rows.v_head;
+    x = load8<SRC>(p + d0 * SB);
+    y = load8<SRC>(p + d1 * SB);
+  };
+  if (tid < n) load(tid);
+
+  int seq = 0;
+  for (int base = 0; base < B; base += 256) {
+    const int b = base + tid;
+    seq += __syncthreads_count(b < B && a.rows.start[b + 1] <= t);
+  }
+  if (seq >= B || t < a.rows.start[seq]) return;  // no sequence's row
+  const int64_t pos = (int64_t)min(a.rows.len[seq], QGEMV_MAX_CONTEXT) - (min(a.rows.start[seq + 1], T) - t);
+  if (tid < pairs) turns[tid] = turn_of(a.position ? position : (int)pos, freq);
+  // the row's slot, below 0 where it has none
+  int64_t slot = -1;
+  if (pos >= 0 && pos < (int64_t)c.width * c.page) {
+    const int idx = page_of(c, (int)pos);
+    const int id = c.table[(int64_t)seq * c.width + idx];
+    if (id >= 0 && id < c.pages) slot = id * c.stride_page + ((int)pos - idx * c.page) * c.stride_slot;
+  }
+  __syncthreads();
+
+  for (int i = tid; i < n; i += 256) {
+    if (i != tid) load(i);
+    const int hk = h - a.q_heads, hv = hk - c.H;
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 w = turns[d0 + e];
+        const float u = x[e], v = y[e];
+        x[e] = u * w.x - v * w.y;
+        y[e] = u * w.y + v * w.x;
+      }
+    } else if (hv < 0 && a.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        if (d0 < 2 * pairs) {
+          const float2 w = turns[(d0 + e) / 2];
+          const float u = x[e], v = x[e + 1];
+          x[e] = u * w.x - v * w.y;
+          x[e + 1] = u * w.y + v * w.x;
+        }
+        if (d1 < 2 * pairs) {
+          const float2 w = turns[(d1 + e) / 2];
+          const float u = y[e], v = y[e + 1];
+          y[e] = u * w.x - v * w.y;
+          y[e + 1] = u * w.y + v * w.x;
+        }
+      }
+    }
+    if (hk < 0) {
+      uint8_t *const o = a.out + t * a.out_row + h * a.out_head;
+      put8<OUT>(o + d0 * 2, x, 1.0f);
+      put8<OUT>(o + d1 * 2, y, 1.0f);
+    } else if (slot >= 0) {
+      uint8_t *const o = hv < 0 ? c.k + slot + hk * c.stride_head : c.v + slot + hv * c.stride_head;
+      const float scale = DST != QGEMV_E4M3 ? 1.0f : hv < 0 ? c.k_scale[hk] : c.v_scale[hv];
+      put8<DST>(o + d0 * DB, x, scale);
+      put8<DST>(o + d1 * DB, y, scale);
+    }
+  }
+}
+
+template <int SRC, int DST>
+int launch_rotate_dst(const RotateArgs &a, hipStream_t stream) {
+  const dim3 grid(a.rows.T), block(256);
+  if (a.out_dtype == QGEMV_BF16)
+    hipLaunchKernelGGL((rotate_kernel<SRC, DST, QGEMV_BF16>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((rotate_kernel<SRC, DST, QGEMV_F16>), grid, block, 0, stream, a);
+  return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
+}
+
+template <int SRC>
+int launch_rotate_src(const RotateArgs &a, hipStream_t stream) {
+  switch (a.rows.c.dtype) {
+    case QGEMV_BF16: return launch_rotate_dst<SRC, QGEMV_BF16>(a, stream);
+    case QGEMV_F16: return launch_rotate_dst<SRC, QGEMV_F16>(a, stream);
+    case QGEMV_E4M3: return launch_rotate_dst<SRC, QGEMV_E4M3>(a, stream);
+  }
+  return QGEMV_EINVAL;
+}
+
 }  // namespace
+
+int launch_rotate(const RotateArgs &a, hipStream_t stream) {
+  switch (a.rows.src) {
+    case QGEMV_F32: return launch_rotate_src<QGEMV_F32>(a, stream);
+    case QGEMV_BF16: return launch_rotate_src<QGEMV_BF16>(a, stream);
+    case QGEMV_F16: return launch_rotate_src<QGEMV_F16>(a, stream);
+  }
+  return QGEMV_EINVAL;
+}
 
 int launch_append(const AppendArgs &a, hipStream_t stream) {
   switch (a.src) {

@@ -2,7 +2,7 @@
 
 #include <algorithm>
 
-#include "qgemv_attend_impl.h"
+#include "qgemv_prefix_impl.h"
 
 namespace qgemv {
 
@@ -11,7 +11,12 @@ int launch_attend_f16(const AttendArgs &a, hipStream_t stream);
 int launch_attend_bf16_e4m3(const AttendArgs &a, hipStream_t stream);
 int launch_attend_f16_e4m3(const AttendArgs &a, hipStream_t stream);
 
-int64_t plan_attend(AttendArgs *a, void *work) {
+int launch_shared_bf16(const AttendArgs &a, hipStream_t stream);
+int launch_shared_f16(const AttendArgs &a, hipStream_t stream);
+int launch_shared_bf16_e4m3(const AttendArgs &a, hipStream_t stream);
+int launch_shared_f16_e4m3(const AttendArgs &a, hipStream_t stream);
+
+int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix) {
   const int D = a->c.D, R = a->M * a->G;
   const bool f8 = a->c.dtype == QGEMV_E4M3;
   // The longest item that the table and the window allow, in tiles: lengths are
@@ -50,8 +55,9 @@ int64_t plan_attend(AttendArgs *a, void *work) {
   // 500..2000: 48 rows, 32 sequences 54.5 -> 42.8; 30 rows, 16 sequences, below
   // the half: 30.5 and 32.0; 6 rows, 128 sequences: 122 and 128).
   const int64_t walked = granules * tw;
-  a->joins = granules > 4 && !(walked <= 32 && items * 4 >= most) &&
-             !(walked <= 64 && !a->shared && a->rt > 1 && items * 2 >= most);
+  // After a common prefix all items have something to be joined with.
+  a->joins = after_prefix || (granules > 4 && !(walked <= 32 && items * 4 >= most) &&
+             !(walked <= 64 && !a->shared && a->rt > 1 && items * 2 >= most));
   a->span = a->joins ? 1 : (int)granules;
   // counted in 32 bits on the device, and threads of a grid on the host
   if (items * granules >= (1 << 30) || items >= (1 << 24)) return QGEMV_EUNSUPPORTED;
@@ -64,12 +70,42 @@ int64_t plan_attend(AttendArgs *a, void *work) {
   a->row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(item_rows, R), 1024 / items));
   // workspace: the plan, maxima and sums, parts
   const auto up = [](int64_t n) { return (n + 255) & ~(int64_t)255; };
-  const int64_t plan_bytes = a->joins ? up(4 * ((int64_t)a->B + 2)) : 256, parts = a->joins ? 2 * most * item_rows : 0;
+  const int64_t plan_bytes = a->joins ? up(4 * ((int64_t)a->B + 2)) : 256, parts = a->joins ? (2 * most + (after_prefix ? items : 0)) * item_rows : 0;
   uint8_t *p = static_cast<uint8_t *>(work);
   a->plan = reinterpret_cast<int32_t *>(p);
   a->ml = reinterpret_cast<float *>(p + plan_bytes);
   a->part = reinterpret_cast<float *>(p + plan_bytes + up(8 * parts));
   return plan_bytes + up(8 * parts) + 4 * parts * D;
+}
+
+int64_t plan_prefix(AttendArgs *a, void *work) {
+  const int D = a->c.D, tokens = prefix_tokens(D);
+  const int64_t rows = (int64_t)a->T * a->G, tiles = (rows + kPrefixRows - 1) / kPrefixRows;
+  const int64_t items = tiles * a->c.H;
+  // what the table can have in common: all of it but each sequence's last page
+  const int64_t granules = std::max<int64_t>(1, ((int64_t)a->c.page * (a->c.width - 1) + tokens - 1) / tokens);
+  // counted in 32 bits on the device
+  if (rows >= (1 << 30) || items * granules >= (1 << 30)) return QGEMV_EUNSUPPORTED;
+  const int64_t slots = (int64_t)prefix_occupancy(D) * device_cu_count();
+  int64_t workgroups = std::max<int64_t>(1, std::min(slots, items * granules));
+  if (workgroups > 8) workgroups &= ~(int64_t)7;  // as many on each XCD
+  a->pre_tiles = (int)tiles;
+  a->pre_workgroups = (int)workgroups;
+  a->pre_most = items ? (int)(workgroups / items) + 2 : 0;
+  const auto up = [](int64_t n) { return (n + 255) & ~(int64_t)255; };
+  // items * pre_most is at most this, which grows with T
+  const int64_t parts = (slots + 2 * items) * kPrefixRows;
+  uint8_t *p = static_cast<uint8_t *>(work);
+  a->pre_plan = reinterpret_cast<int32_t *>(p);
+  a->pre_ml = reinterpret_cast<float *>(p + 256);
+  a->pre_part = reinterpret_cast<float *>(p + 256 + up(8 * parts));
+  return 256 + up(8 * parts) + 4 * parts * D;
+}
+
+int launch_attend_shared(const AttendArgs &a, hipStream_t stream) {
+  const bool f8 = a.c.dtype == QGEMV_E4M3;
+  if (a.q_dtype == QGEMV_BF16) return f8 ? launch_shared_bf16_e4m3(a, stream) : launch_shared_bf16(a, stream);
+  return f8 ? launch_shared_f16_e4m3(a, stream) : launch_shared_f16(a, stream);
 }
 
 int launch_attend(const AttendArgs &a, hipStream_t stream) {

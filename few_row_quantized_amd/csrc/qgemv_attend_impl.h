@@ -158,22 +158,36 @@ __device__ __forceinline__ const __attribute__((address_space(4))) T *constant(c
   return (const __attribute__((address_space(4))) T *)(uintptr_t)p;
 }
 
-template <class Args>
-__device__ __forceinline__ SeqWork seq_work(Args &a, int b) {
+// PRE: tokens that all sequences have in the same pages are another kernel's
+// (qgemv_prefix_impl.h).  Here a sequence begins after them: positions, the
+// table and the sinks are counted from there, and a row before it sees nothing.
+template <bool PRE, class Args>
+__device__ __forceinline__ int common_pages(Args &a) {
+  if constexpr (!PRE) return 0;
+  // never the table's last page, so that each sequence has an id to look up
+  return min((int)(__umulhi(a.c.magic, 2u * (uint32_t)min(max(constant(a.common)[0], 0), QGEMV_MAX_CONTEXT - 1)) >>
+                   a.c.shift),
+             a.c.width - 1);
+}
+
+template <bool PRE, class Args>
+__device__ __forceinline__ SeqWork seq_work(Args &a, int b, int before) {
   SeqWork w;
   const auto start = constant(a.start), lens = constant(a.len);
   const int s0 = min(max(start[b], 0), a.T), s1 = min(max(start[b + 1], s0), a.T);
   // the rows' positions follow the length itself, what they can see the table:
   // past its end there are rows, but no tokens
-  const int len = min(max(lens[b], 0), QGEMV_MAX_CONTEXT);
+  const int all_tokens = min(max(lens[b], 0), QGEMV_MAX_CONTEXT);
+  const int len = PRE ? max(all_tokens - before, 0) : all_tokens;
   w.row0 = s0;
   w.rows = min(s1 - s0, a.M);
   w.pos0 = len - (s1 - s0);
-  w.end = min(a.c.width * a.c.page, max(w.pos0 + w.rows, 0));
+  w.end = min(a.c.width * a.c.page - (PRE ? before : 0), max(w.pos0 + w.rows, 0));
   const int low = a.window ? min(max(0, w.pos0 - a.window + 1), w.end) : 0;
   const int all = (w.end + 31) >> 5;
   w.low_tile = low >> 5;
-  w.sink_tiles = a.window ? min(min((a.sinks >> 5) + ((a.sinks & 31) != 0), w.low_tile), all) : 0;
+  const int sinks = PRE ? max(a.sinks - before, 0) : a.sinks;
+  w.sink_tiles = a.window ? min(min((sinks >> 5) + ((sinks & 31) != 0), w.low_tile), all) : 0;
   w.tiles = w.sink_tiles + max(all - w.low_tile, 0);
   // an item without tokens still writes its rows; one that no workgroups share
   // is one granule
@@ -353,15 +367,15 @@ __device__ __forceinline__ int split_owner(const Split &s, int granule) {
 // The range of this workgroup: granules [cur, range1) of all items in order,
 // the first of them in sequence b, before which lie `base`.  False if there is
 // none.  Workgroup 0 writes the plan for the join.
-template <class Args>
-__device__ __forceinline__ bool attend_range(Args &a, int *scan, int *b, int *base, int *cur, int *range1) {
+template <bool PRE, class Args>
+__device__ __forceinline__ bool attend_range(Args &a, int before, int *scan, int *b, int *base, int *cur, int *range1) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int B = a.B;
   int total = 0;
   int at = 0, end = 0;
   auto place = [&]() { split_range(split_of(a, total), blockIdx.x, &at, &end); };
   auto granules_of = [&](int s) {
-    const SeqWork w = seq_work(a, s);
+    const SeqWork w = seq_work<PRE>(a, s, before);
     return w.items * w.granules;
   };
   auto inclusive = [&](int in) {  // sums over the lanes up to each, by DPP: shifts within 16, then broadcasts
@@ -428,7 +442,7 @@ __device__ __forceinline__ bool attend_range(Args &a, int *scan, int *b, int *ba
   return true;
 }
 
-template <bool BF, bool F8, int D, int RT, bool SH, int OCC>
+template <bool BF, bool F8, int D, int RT, bool SH, int OCC, bool PRE = false>
 __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   using T = Tile<F8, D>;
   constexpr int KL = T::KL, KC = T::KC, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
@@ -453,10 +467,11 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 
   // Items that no two workgroups share have a workgroup each; the others are
   // walked in equal ranges.
-  const bool joins = ap->joins;
+  const int common = common_pages<PRE>(*ap), before = PRE ? common * ap->c.page : 0;
+  const bool joins = PRE || ap->joins;
   int b, base = 0, cur = 0, range1 = 1;
   if (joins) {
-    if (!attend_range(*ap, scan, &b, &base, &cur, &range1)) return;
+    if (!attend_range<PRE>(*ap, before, scan, &b, &base, &cur, &range1)) return;
   } else {
     b = blockIdx.x / ap->seq_items;
   }
@@ -467,7 +482,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
 
   while (cur < range1) {
     ap = reload(ap);
-    const SeqWork w = seq_work(*ap, b);
+    const SeqWork w = seq_work<PRE>(*ap, b, before);
     const int seq_granules = w.items * w.granules, groups = w.groups;
     int item, first = 0;
     if (joins) {
@@ -492,12 +507,12 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
     ap = reload(ap);
     const uint8_t *const kbase = ap->c.k + h * ap->c.stride_head;
     const uint8_t *const vbase = ap->c.v + h * ap->c.stride_head;
-    const int32_t *const table = ap->c.table + (int64_t)b * ap->c.width;
+    const int32_t *const table = ap->c.table + (int64_t)b * ap->c.width + (PRE ? common : 0);
     const int64_t stride_page = ap->c.stride_page, stride_slot = ap->c.stride_slot;
     const int page = ap->c.page, pages = ap->c.pages, shift = ap->c.shift;
     const uint32_t magic = ap->c.magic;
     const int window = ap->window ? ap->window : 1 << 30;  // none: as wide as any position
-    const int sinks = ap->sinks;
+    const int sinks = PRE ? max(ap->sinks - before, 0) : ap->sinks;
     const float sc = ap->scale * (ap->c.k_scale ? constant(ap->c.k_scale)[h] : 1.0f) * kLog2e;
     const int t_end = min((first + n_granules) * TW * ap->span, w.tiles);
     int t = first * TW * ap->span + tw;
@@ -909,12 +924,16 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       const float vs = ap->c.v_scale ? constant(ap->c.v_scale)[h] : 1.0f;
       // a part that does not begin its item is its workgroup's first, one that
       // begins it and does not end it is its last
-      const int64_t part = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
+      int64_t part = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
+      const bool whole = n_granules == w.granules;
+      // (what others walked has to be joined to it, so it is a part in any case)
+      if (PRE && whole)
+        part = 2 * (int64_t)ap->workgroups + (int64_t)b * ap->seq_items + h * (ap->seq_items / ap->c.H) + group;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const int row = row_first + r * 16 + c;
         if (row >= R) continue;
-        if (n_granules == w.granules) {
+        if (!PRE && whole) {
           const int i = row / G, hq = h * G + row - i * G;
           const float f = l[r] == 0.0f ? 0.0f : vs / l[r];
           uint8_t *o = ap->out + (int64_t)(w.row0 + i) * ap->out_row + hq * ap->out_head;
@@ -954,24 +973,55 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   }
 }
 
+// The parts of the common tokens (qgemv_prefix_impl.h): an item is 128 rows of a
+// head of all the call's, and has n granules; workgroups take per of them each.
+constexpr int kPrefixRows = 128;
+
+struct PrefixPlan {
+  int n, per;
+  int most;  // parts that an item can have
+};
+
+template <class Args>
+__device__ __forceinline__ PrefixPlan prefix_plan(Args &a) {
+  PrefixPlan p;
+  p.n = a.pre_plan[0];
+  p.per = a.pre_plan[1];
+  p.most = p.n ? min((p.n + p.per - 2) / p.per + 1, a.pre_most) : 0;
+  return p;
+}
+
+// Where part `i` of a row is; below 0 if it has fewer.
+template <class Args>
+__device__ __forceinline__ int64_t prefix_part(Args &a, const PrefixPlan &p, int h, int row, int i) {
+  const int item = h * a.pre_tiles + row / kPrefixRows;
+  const uint32_t g0 = (uint32_t)item * (uint32_t)p.n;
+  if (i > (int)((g0 + p.n - 1) / p.per - g0 / p.per)) return -1;
+  return ((int64_t)item * a.pre_most + i) * kPrefixRows + row % kPrefixRows;
+}
+
 // Joins the parts of the items that several workgroups shared.  A team of D / 4
 // threads takes a row and all or every 8th of its parts, in order, with a
 // running maximum; teams of one row are joined in order through LDS.
-template <bool BF, int D>
+//
+// PRE: all items, with the parts of the tokens before them.
+template <bool BF, int D, bool PRE = false>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   constexpr int TEAM = D / 4, TEAMS = 256 / TEAM;
   const int item_rows = (a.shared ? 4 : 1) * a.rt * 16;
   const int groups_max = (a.M * a.G + item_rows - 1) / item_rows;
   const int b = blockIdx.x / (a.c.H * groups_max), hg = blockIdx.x - b * (a.c.H * groups_max);
-  const SeqWork w = seq_work(a, b);
+  const SeqWork w = seq_work<PRE>(a, b, common_pages<PRE>(a) * a.c.page);
   const int groups = w.items ? w.groups : 0, h = hg / groups_max, group = hg - h * groups_max;
   if (group >= groups) return;
   const Split split = split_of(a, a.plan[0]);
+  const PrefixPlan pre = PRE ? prefix_plan(a) : PrefixPlan{};
+  const int first_row = w.row0 * a.G + group * item_rows;  // of all rows of the call
   const int g0 = a.plan[1 + b] + (h * groups + group) * w.granules, g1 = g0 + w.granules;
   const int w0 = split_owner(split, g0), w1 = split_owner(split, g1 - 1);
-  if (w0 == w1) return;  // written by its workgroup
+  if (!PRE && w0 == w1) return;  // written by its workgroup
   const int rows = min(w.rows * a.G - group * item_rows, item_rows);
-  const int parts = w1 - w0 + 1;
+  const int own = w1 - w0 + 1, parts = own + pre.most;
   const int per_row = parts >= 2 * TEAMS ? TEAMS : 1;  // teams of a row
   const int team = threadIdx.x / TEAM, d = (threadIdx.x % TEAM) * 4;
   const int sub = team % per_row, at_once = TEAMS / per_row;
@@ -985,9 +1035,19 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
     if (row < rows) {
 #pragma unroll 4
       for (int i = sub; i < parts; i += per_row) {
-        const int64_t at = (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * item_rows + row;
-        const float m2 = a.ml[at * 2], l2 = a.ml[at * 2 + 1];
-        const f32x4_t y = *reinterpret_cast<const f32x4_t *>(a.part + at * D + d);
+        int64_t at = (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * item_rows + row;
+        const float *ml = a.ml, *part = a.part;
+        if constexpr (PRE) {
+          if (own == 1) at = (2 * (int64_t)a.workgroups + blockIdx.x) * item_rows + row;
+          if (i >= own) {
+            at = prefix_part(a, pre, h, first_row + row, i - own);
+            if (at < 0) continue;
+            ml = a.pre_ml;
+            part = a.pre_part;
+          }
+        }
+        const float m2 = ml[at * 2], l2 = ml[at * 2 + 1];
+        const f32x4_t y = *reinterpret_cast<const f32x4_t *>(part + at * D + d);
         const float mn = fmaxf(m, m2), f1 = weight_of(m, mn), f2 = weight_of(m2, mn);
         m = mn;
         l = l * f1 + l2 * f2;
@@ -1029,35 +1089,41 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   }
 }
 
-template <bool BF, bool F8, int D, int RT, bool SH>
+template <bool BF, bool F8, int D, int RT, bool SH, bool PRE>
 int launch_attend_rt(const AttendArgs &a, hipStream_t stream) {
   constexpr int OCC = attend_occupancy(F8, D, RT, SH);
   constexpr size_t bytes = attend_lds(F8, D, RT, SH);
-  const auto kern = attend_kernel<BF, F8, D, RT, SH, OCC>;
+  const auto kern = attend_kernel<BF, F8, D, RT, SH, OCC, PRE>;
   if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
   hipLaunchKernelGGL(kern, dim3(a.workgroups), dim3(256), bytes, stream, a);
   if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
   if (!a.joins) return QGEMV_OK;
-  hipLaunchKernelGGL((join_kernel<BF, D>), dim3(a.B * a.seq_items, a.row_splits), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((join_kernel<BF, D, PRE>), dim3(a.B * a.seq_items, a.row_splits), dim3(256), 0, stream, a);
   return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
 }
 
-template <bool BF, bool F8, int D, bool SH>
+template <bool BF, bool F8, int D, bool SH, bool PRE>
 int launch_attend_d(const AttendArgs &a, hipStream_t stream) {
   if constexpr (D < 256) {
-    if (a.rt == 3) return launch_attend_rt<BF, F8, D, 3, SH>(a, stream);
-    if (a.rt == 4) return launch_attend_rt<BF, F8, D, 4, SH>(a, stream);
+    if (a.rt == 3) return launch_attend_rt<BF, F8, D, 3, SH, PRE>(a, stream);
+    if (a.rt == 4) return launch_attend_rt<BF, F8, D, 4, SH, PRE>(a, stream);
   }
-  return a.rt == 1 ? launch_attend_rt<BF, F8, D, 1, SH>(a, stream) : launch_attend_rt<BF, F8, D, 2, SH>(a, stream);
+  return a.rt == 1 ? launch_attend_rt<BF, F8, D, 1, SH, PRE>(a, stream)
+                   : launch_attend_rt<BF, F8, D, 2, SH, PRE>(a, stream);
 }
 
-template <bool BF, bool F8>
+template <bool BF, bool F8, bool PRE = false>
 int launch_attend_t(const AttendArgs &a, hipStream_t stream) {
   switch (a.c.D) {
-    case 64: return a.shared ? launch_attend_d<BF, F8, 64, true>(a, stream) : launch_attend_d<BF, F8, 64, false>(a, stream);
-    case 128: return a.shared ? launch_attend_d<BF, F8, 128, true>(a, stream) : launch_attend_d<BF, F8, 128, false>(a, stream);
+    case 64:
+      return a.shared ? launch_attend_d<BF, F8, 64, true, PRE>(a, stream)
+                           : launch_attend_d<BF, F8, 64, false, PRE>(a, stream);
+    case 128:
+      return a.shared ? launch_attend_d<BF, F8, 128, true, PRE>(a, stream)
+                           : launch_attend_d<BF, F8, 128, false, PRE>(a, stream);
   }
-  return a.shared ? launch_attend_d<BF, F8, 256, true>(a, stream) : launch_attend_d<BF, F8, 256, false>(a, stream);
+  return a.shared ? launch_attend_d<BF, F8, 256, true, PRE>(a, stream)
+                       : launch_attend_d<BF, F8, 256, false, PRE>(a, stream);
 }
 
 }  // namespace qgemv

@@ -68,6 +68,51 @@ struct AttendArgs {
   int row_splits;  // workgroups of the join for one item
   int seq_items;   // items of a sequence of M rows
   bool joins;      // whether an item can lie in more than one workgroup
+  // attention over a common prefix (qgemv_prefix_impl.h)
+  const int32_t *common;  // its tokens, or null
+  int32_t *pre_plan;      // granules of an item, granules of a workgroup
+  float *pre_ml;          // [items][pre_most][128][2]
+  float *pre_part;        // [items][pre_most][128][D]
+  int pre_tiles;          // items of a head: groups of 128 rows of all
+  int pre_workgroups, pre_most;
+};
+
+struct RotateArgs {
+  AppendArgs rows;
+  const uint8_t *q;
+  uint8_t *out;
+  int64_t q_row, q_head, out_row, out_head;  // bytes
+  const float *freq;        // [pairs]
+  const int32_t *position;  // [axes][T], or null: the row's place in the cache
+  const int32_t *axis;      // [pairs], or null: the first
+  int64_t position_axis;    // elements between axes
+  int q_heads, out_dtype, pairs, axes;
+  bool interleaved;
+};
+
+struct RouteArgs {
+  const uint8_t *logits;
+  int64_t row;        // elements
+  const float *bias;  // [E], or null
+  int32_t *experts;   // [T][k]
+  float *weights;     // [T][k]
+  int T, E, k, dtype, groups, keep, best;
+  bool softmax, renormalise;
+  float scale;
+};
+
+struct AdaptArgs {
+  const float *y;
+  float *out;
+  const uint8_t *x, *a, *b;
+  const int32_t *adapter;
+  const float *scales;  // [n], or null
+  float *part;          // [splits][T][r]: sums of the first product
+  int64_t y_row, out_row, x_row;  // elements
+  int T, n, r, K, N, dtype;
+  int tiles;   // of rows: the most there can be
+  int splits;  // of K
+  int rt;      // 16-row tiles of a tile of rows
 };
 
 struct VerifyArgs {
@@ -87,8 +132,19 @@ struct VerifyArgs {
 int launch_append(const AppendArgs &a, hipStream_t stream);
 // Fills in the launch (shared .. joins) and the workspace's layout from
 // `work`, and returns its size in bytes.
-int64_t plan_attend(AttendArgs *a, void *work);
+int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix = false);
 int launch_attend(const AttendArgs &a, hipStream_t stream);
+// The same for the part of the common tokens, which with plan_attend(.., true)
+// makes a call of launch_attend_shared; the size grows with T.
+int64_t plan_prefix(AttendArgs *a, void *work);
+int launch_attend_shared(const AttendArgs &a, hipStream_t stream);
+int launch_rotate(const RotateArgs &a, hipStream_t stream);
+int launch_route(const RouteArgs &a, hipStream_t stream);
+// Fills in the launch (tiles, splits, rt) for up to kAdaptRows rows, and returns
+// the workspace's size in bytes.
+constexpr int kAdaptRows = 512, kAdaptSplits = 8;
+int64_t plan_adapt(AdaptArgs *a);
+int launch_adapt(const AdaptArgs &a, hipStream_t stream);
 int64_t plan_verify(VerifyArgs *a, void *work);  // slices and workspace alike
 int launch_verify(const VerifyArgs &a, hipStream_t stream);
 

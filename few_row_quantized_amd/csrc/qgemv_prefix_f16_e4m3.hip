@@ -1,0 +1,6 @@
+// Attention over a common prefix: float16 queries over an E4M3 cache.
+#include "qgemv_prefix_impl.h"
+
+namespace qgemv {
+int launch_shared_f16_e4m3(const AttendArgs &a, hipStream_t stream) { return launch_shared_t<false, true>(a, stream); }
+}  // namespace qgemv

@@ -1,0 +1,421 @@
+// Attention of all sequences' rows over the tokens that they have in common.
+//
+// A batch whose sequences begin with the same pages reads them once: the rows
+// of all sequences, T G of them for a key-value head, are one product against
+// the common tokens,
+//
+//   m = max_j s_j,  l = sum_j 2^(s_j - m),  o = sum_j 2^(s_j - m) v_j,
+//   s_j = scale * k_scale[h] * log2(e) * (q . k_j),
+//
+// which is joined with what each sequence's own tokens give (qgemv_attend_impl.h,
+// PRE).  4 R D flops for 4 D bytes of cache, R in the hundreds or thousands: the
+// matrix units bound it, not the memory.
+#pragma once
+
+#include "qgemv_attend_impl.h"
+
+namespace qgemv {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+template <bool BF>
+__device__ __forceinline__ f32x16_t mfma_32x32x16(u32x4_t a, u32x4_t b, f32x16_t c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                   c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                  0, 0, 0);
+}
+
+// Maximum / sum over the two lanes of a query row (lanes c and c + 32).
+__device__ __forceinline__ float pair_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                                  false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                                  false, false);
+  return __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+}
+
+// Tokens of a granule, and the LDS of a workgroup: keys and values of two.
+constexpr int prefix_tokens(int D) { return D == 256 ? 32 : 64; }
+constexpr int prefix_occupancy(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
+constexpr size_t kPrefixHead = 1024;  // positions of the rows, the reductions
+constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)4 * prefix_tokens(D) * D * 2; }
+
+// Where chunk `chunk` (8 values) of token `token` lies in a stage, so that lanes
+// of consecutive tokens that read one chunk each (keys), or 4 chunks of 4 tokens
+// (values), find them in different banks.
+template <int D>
+__device__ __forceinline__ int key_at(int token, int chunk) {
+  constexpr int C = D / 8;
+  return token * C + (chunk ^ (C == 8 ? token >> 1 & 7 : token & 15));
+}
+template <int D>
+__device__ __forceinline__ int value_at(int token, int chunk) {
+  constexpr int C = D / 8;
+  return token * C + (chunk ^ (C == 8 ? (token >> 1 & 1) * 4 : (token & 3) * 4));
+}
+
+template <bool BF, bool F8, int D>
+__global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(AttendArgs) {
+  constexpr int TOK = prefix_tokens(D), C = D / 8, TB = TOK / 32, DB = D / 32, QS = D / 16;
+  constexpr int L = TOK * C / 256;  // chunks of a thread, of keys and of values
+  constexpr int CB = F8 ? 1 : 2;
+  extern __shared__ __align__(16) uint8_t lds[];
+  int *const row_pos = reinterpret_cast<int *>(lds);        // [128] rows of T
+  int *const bounds = reinterpret_cast<int *>(lds + 512);   // smallest end, largest begin, strays, lowest position
+  u32x4_t *const stage = reinterpret_cast<u32x4_t *>(lds + kPrefixHead);  // [2][keys, values][TOK][C]
+
+  KernArgs *ap = kern_args();
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, half = lane >> 5;
+  const int common = common_pages<true>(*ap), before = common * ap->c.page;
+  const int G = ap->G, T = ap->T, R = T * G, B = ap->B;
+  const int window = ap->window ? ap->window : 1 << 30, sinks = ap->sinks;
+
+  // The first token that a row's window can reach: of the sequence with the
+  // lowest position.
+  int low = 0;
+  if (ap->window) {
+    if (tid == 0) bounds[3] = 0x7FFFFFFF;
+    __syncthreads();
+    int least = 0x7FFFFFFF;
+    for (int b = tid; b < B; b += 256) {
+      const int s0 = min(max(ap->start[b], 0), T), s1 = min(max(ap->start[b + 1], s0), T);
+      const int len = min(max(ap->len[b], 0), QGEMV_MAX_CONTEXT);
+      if (s1 > s0) least = min(least, len - (s1 - s0));
+    }
+    atomicMin(&bounds[3], least);
+    __syncthreads();
+    low = __builtin_amdgcn_readfirstlane(min(max(bounds[3] - window + 1, 0), before));
+  }
+  const int all = (before + TOK - 1) / TOK, low_tile = low / TOK;
+  const int sink_tiles = ap->window ? min((int)(((int64_t)sinks + TOK - 1) / TOK), low_tile) : 0;
+  const int n = sink_tiles + all - low_tile;
+  const int items = ap->pre_tiles * ap->c.H;
+  const int total = items * n;
+  const int per = max((total + ap->pre_workgroups - 1) / ap->pre_workgroups, 1);
+  if (blockIdx.x == 0 && tid == 0) {
+    ap->pre_plan[0] = n;
+    ap->pre_plan[1] = per;
+  }
+  // Workgroups of an XCD, which share its L2, walk neighbouring ranges.
+  int wg = blockIdx.x;
+  if (ap->pre_workgroups % 8 == 0) wg = (wg & 7) * (ap->pre_workgroups >> 3) + (wg >> 3);
+  int cur = wg * per;
+  const int end = min(cur + per, total);
+
+  while (cur < end) {
+    const int item = (int)((uint32_t)cur / (uint32_t)n), first = cur - item * n;
+    const int count = min(n - first, end - cur);
+    cur += count;
+    const int h = (int)((uint32_t)item / (uint32_t)ap->pre_tiles), tile0 = item - h * ap->pre_tiles;
+    const int r0 = tile0 * kPrefixRows;
+
+    // ---- positions of the item's rows
+    const int t0 = r0 / G, t1 = min((r0 + kPrefixRows - 1) / G + 1, T);
+    __syncthreads();
+    if (tid < 128) row_pos[tid] = 0x7FFFFFFF;  // a row of no sequence: sees what it likes, and is not read
+    if (tid == 0) {
+      bounds[0] = before;
+      bounds[1] = 0;
+      bounds[2] = 0;
+    }
+    __syncthreads();
+    for (int b = tid; b < B; b += 256) {
+      const int s0 = min(max(ap->start[b], 0), T), s1 = min(max(ap->start[b + 1], s0), T);
+      const int len = min(max(ap->len[b], 0), QGEMV_MAX_CONTEXT);
+      for (int t = max(s0, t0); t < min(s1, t1); ++t) row_pos[t - t0] = len - (s1 - t);
+    }
+    __syncthreads();
+    const int row = r0 + wave * 32 + c;
+    int hi = before, lo = 0;  // the row sees tokens below hi, of them those from lo on or below the sinks
+    if (row < R) {
+      const int pos = row_pos[row / G - t0];
+      if (pos != 0x7FFFFFFF) {
+        hi = min(before, pos + 1);
+        lo = max(pos - window + 1, 0);
+      }
+    }
+    atomicMin(&bounds[0], hi);
+    atomicMax(&bounds[1], lo);
+    __syncthreads();
+    const int least_hi = __builtin_amdgcn_readfirstlane(bounds[0]);
+    const int most_lo = __builtin_amdgcn_readfirstlane(bounds[1]);
+
+    const uint8_t *const kbase = ap->c.k + h * ap->c.stride_head;
+    const uint8_t *const vbase = ap->c.v + h * ap->c.stride_head;
+    const int32_t *const table = ap->c.table;
+    const int64_t stride_page = ap->c.stride_page, stride_slot = ap->c.stride_slot;
+    const int page = ap->c.page, pages = ap->c.pages, shift = ap->c.shift;
+    const uint32_t magic = ap->c.magic;
+    const float sc = ap->scale * (ap->c.k_scale ? constant(ap->c.k_scale)[h] : 1.0f) * kLog2e;
+
+    u32x4_t qf[QS];
+    {
+      const int at = min(row, R - 1), t = at / G, hq = h * G + at - t * G;
+      const uint8_t *q = ap->q + (int64_t)t * ap->q_row + hq * ap->q_head;
+#pragma unroll
+      for (int s = 0; s < QS; ++s) qf[s] = *reinterpret_cast<const u32x4_t *>(q + (s * 16 + half * 8) * 2);
+    }
+
+    auto tile_base = [&](int tile) { return (tile < sink_tiles ? tile : tile - sink_tiles + low_tile) * TOK; };
+    auto is_edge = [&](int tb, uint64_t present) {
+      constexpr uint64_t whole = TOK == 64 ? ~0ull : 0xFFFFFFFFull;
+      return (present != whole) | (tb + TOK > least_hi) | ((tb < most_lo) & (tb + TOK > sinks));
+    };
+    // a lane's token of a tile: its page's id; its place, 0 where it is not there
+    auto load_id = [&](int tile) -> int {
+      const int token = min(tile_base(tile) + (lane & (TOK - 1)), max(before - 1, 0));
+      return table[__umulhi(magic, 2 * token) >> shift];
+    };
+    auto place = [&](int tile, int id, uint64_t *present) -> int64_t {
+      const int token = tile_base(tile) + (lane & (TOK - 1));
+      const bool ok = ((uint32_t)id < (uint32_t)pages) & (tile < first + count) & (token < before);
+      const int in_page = token - (int)(__umulhi(magic, 2 * token) >> shift) * page;
+      const uint64_t mask = __ballot(ok);
+      *present = TOK == 64 ? mask : mask & 0xFFFFFFFFull;
+      return ok ? id * stride_page + in_page * stride_slot : 0;
+    };
+    u32x4_t kt[L], vt[L];
+    auto load_tile = [&](int64_t at) {
+      const int lo32 = (int)at, hi32 = (int)(at >> 32);
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int token = (i * 256 + tid) / C, chunk = tid % C;
+        const int64_t from = (int64_t)(uint32_t)__shfl(lo32, token) | (int64_t)__shfl(hi32, token) << 32;
+        const uint8_t *const k = kbase + from + chunk * (8 * CB), *const v = vbase + from + chunk * (8 * CB);
+        if constexpr (F8) {
+          const u32x2_t x = *reinterpret_cast<const u32x2_t *>(k), y = *reinterpret_cast<const u32x2_t *>(v);
+          kt[i][0] = x[0];
+          kt[i][1] = x[1];
+          vt[i][0] = y[0];
+          vt[i][1] = y[1];
+        } else {
+          kt[i] = *reinterpret_cast<const u32x4_t *>(k);
+          vt[i] = *reinterpret_cast<const u32x4_t *>(v);
+        }
+      }
+    };
+    auto widen = [](u32x4_t x) -> u32x4_t {
+      if constexpr (!F8) return x;
+      return u32x4_t{e4m3_pair<BF, false>(x[0]), e4m3_pair<BF, true>(x[0]), e4m3_pair<BF, false>(x[1]),
+                     e4m3_pair<BF, true>(x[1])};
+    };
+    // a tile's keys and values to a stage; where some row does not see some of
+    // its tokens, without the values that are not there, and without NaNs and
+    // infinities (0 times one is not 0): these are given to the rows that see
+    // them after the tiles
+    auto store_tile = [&](int buffer, bool edge, uint64_t present) {
+      u32x4_t *const ks = stage + buffer * (2 * TOK * C), *const vs = ks + TOK * C;
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int token = (i * 256 + tid) / C, chunk = tid % C;
+        ks[key_at<D>(token, chunk)] = widen(kt[i]);
+        u32x4_t v = widen(vt[i]);
+        if (edge) {
+          const uint32_t ok = 0u - (uint32_t)(present >> token & 1);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            v[x] &= ok;
+            odd |= nonfinite_signs<BF, false>(v[x]);
+            v[x] &= ~nonfinite<BF, false>(v[x]);
+          }
+        }
+        vs[value_at<D>(token, chunk)] = v;
+      }
+      if (edge && (odd & kSigns<false>) != 0) bounds[2] = 1;
+    };
+
+    int t = first;
+    const int t_end = first + count;
+    uint64_t there = 0, there_next = 0;
+    int id = load_id(t);
+    int id_next = load_id(t + 1);
+    int64_t at = place(t, id, &there);
+    load_tile(at);
+    store_tile(0, is_edge(tile_base(t), there), there);
+    at = place(t + 1, id_next, &there_next);
+    load_tile(at);
+    id = load_id(t + 2);
+    __syncthreads();
+
+    f32x16_t acc[DB];
+    float m = kNegInf, l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+
+    int buffer = 0;
+    for (; t < t_end; ++t) {
+      const u32x4_t *const ks = stage + buffer * (2 * TOK * C), *const vs = ks + TOK * C;
+      // ---- scores: lane (c, half) has row c, tokens 32 b + 8 (i / 4) + 4 half + i % 4
+      f32x16_t s[TB];
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+#pragma unroll
+      for (int st = 0; st < QS; ++st)
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+          s[b] = mfma_32x32x16<BF>(ks[key_at<D>(b * 32 + c, st * 2 + half)], qf[st], s[b]);
+      const int tb = tile_base(t);
+      const bool edge = is_edge(tb, there);
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] *= sc;
+      if (edge) {
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int o = b * 32 + 8 * (i / 4) + 4 * half + i % 4, j = tb + o;
+            const bool sees = ((there >> o & 1) != 0) & (j < hi) & ((j >= lo) | (j < sinks));
+            s[b][i] = sees ? s[b][i] : kNegInf;
+          }
+      }
+      // ---- weights
+      float top = s[0][0];
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+      top = pair_max(top);
+      // (a difference, which is exact: m + 8 would round where scores pass 2^25)
+      if (__any(top - m > 8.0f + kHeadroom<BF>)) {
+        const float mn = fmaxf(m, top - kHeadroom<BF>), f = weight_of(m, mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[d][i] *= f;
+      }
+      const float mm = m == kNegInf ? 0.0f : m;
+      float sum = 0.0f;
+      u32x4_t pf[2 * TB];
+#pragma unroll
+      for (int b = 0; b < TB; ++b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - mm);
+          sum += s[b][i];
+        }
+        // weights leave fp32 here, for the matrix product: half a step of q's
+        // type each, as in the attention over a sequence's own tokens
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) pf[b * 2 + u][x] = pair_of<BF>(s[b][u * 8 + x * 2], s[b][u * 8 + x * 2 + 1]);
+      }
+      l += sum;
+      // ---- values: a lane's operand is 8 tokens of one d, turned by the LDS
+#pragma unroll
+      for (int u = 0; u < 2 * TB; ++u)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          typedef __attribute__((address_space(3))) s16x4_t LdsQuad;
+          const int token = u * 16 + 4 * half + (lane & 15) / 4;
+          const int chunk = 4 * d + 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
+          uint8_t *const base = reinterpret_cast<uint8_t *>(const_cast<u32x4_t *>(vs)) + (lane & 1) * 8;
+          const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (LdsQuad *)(base + value_at<D>(token, chunk) * 16));
+          const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (LdsQuad *)(base + value_at<D>(token + 8, chunk) * 16));
+          const uint2 x2 = __builtin_bit_cast(uint2, x), y2 = __builtin_bit_cast(uint2, y);
+          acc[d] = mfma_32x32x16<BF>(u32x4_t{x2.x, x2.y, y2.x, y2.y}, pf[u], acc[d]);
+        }
+      // ---- the next tile
+      buffer ^= 1;
+      const int next = tile_base(t + 1);
+      store_tile(buffer, is_edge(next, there_next), there_next);
+      there = there_next;
+      at = place(t + 2, id, &there_next);
+      load_tile(at);
+      id = load_id(t + 3);
+      __syncthreads();
+    }
+
+    if (bounds[2]) {
+      // The NaNs and infinities of the tiles above, to the rows that see their
+      // tokens.
+#pragma unroll 1
+      for (int t2 = first; t2 < t_end; ++t2) {
+        uint64_t present;
+        const int64_t from = place(t2, load_id(t2), &present);
+        const int tb = tile_base(t2);
+        if (!is_edge(tb, present)) continue;
+#pragma unroll 1
+        for (int o = 0; o < TOK; ++o) {
+          if (!(present >> o & 1)) continue;
+          const int64_t at_o = (int64_t)(uint32_t)__shfl((int)from, o) | (int64_t)__shfl((int)(from >> 32), o) << 32;
+          const int j = tb + o;
+          uint32_t sees = (j < hi) & ((j >= lo) | (j < sinks)) ? ~0u : 0u;
+          asm volatile("" : "+v"(sees));  // a mask in a register, no branch for each value
+          const uint8_t *const p = vbase + at_o + 4 * half * CB;
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              uint32_t v[CB];
+              load_words<false, CB>(p + (d * 32 + 2 * i) * CB, v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                constexpr int PER = 4 / CB;
+                const uint32_t is = 0u - (nonfinite<BF, F8>(v[k / PER]) >> (k % PER * 8 * CB) & 1u);
+                const uint32_t x = __builtin_bit_cast(uint32_t, value_of<BF, F8>(v[k / PER], k % PER));
+                acc[d][i + k] += __builtin_bit_cast(float, x & is & sees);
+              }
+            }
+        }
+      }
+    }
+
+    // ---- write: lane (c, half) has row c and d = 32 b + 8 (i / 4) + 4 half + i % 4
+    l = pair_sum(l);
+    if (row < R) {
+      const int part = (int)((uint32_t)(item * n + first) / (uint32_t)per) - (int)((uint32_t)(item * n) / (uint32_t)per);
+      const int64_t to = ((int64_t)item * ap->pre_most + part) * kPrefixRows + wave * 32 + c;
+      float *const o = ap->pre_part + to * D;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f32x4_t *>(o + d * 32 + 2 * i + 4 * half) =
+              f32x4_t{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]};
+      if (half == 0) {
+        ap->pre_ml[to * 2] = m;
+        ap->pre_ml[to * 2 + 1] = l;
+      }
+    }
+  }
+}
+
+template <bool BF, bool F8, int D>
+int launch_prefix_d(const AttendArgs &a, hipStream_t stream) {
+  constexpr size_t bytes = prefix_lds(D);
+  const auto kern = prefix_kernel<BF, F8, D>;
+  if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
+  hipLaunchKernelGGL(kern, dim3(a.pre_workgroups), dim3(256), bytes, stream, a);
+  return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
+}
+
+template <bool BF, bool F8>
+int launch_shared_t(const AttendArgs &a, hipStream_t stream) {
+  const int s = a.c.D == 64 ? launch_prefix_d<BF, F8, 64>(a, stream)
+                : a.c.D == 128 ? launch_prefix_d<BF, F8, 128>(a, stream)
+                               : launch_prefix_d<BF, F8, 256>(a, stream);
+  return s == QGEMV_OK ? launch_attend_t<BF, F8, true>(a, stream) : s;
+}
+
+}  // namespace qgemv

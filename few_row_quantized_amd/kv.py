@@ -1,6 +1,8 @@
 """The verify step around the quantized products, on torch device tensors:
-appending the new rows' keys and values to a paged cache, attention of those
-rows over it, and acceptance of the drafted tokens.
+appending the new rows' keys and values to a paged cache, with the rotation of
+positions on the way or without, attention of those rows over it, also with a
+prompt that the sequences share, and acceptance of the drafted tokens; routing
+of rows to experts, and low-rank adapters beside a projection.
 
 Argument marshalling only, as in :mod:`few_row_quantized_amd.qgemv`, which
 offers these names: types, shapes and strides are checked (ValueError) by the
@@ -35,7 +37,8 @@ def _calls():
             raise RuntimeError(f"_qgemv_torch is not built ({e}); run `python -m few_row_quantized_amd.build`") from e
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.qgemv_kv_append, L.qgemv_kv_attend_workspace, L.qgemv_kv_attend, L.qgemv_verify_drafts_workspace,
-            L.qgemv_verify_drafts)), torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None)
+            L.qgemv_verify_drafts, L.qgemv_kv_attend_shared_workspace, L.qgemv_kv_attend_shared,
+            L.qgemv_kv_append_rotated, L.qgemv_route, L.qgemv_adapt_workspace, L.qgemv_adapt)), torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None)
         _module = m
     return _module
 
@@ -108,6 +111,26 @@ def append(cache: KvCache, new_k, new_v, start, len, stream=None) -> None:
         _q._check(status, "qgemv_kv_append")
 
 
+def append_rotated(cache: KvCache, q, new_k, new_v, start, len, freq, position=None, axes=None,
+                   interleaved: bool = False, out=None, stream=None):
+    """append() with positions turned on the way: the pairs of values of the
+    queries q [T, q_heads, dim] and of new_k (of one type, as new_v) by the angle
+    position * freq.  freq float32 [pairs], a multiple of 8 up to dim / 2; pair
+    i is the values i and pairs + i, with interleaved 2 i and 2 i + 1.  position
+    int32 [A, T], the rows' positions on A axes, and axes int32 [pairs], the
+    axis of each pair (the first unless given); without position a row's place
+    in its sequence.  Returns the turned queries: out, else a tensor of the
+    cache's type (bfloat16 for an 8-bit cache).  out may be q itself."""
+    if stream is not None and out is None and cache.k.is_cuda:
+        with _allocating(stream, cache.device):
+            return append_rotated(cache, q, new_k, new_v, start, len, freq, position, axes, interleaved)
+    r = _calls().append_rotated(cache._address, cache.k, q, new_k, new_v, start, len, freq, position, axes,
+                                interleaved, out, stream)
+    if type(r) is int:
+        _q._check(r, "qgemv_kv_append_rotated")
+    return r
+
+
 def attend_workspace(cache: KvCache, M: int, q_heads: int, T: int):
     """Scratch memory for attend() calls of up to M rows a sequence and T in
     all, of any window; one for each stream that runs them."""
@@ -129,6 +152,72 @@ def attend(cache: KvCache, q, start, len, M: int, window: int = 0, sinks: int = 
     r = _calls().attend(cache._address, cache.k, q, start, len, M, window, sinks, scale, out, lse, workspace, stream)
     if type(r) is int:
         _q._check(r, "qgemv_kv_attend")
+    return r
+
+
+def attend_shared_workspace(cache: KvCache, M: int, q_heads: int, T: int):
+    """Scratch memory for attend_shared() calls of up to M rows a sequence and T
+    in all, of any window; one for each stream that runs them."""
+    need = _q._check(_q.lib().qgemv_kv_attend_shared_workspace(cache._ref, M, q_heads, T),
+                     "qgemv_kv_attend_shared_workspace")
+    return torch.empty(need, dtype=torch.uint8, device=cache.device)
+
+
+def attend_shared(cache: KvCache, q, start, len, M: int, shared, window: int = 0, sinks: int = 0, scale=None,
+                  out=None, lse=None, workspace=None, stream=None):
+    """attend() for sequences whose first tokens, `shared` of them (int32 [1] on
+    the device), lie in the same pages of every sequence's table row: what they
+    have in common, in whole pages, is read once for all rows."""
+    if stream is not None and (out is None or workspace is None) and cache.k.is_cuda:
+        with _allocating(stream, cache.device):
+            return attend_shared(cache, q, start, len, M, shared, window, sinks, scale, out, lse, workspace)
+    r = _calls().attend_shared(cache._address, cache.k, q, start, len, shared, M, window, sinks, scale, out, lse,
+                               workspace, stream)
+    if type(r) is int:
+        _q._check(r, "qgemv_kv_attend_shared")
+    return r
+
+
+_SCORES = {"softmax": _q.SOFTMAX, "sigmoid": _q.SIGMOID}
+
+
+def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, keep: int = 1, best: int = 1,
+          renormalise: bool = True, scale: float = 1.0, stream=None):
+    """The k experts of each row of logits [T, E] and their weights: experts
+    int32 [T, k], -1 where fewer are there, and float32 [T, k].  score "softmax"
+    or "sigmoid"; bias float32 [E], added to the scores for the choice alone; of
+    `groups` groups of neighbours the `keep` with the greatest sums of their
+    `best` (1 or 2) greatest choices; weights over their sum unless renormalise
+    is false, times scale."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if stream is not None and logits.is_cuda:
+        with _allocating(stream, logits.device):
+            return route(logits, k, score, bias, groups, keep, best, renormalise, scale)
+    r = _calls().route(logits, k, _SCORES[score], bias, groups, keep, best, renormalise, scale, stream)
+    if type(r) is int:
+        _q._check(r, "qgemv_route")
+    return r
+
+
+def adapt_workspace(a, T: int):
+    """Scratch memory for adapt() calls of up to T rows with the adapters a (and
+    b) or others of their rank; one for each stream that runs them."""
+    need = _q._check(_q.lib().qgemv_adapt_workspace(T, a.shape[1]), "qgemv_adapt_workspace")
+    return torch.empty(need, dtype=torch.uint8, device=a.device)
+
+
+def adapt(y, x, a, b, adapter, scales=None, out=None, workspace=None, stream=None):
+    """y + scales * B (A x) of each row's adapter: y float32 [T, N], a product
+    of x [T, K]; a [n, r, K] and b [n, N, r] of x's type (bfloat16 or float16);
+    adapter int32 [T], none where outside [0, n); scales float32 [n].  Returns
+    out, else a new tensor; out may be y itself."""
+    if stream is not None and (out is None or workspace is None) and y.is_cuda:
+        with _allocating(stream, y.device):
+            return adapt(y, x, a, b, adapter, scales, out, workspace)
+    r = _calls().adapt(y, x, a, b, adapter, scales, out, workspace, stream)
+    if type(r) is int:
+        _q._check(r, "qgemv_adapt")
     return r
 
 

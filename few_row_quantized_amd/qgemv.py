@@ -44,6 +44,13 @@ MAX_GROUP = 64
 MAX_CONTEXT = 1 << 30
 MAX_VOCABULARY = 1 << 24
 
+SOFTMAX = 0
+SIGMOID = 1
+MAX_ROUTED = 1024
+MAX_GROUPS = 64
+MAX_CHOSEN = 64
+MAX_RANK = 256
+
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqgemv.so")
 
 _lib = None
@@ -98,9 +105,20 @@ def lib() -> ctypes.CDLL:
                                       ctypes.c_float, vp, i64, vp]
         L.qgemv_verify_drafts_workspace.argtypes = [i, i]
         L.qgemv_verify_drafts.argtypes = [vp, i64, vp, i64, i, vp, vp, vp, vp, vp, i, i, i, i, vp, i64, vp]
+        L.qgemv_kv_attend_shared_workspace.argtypes = [kv, i, i, i]
+        L.qgemv_kv_attend_shared.argtypes = [kv, vp, i64, i64, vp, i64, i64, i, vp, vp, vp, vp, i, i, i, i, i,
+                                             ctypes.c_float, vp, i64, vp]
+        L.qgemv_kv_append_rotated.argtypes = [kv, vp, i64, i64, i, vp, i64, i64, i, vp, i64, i64, vp, i64, i64, i,
+                                              vp, vp, i, vp, i, vp, i64, i, vp, i, vp]
+        L.qgemv_route.argtypes = [vp, i64, i, vp, vp, vp, i, i, i, i, i, i, i, i, ctypes.c_float, vp]
+        L.qgemv_adapt_workspace.argtypes = [i, i]
+        L.qgemv_adapt.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i, vp, vp, i, i, i, i, i, vp, i64, vp]
         L.qgemv_kv_attend_workspace.restype = i64
+        L.qgemv_kv_attend_shared_workspace.restype = i64
+        L.qgemv_adapt_workspace.restype = i64
         L.qgemv_verify_drafts_workspace.restype = i64
         for name in ("qgemv_kv_append", "qgemv_kv_attend", "qgemv_verify_drafts",
+                     "qgemv_kv_attend_shared", "qgemv_kv_append_rotated", "qgemv_route", "qgemv_adapt",
                      "qgemv_small", "qgemv_run_path", "qgemv_small_add", "qgemv_run_path_add",
                      "qgemv_small_fp", "qgemv_run_path_fp", "qgemv_select_fp", "qgemv_gather",
                      "qgemv_path_supported_fp", "qgemv_unpack_probe_fp",
@@ -283,7 +301,8 @@ def small(codes, scales, biases, x, bits: int, group_size: int, out=None, path="
 
 # ---------------------------------------------------------------- verify step around the products
 
-_KV = ("KvCache", "append", "attend", "attend_workspace", "verify", "verify_workspace")
+_KV = ("KvCache", "append", "append_rotated", "attend", "attend_workspace", "attend_shared",
+       "attend_shared_workspace", "verify", "verify_workspace", "route", "adapt", "adapt_workspace")
 
 
 def __getattr__(name):

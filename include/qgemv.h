@@ -409,6 +409,125 @@ int qgemv_kv_attend(const qgemv_kv_cache *cache, const void *q, int64_t q_row, i
                     int sinks, float scale, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
+ * qgemv_kv_attend_shared -- qgemv_kv_attend for sequences that begin with the
+ * same tokens in the same pages (a common prompt), whose keys and values are
+ * read once for all of them.
+ *   shared  int32 [1], DEVICE: how many tokens the sequences have in common.
+ *           Its whole pages, at most all of the table's but the last column,
+ *           are read through the first sequence's table row; the caller has
+ *           them in every row alike.  0 or less: none.  A length may end before
+ *           them.
+ * Other arguments, requirements and results as qgemv_kv_attend; rows of no
+ * sequence are left unwritten.  The two ways to compute a row agree within the
+ * roundings named there, not bit for bit.
+ *   workspace  qgemv_kv_attend_shared_workspace bytes: enough for every smaller
+ *           M and T and every window over the same cache.
+ * Besides the limits there, 2^30 rows times query heads on a key-value head and
+ * 2^30 pieces of the common part are too many (QGEMV_EUNSUPPORTED).
+ */
+int64_t qgemv_kv_attend_shared_workspace(const qgemv_kv_cache *cache, int M, int q_heads, int T);
+int qgemv_kv_attend_shared(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head,
+                           void *out, int64_t out_row, int64_t out_head, int q_dtype, float *lse,
+                           const int32_t *start, const int32_t *len, const int32_t *shared, int T, int M,
+                           int q_heads, int window, int sinks, float scale, void *workspace,
+                           int64_t workspace_bytes, void *stream);
+
+/*
+ * qgemv_kv_append_rotated -- qgemv_kv_append with the rotation of positions on
+ * the way, and the queries rotated for the attention after it:
+ *
+ *   angle(t, i) = p(t, axis(i)) * freq[i]                       0 <= i < pairs
+ *   (a, b) -> (a cos angle - b sin angle, a sin angle + b cos angle)
+ *
+ * of the pairs of each query and key: values i and pairs + i of a head, or with
+ * interleaved 2 i and 2 i + 1; a head's values from 2 * pairs on, and all of
+ * new_v, stay.
+ *   q       [T][q_heads][dim] of src_dtype; out the same of out_dtype
+ *           (QGEMV_BF16 or QGEMV_F16): q itself (same type and strides), or
+ *           apart from it (QGEMV_EINVAL).  Rows of no sequence are left
+ *           unwritten.
+ *   freq    fp32 [pairs], DEVICE; pairs a multiple of 8, at most dim / 2.
+ *   position  int32 [axes][T], DEVICE, axes position_axis elements apart: the
+ *           rows' positions on each axis; NULL: one axis, a row's place in its
+ *           sequence.
+ *   axis    int32 [pairs], DEVICE, limited to 0 .. axes - 1: the axis of each
+ *           pair; NULL: the first.  NULL where position is.
+ * Angles are fp64, cos and sin fp32 (within 2^-22), a rotated value is rounded
+ * to fp32 and then once to its type.  Other arguments, requirements and
+ * errors as qgemv_kv_append.
+ */
+int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head, int q_heads,
+                            void *out, int64_t out_row, int64_t out_head, int out_dtype, const void *new_k,
+                            int64_t k_row, int64_t k_head, const void *new_v, int64_t v_row, int64_t v_head,
+                            int src_dtype, const int32_t *start, const int32_t *len, int T, const float *freq,
+                            int pairs, const int32_t *position, int64_t position_axis, int axes,
+                            const int32_t *axis, int interleaved, void *stream);
+
+/*
+ * qgemv_route -- the experts of each row and their weights; experts [T * k] is
+ * what qgemv_gather takes as e_idx.
+ *
+ *   score_e  = exp(x_e) / sum exp(x)  (QGEMV_SOFTMAX)  or  1 / (1 + exp(-x_e))
+ *   choice_e = score_e + bias_e
+ *
+ * The E experts make `groups` groups of neighbours.  Of these the `keep` whose
+ * `best` (1 or 2) greatest choices have the greatest sum remain, and of their
+ * experts the k of greatest choice, in that order; equal ones by their number.
+ * weights are scale times the scores (without the bias), with renormalise over
+ * their sum (0 where that is 0).
+ *   logits  [T][E] of QGEMV_F32, QGEMV_BF16 or QGEMV_F16, row stride `row`
+ *           elements.  An expert whose logit is -inf or NaN, or whose choice
+ *           is, is not there: it has no part in the softmax (its logit) and is
+ *           not chosen, nor is a group of such.  Where fewer than k are there,
+ *           the list ends with -1 (which qgemv_gather skips) and weight 0.  A
+ *           logit of +inf leaves a row's softmax without values: weights NaN.
+ *   bias    fp32 [E], DEVICE, or NULL.
+ * Scores and choices are fp64; without a bias and with best = 1 the choice is
+ * by the logits themselves, which their scores' order is.  Deterministic.
+ * At most QGEMV_MAX_ROUTED experts, QGEMV_MAX_GROUPS groups, k of
+ * QGEMV_MAX_CHOSEN (QGEMV_EUNSUPPORTED) and of the experts of `keep` groups
+ * (QGEMV_EINVAL); 2^24 rows are too many.
+ */
+#define QGEMV_SOFTMAX 0
+#define QGEMV_SIGMOID 1
+#define QGEMV_MAX_ROUTED 1024
+#define QGEMV_MAX_GROUPS 64
+#define QGEMV_MAX_CHOSEN 64
+int qgemv_route(const void *logits, int64_t row, int dtype, const float *bias, int32_t *experts, float *weights,
+                int T, int E, int k, int score, int groups, int keep, int best, int renormalise, float scale,
+                void *stream);
+
+/*
+ * qgemv_adapt -- low-rank adapters of many requests beside a shared projection:
+ *
+ *   out[t] = y[t] + scales[a] * B[a] (A[a] x[t]),   a = adapter[t]
+ *
+ *   y, out  fp32 [T][N], row strides in elements, 4-byte aligned: a product's
+ *           output, or columns of it.  out may be y itself (rows without an
+ *           adapter are then not touched), otherwise it must not overlap it.
+ *   x       [T][K] of QGEMV_BF16 or QGEMV_F16, the product's activations, row
+ *           stride a multiple of 8 elements.
+ *   a, b    [n][r][K] and [n][N][r] of the same type, packed: the adapters.  K
+ *           and r multiples of 8, r at most QGEMV_MAX_RANK; an adapter of
+ *           lower rank is one with rows and columns of zeros.
+ *   adapter int32 [T], DEVICE: each row's, or none where outside [0, n).
+ *   scales  fp32 [n], DEVICE, or NULL: 1.
+ *   workspace  qgemv_adapt_workspace bytes, 16-byte aligned, contents free;
+ *           enough for every smaller T and r; not shared by calls that may run
+ *           at the same time.
+ * x, a, b 16-byte aligned.  Products of 16-bit values are summed in fp32; the
+ * rank's sums enter the second product as two 16-bit parts (a relative error of
+ * 2^-17 of each in bf16, in fp16 2^-23 of the row's largest).  Deterministic, and
+ * a row's result does not depend on the other rows' values.  2^24 rows are
+ * too many.
+ */
+#define QGEMV_MAX_RANK 256
+int64_t qgemv_adapt_workspace(int T, int r);
+int qgemv_adapt(const float *y, int64_t y_row, float *out, int64_t out_row, const void *x, int64_t x_row,
+                const void *a, const void *b, int dtype, const int32_t *adapter, const float *scales, int T, int n,
+                int r, int K, int N, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * qgemv_verify_drafts -- which drafted tokens of each sequence are accepted,
  * and the token after them.
  *   p       [T][V] target probabilities after row t (QGEMV_F32, QGEMV_BF16 or

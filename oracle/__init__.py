@@ -29,3 +29,8 @@ from .kv_oracle import (  # noqa: F401
     verify_weights,
     visible,
 )
+from .step_oracle import (  # noqa: F401
+    adapt_reference,
+    rotate_reference,
+    route_reference,
+)
