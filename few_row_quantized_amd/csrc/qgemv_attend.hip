@@ -80,7 +80,9 @@ int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix) {
 
 int64_t plan_prefix(AttendArgs *a, void *work) {
   const int D = a->c.D, tokens = prefix_tokens(D);
-  const int64_t rows = (int64_t)a->T * a->G, tiles = (rows + kPrefixRows - 1) / kPrefixRows;
+  const int64_t rows = (int64_t)a->T * a->G;
+  a->pre_rows = 128;
+  const int64_t tiles = (rows + a->pre_rows - 1) / a->pre_rows;
   const int64_t items = tiles * a->c.H;
   // what the table can have in common: all of it but each sequence's last page
   const int64_t granules = std::max<int64_t>(1, ((int64_t)a->c.page * (a->c.width - 1) + tokens - 1) / tokens);
@@ -93,8 +95,9 @@ int64_t plan_prefix(AttendArgs *a, void *work) {
   a->pre_workgroups = (int)workgroups;
   a->pre_most = items ? (int)(workgroups / items) + 2 : 0;
   const auto up = [](int64_t n) { return (n + 255) & ~(int64_t)255; };
-  // items * pre_most is at most this, which grows with T
-  const int64_t parts = (slots + 2 * items) * kPrefixRows;
+  // items * pre_most is at most workgroups + 2 items: so much in units that grow
+  // with T, whatever rows the call takes together
+  const int64_t parts = (2 * (int64_t)device_cu_count() + 2 * items) * a->pre_rows;
   uint8_t *p = static_cast<uint8_t *>(work);
   a->pre_plan = reinterpret_cast<int32_t *>(p);
   a->pre_ml = reinterpret_cast<float *>(p + 256);

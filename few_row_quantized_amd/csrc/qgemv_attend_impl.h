@@ -973,10 +973,9 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   }
 }
 
-// The parts of the common tokens (qgemv_prefix_impl.h): an item is 128 rows of a
-// head of all the call's, and has n granules; workgroups take per of them each.
-constexpr int kPrefixRows = 128;
-
+// The parts of the common tokens (qgemv_prefix_impl.h): an item is 128 or 256 rows
+// of a head of all the call's, and has n granules; workgroups take per of them
+// each.
 struct PrefixPlan {
   int n, per;
   int most;  // parts that an item can have
@@ -994,10 +993,10 @@ __device__ __forceinline__ PrefixPlan prefix_plan(Args &a) {
 // Where part `i` of a row is; below 0 if it has fewer.
 template <class Args>
 __device__ __forceinline__ int64_t prefix_part(Args &a, const PrefixPlan &p, int h, int row, int i) {
-  const int item = h * a.pre_tiles + row / kPrefixRows;
+  const int item = h * a.pre_tiles + row / a.pre_rows;
   const uint32_t g0 = (uint32_t)item * (uint32_t)p.n;
   if (i > (int)((g0 + p.n - 1) / p.per - g0 / p.per)) return -1;
-  return ((int64_t)item * a.pre_most + i) * kPrefixRows + row % kPrefixRows;
+  return ((int64_t)item * a.pre_most + i) * a.pre_rows + row % a.pre_rows;
 }
 
 // Joins the parts of the items that several workgroups shared.  A team of D / 4

@@ -71,9 +71,10 @@ struct AttendArgs {
   // attention over a common prefix (qgemv_prefix_impl.h)
   const int32_t *common;  // its tokens, or null
   int32_t *pre_plan;      // granules of an item, granules of a workgroup
-  float *pre_ml;          // [items][pre_most][128][2]
-  float *pre_part;        // [items][pre_most][128][D]
-  int pre_tiles;          // items of a head: groups of 128 rows of all
+  float *pre_ml;          // [items][pre_most][pre_rows][2]
+  float *pre_part;        // [items][pre_most][pre_rows][D]
+  int pre_rows;           // rows of an item
+  int pre_tiles;          // items of a head: groups of so many rows of all
   int pre_workgroups, pre_most;
 };
 

@@ -41,8 +41,20 @@ __device__ __forceinline__ float pair_sum(float x) {
   return __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
 }
 
+// The smallest of a wave's values, in all lanes.
+__device__ __forceinline__ int wave_least(int x) {
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x111, 0xF, 0xF, false));
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x112, 0xF, 0xF, false));
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x114, 0xF, 0xF, false));
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x118, 0xF, 0xF, false));
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x142, 0xA, 0xF, false));
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x143, 0xC, 0xF, false));
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
 // Tokens of a granule, and the LDS of a workgroup: keys and values of two.
 constexpr int prefix_tokens(int D) { return D == 256 ? 32 : 64; }
+constexpr int kPrefixRows = 128;  // of an item
 constexpr int prefix_occupancy(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
 constexpr size_t kPrefixHead = 1024;  // positions of the rows, the reductions
 constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)4 * prefix_tokens(D) * D * 2; }
@@ -68,7 +80,7 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
   constexpr int CB = F8 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t lds[];
   int *const row_pos = reinterpret_cast<int *>(lds);        // [128] rows of T
-  int *const bounds = reinterpret_cast<int *>(lds + 512);   // smallest end, largest begin, strays, lowest position
+  int *const bounds = reinterpret_cast<int *>(lds + 512);   // of each wave: smallest end, largest begin; then strays
   u32x4_t *const stage = reinterpret_cast<u32x4_t *>(lds + kPrefixHead);  // [2][keys, values][TOK][C]
 
   KernArgs *ap = kern_args();
@@ -83,17 +95,16 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
   // lowest position.
   int low = 0;
   if (ap->window) {
-    if (tid == 0) bounds[3] = 0x7FFFFFFF;
-    __syncthreads();
     int least = 0x7FFFFFFF;
     for (int b = tid; b < B; b += 256) {
       const int s0 = min(max(ap->start[b], 0), T), s1 = min(max(ap->start[b + 1], s0), T);
       const int len = min(max(ap->len[b], 0), QGEMV_MAX_CONTEXT);
       if (s1 > s0) least = min(least, len - (s1 - s0));
     }
-    atomicMin(&bounds[3], least);
+    bounds[wave] = wave_least(least);
     __syncthreads();
-    low = __builtin_amdgcn_readfirstlane(min(max(bounds[3] - window + 1, 0), before));
+    least = min(min(bounds[0], bounds[1]), min(bounds[2], bounds[3]));
+    low = __builtin_amdgcn_readfirstlane(min(max(least - window + 1, 0), before));
   }
   const int all = (before + TOK - 1) / TOK, low_tile = low / TOK;
   const int sink_tiles = ap->window ? min((int)(((int64_t)sinks + TOK - 1) / TOK), low_tile) : 0;
@@ -116,38 +127,7 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
     const int count = min(n - first, end - cur);
     cur += count;
     const int h = (int)((uint32_t)item / (uint32_t)ap->pre_tiles), tile0 = item - h * ap->pre_tiles;
-    const int r0 = tile0 * kPrefixRows;
-
-    // ---- positions of the item's rows
-    const int t0 = r0 / G, t1 = min((r0 + kPrefixRows - 1) / G + 1, T);
-    __syncthreads();
-    if (tid < 128) row_pos[tid] = 0x7FFFFFFF;  // a row of no sequence: sees what it likes, and is not read
-    if (tid == 0) {
-      bounds[0] = before;
-      bounds[1] = 0;
-      bounds[2] = 0;
-    }
-    __syncthreads();
-    for (int b = tid; b < B; b += 256) {
-      const int s0 = min(max(ap->start[b], 0), T), s1 = min(max(ap->start[b + 1], s0), T);
-      const int len = min(max(ap->len[b], 0), QGEMV_MAX_CONTEXT);
-      for (int t = max(s0, t0); t < min(s1, t1); ++t) row_pos[t - t0] = len - (s1 - t);
-    }
-    __syncthreads();
-    const int row = r0 + wave * 32 + c;
-    int hi = before, lo = 0;  // the row sees tokens below hi, of them those from lo on or below the sinks
-    if (row < R) {
-      const int pos = row_pos[row / G - t0];
-      if (pos != 0x7FFFFFFF) {
-        hi = min(before, pos + 1);
-        lo = max(pos - window + 1, 0);
-      }
-    }
-    atomicMin(&bounds[0], hi);
-    atomicMax(&bounds[1], lo);
-    __syncthreads();
-    const int least_hi = __builtin_amdgcn_readfirstlane(bounds[0]);
-    const int most_lo = __builtin_amdgcn_readfirstlane(bounds[1]);
+    const int r0 = tile0 * kPrefixRows, row = r0 + wave * 32 + c;
 
     const uint8_t *const kbase = ap->c.k + h * ap->c.stride_head;
     const uint8_t *const vbase = ap->c.v + h * ap->c.stride_head;
@@ -155,8 +135,20 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
     const int64_t stride_page = ap->c.stride_page, stride_slot = ap->c.stride_slot;
     const int page = ap->c.page, pages = ap->c.pages, shift = ap->c.shift;
     const uint32_t magic = ap->c.magic;
-    const float sc = ap->scale * (ap->c.k_scale ? constant(ap->c.k_scale)[h] : 1.0f) * kLog2e;
+    const float signed_sc = ap->scale * (ap->c.k_scale ? constant(ap->c.k_scale)[h] : 1.0f) * kLog2e;
 
+    // ---- the first tiles' page ids and the queries, on their way while the
+    // rows' positions are found.  The queries take the scale's sign (and are 0
+    // where it is 0), so that the largest product has the largest score.
+    auto tile_base = [&](int tile) { return (tile < sink_tiles ? tile : tile - sink_tiles + low_tile) * TOK; };
+    // the page id of a lane's token
+    auto load_id = [&](int tile) -> int {
+      const int token = min(tile_base(tile) + (lane & (TOK - 1)), max(before - 1, 0));
+      return table[__umulhi(magic, 2 * token) >> shift];
+    };
+    int t = first;
+    const int t_end = first + count;
+    int id = load_id(t), id_next = load_id(t + 1);
     u32x4_t qf[QS];
     {
       const int at = min(row, R - 1), t = at / G, hq = h * G + at - t * G;
@@ -165,16 +157,43 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
       for (int s = 0; s < QS; ++s) qf[s] = *reinterpret_cast<const u32x4_t *>(q + (s * 16 + half * 8) * 2);
     }
 
-    auto tile_base = [&](int tile) { return (tile < sink_tiles ? tile : tile - sink_tiles + low_tile) * TOK; };
+    // ---- positions of the item's rows
+    const int t0 = r0 / G, t1 = min((r0 + kPrefixRows - 1) / G + 1, T);
+    __syncthreads();
+    if (tid < 128) row_pos[tid] = 0x7FFFFFFF;  // a row of no sequence: sees what it likes, and is not read
+    if (tid == 0) bounds[8] = 0;
+    __syncthreads();
+    for (int b = tid; b < B; b += 256) {
+      const int s0 = min(max(ap->start[b], 0), T), s1 = min(max(ap->start[b + 1], s0), T);
+      const int len = min(max(ap->len[b], 0), QGEMV_MAX_CONTEXT);
+      for (int t = max(s0, t0); t < min(s1, t1); ++t) row_pos[t - t0] = len - (s1 - t);
+    }
+    __syncthreads();
+    int hi = before, lo = 0;  // the row sees tokens below hi, of them those from lo on or below the sinks
+    if (row < R) {
+      const int pos = row_pos[row / G - t0];
+      if (pos != 0x7FFFFFFF) {
+        hi = min(before, pos + 1);
+        lo = max(pos - window + 1, 0);
+      }
+    }
+    bounds[wave] = wave_least(hi);
+    bounds[4 + wave] = -wave_least(-lo);
+    __syncthreads();
+    const int least_hi = __builtin_amdgcn_readfirstlane(min(min(bounds[0], bounds[1]), min(bounds[2], bounds[3])));
+    const int most_lo = __builtin_amdgcn_readfirstlane(max(max(bounds[4], bounds[5]), max(bounds[6], bounds[7])));
+    const float sc = signed_sc == 0.0f ? 1.0f : __builtin_fabsf(signed_sc);
+    {
+      const uint32_t flip = signed_sc < 0.0f ? 0x80008000u : 0u, keep = signed_sc == 0.0f ? 0u : ~0u;
+#pragma unroll
+      for (int s = 0; s < QS; ++s) qf[s] = (qf[s] ^ flip) & keep;
+    }
+
     auto is_edge = [&](int tb, uint64_t present) {
       constexpr uint64_t whole = TOK == 64 ? ~0ull : 0xFFFFFFFFull;
       return (present != whole) | (tb + TOK > least_hi) | ((tb < most_lo) & (tb + TOK > sinks));
     };
-    // a lane's token of a tile: its page's id; its place, 0 where it is not there
-    auto load_id = [&](int tile) -> int {
-      const int token = min(tile_base(tile) + (lane & (TOK - 1)), max(before - 1, 0));
-      return table[__umulhi(magic, 2 * token) >> shift];
-    };
+    // a lane's place of a tile's token, 0 where it is not there
     auto place = [&](int tile, int id, uint64_t *present) -> int64_t {
       const int token = tile_base(tile) + (lane & (TOK - 1));
       const bool ok = ((uint32_t)id < (uint32_t)pages) & (tile < first + count) & (token < before);
@@ -231,14 +250,10 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
         }
         vs[value_at<D>(token, chunk)] = v;
       }
-      if (edge && (odd & kSigns<false>) != 0) bounds[2] = 1;
+      if (edge && (odd & kSigns<false>) != 0) bounds[8] = 1;
     };
 
-    int t = first;
-    const int t_end = first + count;
     uint64_t there = 0, there_next = 0;
-    int id = load_id(t);
-    int id_next = load_id(t + 1);
     int64_t at = place(t, id, &there);
     load_tile(at);
     store_tile(0, is_edge(tile_base(t), there), there);
@@ -263,24 +278,26 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
       for (int b = 0; b < TB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+      int ln = lane;
+      asm volatile("" : "+v"(ln));  // places computed anew for each tile, not kept in registers
 #pragma unroll
       for (int st = 0; st < QS; ++st)
 #pragma unroll
         for (int b = 0; b < TB; ++b)
-          s[b] = mfma_32x32x16<BF>(ks[key_at<D>(b * 32 + c, st * 2 + half)], qf[st], s[b]);
+          s[b] = mfma_32x32x16<BF>(ks[key_at<D>(b * 32 + (ln & 31), st * 2 + (ln >> 5))], qf[st], s[b]);
       const int tb = tile_base(t);
       const bool edge = is_edge(tb, there);
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] *= sc;
       if (edge) {
+        int from = 4 * half;  // the lane's first token
+        asm volatile("" : "+v"(from));
+        const uint64_t mine = there >> from;
+        const int j0 = tb + from;
 #pragma unroll
         for (int b = 0; b < TB; ++b)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int o = b * 32 + 8 * (i / 4) + 4 * half + i % 4, j = tb + o;
-            const bool sees = ((there >> o & 1) != 0) & (j < hi) & ((j >= lo) | (j < sinks));
+            const int o = b * 32 + 8 * (i / 4) + i % 4;
+            const bool sees = ((mine >> o & 1) != 0) & (o < hi - j0) & ((o >= lo - j0) | (o < sinks - j0));
             s[b][i] = sees ? s[b][i] : kNegInf;
           }
       }
@@ -290,7 +307,7 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
       for (int b = 0; b < TB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-      top = pair_max(top);
+      top = pair_max(top) * sc;
       // (a difference, which is exact: m + 8 would round where scores pass 2^25)
       if (__any(top - m > 8.0f + kHeadroom<BF>)) {
         const float mn = fmaxf(m, top - kHeadroom<BF>), f = weight_of(m, mn);
@@ -308,7 +325,7 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
       for (int b = 0; b < TB; ++b) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - mm);
+          s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], sc, -mm));
           sum += s[b][i];
         }
         // weights leave fp32 here, for the matrix product: half a step of q's
@@ -325,9 +342,9 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
           typedef __attribute__((address_space(3))) s16x4_t LdsQuad;
-          const int token = u * 16 + 4 * half + (lane & 15) / 4;
-          const int chunk = 4 * d + 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
-          uint8_t *const base = reinterpret_cast<uint8_t *>(const_cast<u32x4_t *>(vs)) + (lane & 1) * 8;
+          const int token = u * 16 + 4 * (ln >> 5) + (ln & 15) / 4;
+          const int chunk = 4 * d + 2 * (ln >> 4 & 1) + (ln >> 1 & 1);
+          uint8_t *const base = reinterpret_cast<uint8_t *>(const_cast<u32x4_t *>(vs)) + (ln & 1) * 8;
           const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
               (LdsQuad *)(base + value_at<D>(token, chunk) * 16));
           const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -346,7 +363,7 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
       __syncthreads();
     }
 
-    if (bounds[2]) {
+    if (bounds[8]) {
       // The NaNs and infinities of the tiles above, to the rows that see their
       // tokens.
 #pragma unroll 1
