@@ -79,9 +79,9 @@ int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix) {
 }
 
 int64_t plan_prefix(AttendArgs *a, void *work) {
-  const int D = a->c.D, tokens = prefix_tokens(D);
+  const int D = a->c.D, tokens = kPrefixTokens;
   const int64_t rows = (int64_t)a->T * a->G;
-  a->pre_rows = 128;
+  a->pre_rows = kPrefixRows;
   const int64_t tiles = (rows + a->pre_rows - 1) / a->pre_rows;
   const int64_t items = tiles * a->c.H;
   // what the table can have in common: all of it but each sequence's last page

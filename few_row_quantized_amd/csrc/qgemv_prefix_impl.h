@@ -52,36 +52,30 @@ __device__ __forceinline__ int wave_least(int x) {
   return __builtin_amdgcn_readlane(x, 63);
 }
 
-// Tokens of a granule, and the LDS of a workgroup: keys and values of two.
-constexpr int prefix_tokens(int D) { return D == 256 ? 32 : 64; }
-constexpr int kPrefixRows = 128;  // of an item
+constexpr int kPrefixRows = 128;   // of an item: 32 a wave
+constexpr int kPrefixTokens = 64;  // of a granule
 constexpr int prefix_occupancy(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
-constexpr size_t kPrefixHead = 1024;  // positions of the rows, the reductions
-constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)4 * prefix_tokens(D) * D * 2; }
 
-// Where chunk `chunk` (8 values) of token `token` lies in a stage, so that lanes
-// of consecutive tokens that read one chunk each (keys), or 4 chunks of 4 tokens
-// (values), find them in different banks.
-template <int D>
-__device__ __forceinline__ int key_at(int token, int chunk) {
-  constexpr int C = D / 8;
-  return token * C + (chunk ^ (C == 8 ? token >> 1 & 7 : token & 15));
-}
-template <int D>
-__device__ __forceinline__ int value_at(int token, int chunk) {
-  constexpr int C = D / 8;
-  return token * C + (chunk ^ (C == 8 ? (token >> 1 & 1) * 4 : (token & 3) * 4));
-}
+// LDS of a workgroup: positions of the rows and the reductions, then keys of two
+// tiles and values of two.  Rows are padded, so that lanes of consecutive tokens
+// that read one chunk of 16 bytes each (keys), or 64 bytes of 4 tokens (values),
+// find them in different banks, at distances that a load's offset can hold.
+constexpr int kPrefixHead = 1024 + 4096;  // the latter: each wave's places of two tiles' tokens
+constexpr int key_row(int D) { return 2 * D + 16; }
+constexpr int value_row(int D) { return 2 * D + 64; }
+constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)2 * kPrefixTokens * (key_row(D) + value_row(D)); }
 
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(AttendArgs) {
-  constexpr int TOK = prefix_tokens(D), C = D / 8, TB = TOK / 32, DB = D / 32, QS = D / 16;
+  constexpr int TOK = kPrefixTokens, C = D / 8, DB = D / 32, QS = D / 16;
   constexpr int L = TOK * C / 256;  // chunks of a thread, of keys and of values
+  constexpr int KR = key_row(D), VR = value_row(D);
   constexpr int CB = F8 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t lds[];
   int *const row_pos = reinterpret_cast<int *>(lds);        // [128] rows of T
   int *const bounds = reinterpret_cast<int *>(lds + 512);   // of each wave: smallest end, largest begin; then strays
-  u32x4_t *const stage = reinterpret_cast<u32x4_t *>(lds + kPrefixHead);  // [2][keys, values][TOK][C]
+  int64_t *const ring = reinterpret_cast<int64_t *>(lds + 1024) + (threadIdx.x >> 6) * 128;
+  uint8_t *const keys = lds + kPrefixHead, *const values = keys + 2 * TOK * KR;
 
   KernArgs *ap = kern_args();
   const int tid = threadIdx.x, lane = tid & 63;
@@ -143,7 +137,7 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
     auto tile_base = [&](int tile) { return (tile < sink_tiles ? tile : tile - sink_tiles + low_tile) * TOK; };
     // the page id of a lane's token
     auto load_id = [&](int tile) -> int {
-      const int token = min(tile_base(tile) + (lane & (TOK - 1)), max(before - 1, 0));
+      const int token = min(tile_base(tile) + lane, max(before - 1, 0));
       return table[__umulhi(magic, 2 * token) >> shift];
     };
     int t = first;
@@ -190,35 +184,36 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
     }
 
     auto is_edge = [&](int tb, uint64_t present) {
-      constexpr uint64_t whole = TOK == 64 ? ~0ull : 0xFFFFFFFFull;
-      return (present != whole) | (tb + TOK > least_hi) | ((tb < most_lo) & (tb + TOK > sinks));
+      return (present != ~0ull) | (tb + TOK > least_hi) | ((tb < most_lo) & (tb + TOK > sinks));
     };
-    // a lane's place of a tile's token, 0 where it is not there
-    auto place = [&](int tile, int id, uint64_t *present) -> int64_t {
-      const int token = tile_base(tile) + (lane & (TOK - 1));
+    // a lane's place of a tile's token into the ring, 0 where it is not there
+    auto put = [&](int tile, int id) -> uint64_t {
+      const int token = tile_base(tile) + lane;
       const bool ok = ((uint32_t)id < (uint32_t)pages) & (tile < first + count) & (token < before);
       const int in_page = token - (int)(__umulhi(magic, 2 * token) >> shift) * page;
-      const uint64_t mask = __ballot(ok);
-      *present = TOK == 64 ? mask : mask & 0xFFFFFFFFull;
-      return ok ? id * stride_page + in_page * stride_slot : 0;
+      ring[(tile & 1) * 64 + lane] = ok ? id * stride_page + in_page * stride_slot : 0;
+      // a wave's LDS accesses stay in order; this keeps the compiler from moving them
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      return __ballot(ok);
     };
+    // A thread's share of a tile's keys, and of another's values, on their way: its
+    // chunk of 8 values of every (256 / C)th token.
     u32x4_t kt[L], vt[L];
-    auto load_tile = [&](int64_t at) {
-      const int lo32 = (int)at, hi32 = (int)(at >> 32);
+    typedef int64_t Places[L];
+    auto look_up = [&](int tile, Places &to) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) to[i] = ring[(tile & 1) * 64 + i * (256 / C) + tid / C];
+    };
+    auto load_rows = [&](const uint8_t *from, const Places &at, u32x4_t (&to)[L]) {
 #pragma unroll
       for (int i = 0; i < L; ++i) {
-        const int token = (i * 256 + tid) / C, chunk = tid % C;
-        const int64_t from = (int64_t)(uint32_t)__shfl(lo32, token) | (int64_t)__shfl(hi32, token) << 32;
-        const uint8_t *const k = kbase + from + chunk * (8 * CB), *const v = vbase + from + chunk * (8 * CB);
+        const uint8_t *const p = from + tid % C * (8 * CB) + at[i];
         if constexpr (F8) {
-          const u32x2_t x = *reinterpret_cast<const u32x2_t *>(k), y = *reinterpret_cast<const u32x2_t *>(v);
-          kt[i][0] = x[0];
-          kt[i][1] = x[1];
-          vt[i][0] = y[0];
-          vt[i][1] = y[1];
+          const u32x2_t x = *reinterpret_cast<const u32x2_t *>(p);
+          to[i][0] = x[0];
+          to[i][1] = x[1];
         } else {
-          kt[i] = *reinterpret_cast<const u32x4_t *>(k);
-          vt[i] = *reinterpret_cast<const u32x4_t *>(v);
+          to[i] = *reinterpret_cast<const u32x4_t *>(p);
         }
       }
     };
@@ -227,40 +222,36 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
       return u32x4_t{e4m3_pair<BF, false>(x[0]), e4m3_pair<BF, true>(x[0]), e4m3_pair<BF, false>(x[1]),
                      e4m3_pair<BF, true>(x[1])};
     };
-    // a tile's keys and values to a stage; where some row does not see some of
-    // its tokens, without the values that are not there, and without NaNs and
-    // infinities (0 times one is not 0): these are given to the rows that see
-    // them after the tiles
-    auto store_tile = [&](int buffer, bool edge, uint64_t present) {
-      u32x4_t *const ks = stage + buffer * (2 * TOK * C), *const vs = ks + TOK * C;
-      uint32_t odd = 0;
+    auto store_keys = [&](int tile, const u32x4_t (&from)[L]) {
+      uint8_t *const to = keys + (tile & 1) * (TOK * KR) + tid / C * KR + tid % C * 16;
 #pragma unroll
-      for (int i = 0; i < L; ++i) {
-        const int token = (i * 256 + tid) / C, chunk = tid % C;
-        ks[key_at<D>(token, chunk)] = widen(kt[i]);
-        u32x4_t v = widen(vt[i]);
-        if (edge) {
-          const uint32_t ok = 0u - (uint32_t)(present >> token & 1);
+      for (int i = 0; i < L; ++i) *reinterpret_cast<u32x4_t *>(to + i * (256 / C) * KR) = widen(from[i]);
+    };
+    // Where some row does not see some of a tile's tokens: without the values that
+    // are not there, and without NaNs and infinities (0 times one is not 0), which
+    // are given to the rows that see them after the tiles.
+    auto store_values = [&](int tile, bool edge, uint64_t present) {
+      uint8_t *const to = values + (tile & 1) * (TOK * VR) + tid / C * VR + tid % C * 16;
+      if (edge) {
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          const uint32_t ok = 0u - (uint32_t)(present >> (i * (256 / C) + tid / C) & 1);
+          u32x4_t v = widen(vt[i]);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             v[x] &= ok;
             odd |= nonfinite_signs<BF, false>(v[x]);
             v[x] &= ~nonfinite<BF, false>(v[x]);
           }
+          *reinterpret_cast<u32x4_t *>(to + i * (256 / C) * VR) = v;
         }
-        vs[value_at<D>(token, chunk)] = v;
+        if ((odd & kSigns<false>) != 0) bounds[8] = 1;
+      } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) *reinterpret_cast<u32x4_t *>(to + i * (256 / C) * VR) = widen(vt[i]);
       }
-      if (edge && (odd & kSigns<false>) != 0) bounds[8] = 1;
     };
-
-    uint64_t there = 0, there_next = 0;
-    int64_t at = place(t, id, &there);
-    load_tile(at);
-    store_tile(0, is_edge(tile_base(t), there), there);
-    at = place(t + 1, id_next, &there_next);
-    load_tile(at);
-    id = load_id(t + 2);
-    __syncthreads();
 
     f32x16_t acc[DB];
     float m = kNegInf, l = 0.0f;
@@ -268,32 +259,61 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-
-    int buffer = 0;
-    for (; t < t_end; ++t) {
-      const u32x4_t *const ks = stage + buffer * (2 * TOK * C), *const vs = ks + TOK * C;
-      // ---- scores: lane (c, half) has row c, tokens 32 b + 8 (i / 4) + 4 half + i % 4
-      f32x16_t s[TB];
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
-      int ln = lane;
-      asm volatile("" : "+v"(ln));  // places computed anew for each tile, not kept in registers
+    // Scores of half a tile: lane (c, half) has row c, tokens 32 b + 8 (i / 4) +
+    // 4 half + i % 4.
+    f32x16_t s[2];
+    u32x4_t p[2][2];  // their weights, as operands of the second product
+    const uint8_t *const key0 = keys + c * KR + half * 16;
+    auto products = [&](int tile, int b) {
+      const uint8_t *const from = key0 + (tile & 1) * (TOK * KR);
+      const f32x16_t none = {};
 #pragma unroll
       for (int st = 0; st < QS; ++st)
+        s[b] = mfma_32x32x16<BF>(*reinterpret_cast<const u32x4_t *>(from + b * (32 * KR) + st * 32), qf[st], st ? s[b] : none);
+    };
+    // Weights leave fp32 for the matrix product: half a step of q's type each, as
+    // in the attention over a sequence's own tokens.
+    auto weigh = [&](int b) {
+      const float mm = m == kNegInf ? 0.0f : m;
+      float sum = 0.0f;
 #pragma unroll
-        for (int b = 0; b < TB; ++b)
-          s[b] = mfma_32x32x16<BF>(ks[key_at<D>(b * 32 + (ln & 31), st * 2 + (ln >> 5))], qf[st], s[b]);
-      const int tb = tile_base(t);
-      const bool edge = is_edge(tb, there);
-      if (edge) {
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][u * 8 + x * 2], sc, -mm));
+          const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][u * 8 + x * 2 + 1], sc, -mm));
+          sum += w0;
+          sum += w1;
+          p[b][u][x] = pair_of<BF>(w0, w1);
+        }
+      l += sum;
+    };
+    // Half a tile's values by their weights; a lane's operand is 8 tokens of one d,
+    // turned by the LDS.
+    const uint8_t *const value0 = values + (4 * half + (lane & 15) / 4) * VR + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+    auto add = [&](int tile, int b) {
+      typedef __attribute__((address_space(3))) s16x4_t LdsQuad;
+      uint8_t *const from = const_cast<uint8_t *>(value0) + (tile & 1) * (TOK * VR);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          const int to = (b * 32 + u * 16) * VR + d * 64;
+          const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad *)(from + to)));
+          const uint2 y = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad *)(from + to + 8 * VR)));
+          acc[d] = mfma_32x32x16<BF>(u32x4_t{x.x, x.y, y.x, y.y}, p[b][u], acc[d]);
+        }
+    };
+    // Scores of a tile that have no part, and the reference of the weights.
+    auto look = [&](int tile, uint64_t present) {
+      const int tb = tile_base(tile);
+      if (is_edge(tb, present)) {
         int from = 4 * half;  // the lane's first token
         asm volatile("" : "+v"(from));
-        const uint64_t mine = there >> from;
+        const uint64_t mine = present >> from;
         const int j0 = tb + from;
 #pragma unroll
-        for (int b = 0; b < TB; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int o = b * 32 + 8 * (i / 4) + i % 4;
@@ -301,85 +321,119 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
             s[b][i] = sees ? s[b][i] : kNegInf;
           }
       }
-      // ---- weights
       float top = s[0][0];
 #pragma unroll
-      for (int b = 0; b < TB; ++b)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
       top = pair_max(top) * sc;
       // (a difference, which is exact: m + 8 would round where scores pass 2^25)
       if (__any(top - m > 8.0f + kHeadroom<BF>)) {
-        const float mn = fmaxf(m, top - kHeadroom<BF>), f = weight_of(m, mn);
+        // The reference is a whole number, and what is scaled by powers of two
+        // keeps its bits: also the weights that are yet to be added up.
+        const float mn = fmaxf(m, __builtin_floorf(top) - kHeadroom<BF>);
+        const float f = __builtin_amdgcn_ldexpf(1.0f, max((int)(m - mn), -300));
         m = mn;
         l *= f;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[d][i] *= f;
-      }
-      const float mm = m == kNegInf ? 0.0f : m;
-      float sum = 0.0f;
-      u32x4_t pf[2 * TB];
-#pragma unroll
-      for (int b = 0; b < TB; ++b) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], sc, -mm));
-          sum += s[b][i];
-        }
-        // weights leave fp32 here, for the matrix product: half a step of q's
-        // type each, as in the attention over a sequence's own tokens
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) pf[b * 2 + u][x] = pair_of<BF>(s[b][u * 8 + x * 2], s[b][u * 8 + x * 2 + 1]);
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t w = p[1][u][x];
+            p[1][u][x] = pair_of<BF>(value_of<BF, false>(w, 0) * f, value_of<BF, false>(w, 1) * f);
+          }
       }
-      l += sum;
-      // ---- values: a lane's operand is 8 tokens of one d, turned by the LDS
+    };
+
+    // ---- While a tile's scores are weighed, the tile after it is multiplied with
+    // the queries and the one before it added up, half a tile of each at a time:
+    // matrix and vector instructions of different halves fill one another's time
+    // without more registers.  At the top of step t LDS holds the keys of t + 1 and
+    // the values of t - 1 and t; registers bring the keys of t + 2 and the values
+    // of t + 1.  One barrier a tile: after it, the keys of t and the values of
+    // t - 1 have been read by all, and what was stored in the step before is there.
+    uint64_t there1, there2, there3;  // of t + 1, ..
+    {
+      u32x4_t second[L];
+      Places at;
+      const uint64_t there0 = put(t, id);
+      look_up(t, at);
+      load_rows(kbase, at, kt);
+      load_rows(vbase, at, vt);
+      there1 = put(t + 1, id_next);
+      look_up(t + 1, at);
+      load_rows(kbase, at, second);
+      id = load_id(t + 2);
+      id_next = load_id(t + 3);
+      // (before the first tile there are no values: weights of 0, which need
+      // finite numbers to stand there)
+      uint8_t *const none = values + (~t & 1) * (TOK * VR) + tid / C * VR + tid % C * 16;
 #pragma unroll
-      for (int u = 0; u < 2 * TB; ++u)
+      for (int i = 0; i < L; ++i) *reinterpret_cast<u32x4_t *>(none + i * (256 / C) * VR) = u32x4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          typedef __attribute__((address_space(3))) s16x4_t LdsQuad;
-          const int token = u * 16 + 4 * (ln >> 5) + (ln & 15) / 4;
-          const int chunk = 4 * d + 2 * (ln >> 4 & 1) + (ln >> 1 & 1);
-          uint8_t *const base = reinterpret_cast<uint8_t *>(const_cast<u32x4_t *>(vs)) + (ln & 1) * 8;
-          const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (LdsQuad *)(base + value_at<D>(token, chunk) * 16));
-          const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (LdsQuad *)(base + value_at<D>(token + 8, chunk) * 16));
-          const uint2 x2 = __builtin_bit_cast(uint2, x), y2 = __builtin_bit_cast(uint2, y);
-          acc[d] = mfma_32x32x16<BF>(u32x4_t{x2.x, x2.y, y2.x, y2.y}, pf[u], acc[d]);
-        }
-      // ---- the next tile
-      buffer ^= 1;
-      const int next = tile_base(t + 1);
-      store_tile(buffer, is_edge(next, there_next), there_next);
-      there = there_next;
-      at = place(t + 2, id, &there_next);
-      load_tile(at);
-      id = load_id(t + 3);
+      for (int u = 0; u < 2; ++u) p[1][u] = u32x4_t{0, 0, 0, 0};
+      store_keys(t, kt);
+      store_values(t, is_edge(tile_base(t), there0), there0);
+      store_keys(t + 1, second);
+      load_rows(vbase, at, vt);
+      there2 = put(t + 2, id);
+      look_up(t + 2, at);
+      load_rows(kbase, at, kt);
+      there3 = put(t + 3, id_next);
+      id = load_id(t + 4);
       __syncthreads();
+      products(t, 0);
+      products(t, 1);
+      look(t, there0);
     }
+    do {
+      Places at2, at3;
+      look_up(t + 2, at2);
+      look_up(t + 3, at3);
+      weigh(0);
+      add(t - 1, 1);
+      __syncthreads();
+      // (past the last tile: keys and values of the first slot, which nothing reads)
+      store_keys(t + 2, kt);
+      store_values(t + 1, is_edge(tile_base(t + 1), there1), there1);
+      load_rows(kbase, at3, kt);
+      load_rows(vbase, at2, vt);
+      products(t + 1, 0);
+      weigh(1);
+      __builtin_amdgcn_sched_barrier(0);
+      products(t + 1, 1);
+      add(t, 0);
+      // (computed here, beside the products, not where it is used next)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) asm volatile("" : "+v"(p[1][u]));
+      ++t;
+      look(t, there1);  // (past the last tile nothing is there)
+      there1 = there2;
+      there2 = there3;
+      there3 = put(t + 3, id);
+      id = load_id(t + 4);
+    } while (t < t_end);
+    add(t - 1, 1);
 
     if (bounds[8]) {
       // The NaNs and infinities of the tiles above, to the rows that see their
       // tokens.
 #pragma unroll 1
       for (int t2 = first; t2 < t_end; ++t2) {
-        uint64_t present;
-        const int64_t from = place(t2, load_id(t2), &present);
+        const uint64_t present = put(t2, load_id(t2));
         const int tb = tile_base(t2);
         if (!is_edge(tb, present)) continue;
 #pragma unroll 1
         for (int o = 0; o < TOK; ++o) {
           if (!(present >> o & 1)) continue;
-          const int64_t at_o = (int64_t)(uint32_t)__shfl((int)from, o) | (int64_t)__shfl((int)(from >> 32), o) << 32;
           const int j = tb + o;
           uint32_t sees = (j < hi) & ((j >= lo) | (j < sinks)) ? ~0u : 0u;
           asm volatile("" : "+v"(sees));  // a mask in a register, no branch for each value
-          const uint8_t *const p = vbase + at_o + 4 * half * CB;
+          const uint8_t *const p = vbase + ring[(t2 & 1) * 64 + o] + 4 * half * CB;
 #pragma unroll
           for (int d = 0; d < DB; ++d)
 #pragma unroll
