@@ -34,7 +34,8 @@ int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix) {
   // up to 128 tokens: 8 sequences 13.0 -> 7.0 and 13.1 -> 8.2 us, 95 of them 26.5
   // -> 10.9 and 27.3 -> 12.3; of 110..160 tokens, where the rule ends, 16.7 and
   // 12.3 for 8, but 16.9 and 21.0 for 32, and 32.0 and 13.3 for 95).
-  const int rt_max = D == 256 ? 2 : 4;
+  // (After a common prefix and at D = 128: 48, what two workgroups a CU hold.)
+  const int rt_max = D == 256 ? 2 : after_prefix && D == 128 ? 3 : 4;
   a->shared = R > rt_max * 16 || (R > 48 && D == 128 && !f8 && tiles <= 4);
   a->group_magic = (65536 + a->G - 1) / a->G;
   const int waves = a->shared ? 4 : 1, tw = 4 / waves;
@@ -43,7 +44,7 @@ int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix) {
   const int item_rows = waves * a->rt * 16;
   const int64_t granules = (tiles + tw - 1) / tw;
   const int64_t items = (int64_t)a->B * a->c.H * groups;
-  const int occupancy = attend_occupancy(f8, D, a->rt, a->shared);
+  const int occupancy = after_prefix && D < 256 ? 2 : attend_occupancy(f8, D, a->rt, a->shared);
   const int64_t most = (int64_t)occupancy * device_cu_count();
   // Whether items are shared by workgroups, or walked by one each: without parts
   // and a second kernel, and given out as workgroups end.  They are not where
@@ -64,7 +65,7 @@ int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix) {
   a->seq_items = a->c.H * groups;
   a->workgroups = (int)(a->joins ? std::min(most, items * granules) : items);
   // ranks: workgroups of a CU, where all of them run
-  a->ranks = a->joins && a->workgroups == most ? occupancy : 1;
+  a->ranks = a->joins && a->workgroups == most && !(after_prefix && D < 256) ? occupancy : 1;
   a->rank_size = a->workgroups / a->ranks;
   page_magic(a->rank_size, &a->rank_magic, &a->rank_shift);
   a->row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(item_rows, R), 1024 / items));
@@ -75,6 +76,7 @@ int64_t plan_attend(AttendArgs *a, void *work, bool after_prefix) {
   a->plan = reinterpret_cast<int32_t *>(p);
   a->ml = reinterpret_cast<float *>(p + plan_bytes);
   a->part = reinterpret_cast<float *>(p + plan_bytes + up(8 * parts));
+  if (after_prefix) a->grid = (int)std::min(most, (int64_t)a->pre_workgroups + a->workgroups);
   return plan_bytes + up(8 * parts) + 4 * parts * D;
 }
 

@@ -368,12 +368,12 @@ __device__ __forceinline__ int split_owner(const Split &s, int granule) {
 // the first of them in sequence b, before which lie `base`.  False if there is
 // none.  Workgroup 0 writes the plan for the join.
 template <bool PRE, class Args>
-__device__ __forceinline__ bool attend_range(Args &a, int before, int *scan, int *b, int *base, int *cur, int *range1) {
+__device__ __forceinline__ bool attend_range(Args &a, int before, int wg, int *scan, int *b, int *base, int *cur, int *range1) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int B = a.B;
   int total = 0;
   int at = 0, end = 0;
-  auto place = [&]() { split_range(split_of(a, total), blockIdx.x, &at, &end); };
+  auto place = [&]() { split_range(split_of(a, total), wg, &at, &end); };
   auto granules_of = [&](int s) {
     const SeqWork w = seq_work<PRE>(a, s, before);
     return w.items * w.granules;
@@ -390,14 +390,14 @@ __device__ __forceinline__ bool attend_range(Args &a, int before, int *scan, int
   if (B == 1) {
     total = granules_of(0);
     place();
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[2] = total;
+    if (wg == 0 && threadIdx.x == 0) a.plan[2] = total;
     *b = 0;
     *base = 0;
   } else if (B <= 64) {  // every wave by itself
     const int n = lane < B ? granules_of(lane) : 0, in = inclusive(n);
     total = __builtin_amdgcn_readlane(in, 63);
     place();
-    if (blockIdx.x == 0 && wave == 0 && lane < B) a.plan[2 + lane] = in;
+    if (wg == 0 && wave == 0 && lane < B) a.plan[2 + lane] = in;
     const uint64_t mine = __ballot(n && at >= in - n && at < in);
     const int at_lane = mine ? (int)__ffsll((long long)mine) - 1 : 0;
     *b = __builtin_amdgcn_readfirstlane(at_lane);
@@ -423,7 +423,7 @@ __device__ __forceinline__ bool attend_range(Args &a, int before, int *scan, int
             scan[4] = s;
             scan[5] = in - n;
           }
-          if (blockIdx.x == 0 && s < B) a.plan[2 + s] = in;
+          if (wg == 0 && s < B) a.plan[2 + s] = in;
         }
         __syncthreads();
       }
@@ -432,7 +432,7 @@ __device__ __forceinline__ bool attend_range(Args &a, int before, int *scan, int
     *b = __builtin_amdgcn_readfirstlane(scan[4]);
     *base = __builtin_amdgcn_readfirstlane(scan[5]);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  if (wg == 0 && threadIdx.x == 0) {
     a.plan[0] = total;
     a.plan[1] = 0;
   }
@@ -442,16 +442,15 @@ __device__ __forceinline__ bool attend_range(Args &a, int before, int *scan, int
   return true;
 }
 
-template <bool BF, bool F8, int D, int RT, bool SH, int OCC, bool PRE = false>
-__global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
+template <bool BF, bool F8, int D, int RT, bool SH, bool PRE>
+__device__ __forceinline__ void attend_body(KernArgs *ap, uint8_t *const lds, const int wg) {
   using T = Tile<F8, D>;
   constexpr int KL = T::KL, KC = T::KC, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
   constexpr int CB = F8 ? 1 : 2;
   constexpr int QS = D / 32;  // steps of the first product
   constexpr bool QLDS = queries_in_lds(D, RT, SH);
   constexpr int CHUNKS = SH ? 4 : 1, TW = 4 / CHUNKS;  // waves that split the rows, and the tokens
-  extern __shared__ __align__(16) uint8_t lds[];
-  // [4 waves][2][32] token offsets, the scan, then the queries and the waves'
+  // LDS: [4 waves][2][32] token offsets, the scan, then the queries and the waves'
   // keys and, after the tokens, in the same place what waves hand over
   int64_t *const ring = reinterpret_cast<int64_t *>(lds);
   int *const scan = reinterpret_cast<int *>(lds + 2048);
@@ -459,7 +458,6 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   float *const give_ml = reinterpret_cast<float *>(lds + kLdsHead);
   f32x4_t *const give = reinterpret_cast<f32x4_t *>(lds + kLdsHead + 2 * RT * 64 * 2 * 4);
 
-  KernArgs *ap = kern_args();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -471,9 +469,9 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   const bool joins = PRE || ap->joins;
   int b, base = 0, cur = 0, range1 = 1;
   if (joins) {
-    if (!attend_range<PRE>(*ap, before, scan, &b, &base, &cur, &range1)) return;
+    if (!attend_range<PRE>(*ap, before, wg, scan, &b, &base, &cur, &range1)) return;
   } else {
-    b = blockIdx.x / ap->seq_items;
+    b = wg / ap->seq_items;
   }
 
   int64_t *const my_ring = ring + wave * 64;
@@ -494,7 +492,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       item = (int)((uint32_t)(cur - base) / (uint32_t)w.granules);
       first = (cur - base) - item * w.granules;
     } else {
-      item = blockIdx.x - b * ap->seq_items;
+      item = wg - b * ap->seq_items;
       if (item >= w.items) return;
     }
     const int n_granules = min(w.granules - first, range1 - cur);
@@ -924,7 +922,7 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
       const float vs = ap->c.v_scale ? constant(ap->c.v_scale)[h] : 1.0f;
       // a part that does not begin its item is its workgroup's first, one that
       // begins it and does not end it is its last
-      int64_t part = 2 * (int64_t)blockIdx.x + (first == 0 ? 1 : 0);
+      int64_t part = 2 * (int64_t)wg + (first == 0 ? 1 : 0);
       const bool whole = n_granules == w.granules;
       // (what others walked has to be joined to it, so it is a part in any case)
       if (PRE && whole)
@@ -973,9 +971,16 @@ __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   }
 }
 
-// The parts of the common tokens (qgemv_prefix_impl.h): an item is 128 or 256 rows
-// of a head of all the call's, and has n granules; workgroups take per of them
-// each.
+template <bool BF, bool F8, int D, int RT, bool SH, int OCC, bool PRE = false>
+__global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  attend_body<BF, F8, D, RT, SH, PRE>(kern_args(), lds, blockIdx.x);
+}
+
+// The parts of the common tokens (qgemv_prefix_impl.h): an item is 128 rows of a
+// head of all the call's, and has n granules; workgroups take per of them each.
+// Where there are workgroups for several parts of each item, n is filled up to
+// whole parts.
 struct PrefixPlan {
   int n, per;
   int most;  // parts that an item can have
@@ -1088,41 +1093,39 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   }
 }
 
-template <bool BF, bool F8, int D, int RT, bool SH, bool PRE>
-int launch_attend_rt(const AttendArgs &a, hipStream_t stream) {
-  constexpr int OCC = attend_occupancy(F8, D, RT, SH);
-  constexpr size_t bytes = attend_lds(F8, D, RT, SH);
-  const auto kern = attend_kernel<BF, F8, D, RT, SH, OCC, PRE>;
-  if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
-  hipLaunchKernelGGL(kern, dim3(a.workgroups), dim3(256), bytes, stream, a);
-  if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
-  if (!a.joins) return QGEMV_OK;
+template <bool BF, int D, bool PRE>
+int launch_join(const AttendArgs &a, hipStream_t stream) {
   hipLaunchKernelGGL((join_kernel<BF, D, PRE>), dim3(a.B * a.seq_items, a.row_splits), dim3(256), 0, stream, a);
   return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
 }
 
-template <bool BF, bool F8, int D, bool SH, bool PRE>
-int launch_attend_d(const AttendArgs &a, hipStream_t stream) {
-  if constexpr (D < 256) {
-    if (a.rt == 3) return launch_attend_rt<BF, F8, D, 3, SH, PRE>(a, stream);
-    if (a.rt == 4) return launch_attend_rt<BF, F8, D, 4, SH, PRE>(a, stream);
-  }
-  return a.rt == 1 ? launch_attend_rt<BF, F8, D, 1, SH, PRE>(a, stream)
-                   : launch_attend_rt<BF, F8, D, 2, SH, PRE>(a, stream);
+template <bool BF, bool F8, int D, int RT, bool SH>
+int launch_attend_rt(const AttendArgs &a, hipStream_t stream) {
+  constexpr int OCC = attend_occupancy(F8, D, RT, SH);
+  constexpr size_t bytes = attend_lds(F8, D, RT, SH);
+  const auto kern = attend_kernel<BF, F8, D, RT, SH, OCC>;
+  if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
+  hipLaunchKernelGGL(kern, dim3(a.workgroups), dim3(256), bytes, stream, a);
+  if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
+  return a.joins ? launch_join<BF, D, false>(a, stream) : QGEMV_OK;
 }
 
-template <bool BF, bool F8, bool PRE = false>
+template <bool BF, bool F8, int D, bool SH>
+int launch_attend_d(const AttendArgs &a, hipStream_t stream) {
+  if constexpr (D < 256) {
+    if (a.rt == 3) return launch_attend_rt<BF, F8, D, 3, SH>(a, stream);
+    if (a.rt == 4) return launch_attend_rt<BF, F8, D, 4, SH>(a, stream);
+  }
+  return a.rt == 1 ? launch_attend_rt<BF, F8, D, 1, SH>(a, stream) : launch_attend_rt<BF, F8, D, 2, SH>(a, stream);
+}
+
+template <bool BF, bool F8>
 int launch_attend_t(const AttendArgs &a, hipStream_t stream) {
   switch (a.c.D) {
-    case 64:
-      return a.shared ? launch_attend_d<BF, F8, 64, true, PRE>(a, stream)
-                           : launch_attend_d<BF, F8, 64, false, PRE>(a, stream);
-    case 128:
-      return a.shared ? launch_attend_d<BF, F8, 128, true, PRE>(a, stream)
-                           : launch_attend_d<BF, F8, 128, false, PRE>(a, stream);
+    case 64: return a.shared ? launch_attend_d<BF, F8, 64, true>(a, stream) : launch_attend_d<BF, F8, 64, false>(a, stream);
+    case 128: return a.shared ? launch_attend_d<BF, F8, 128, true>(a, stream) : launch_attend_d<BF, F8, 128, false>(a, stream);
   }
-  return a.shared ? launch_attend_d<BF, F8, 256, true, PRE>(a, stream)
-                       : launch_attend_d<BF, F8, 256, false, PRE>(a, stream);
+  return a.shared ? launch_attend_d<BF, F8, 256, true>(a, stream) : launch_attend_d<BF, F8, 256, false>(a, stream);
 }
 
 }  // namespace qgemv

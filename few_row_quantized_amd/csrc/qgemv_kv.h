@@ -76,6 +76,7 @@ struct AttendArgs {
   int pre_rows;           // rows of an item
   int pre_tiles;          // items of a head: groups of so many rows of all
   int pre_workgroups, pre_most;
+  int grid;               // of the launch that has both
 };
 
 struct RotateArgs {

@@ -66,18 +66,16 @@ constexpr int value_row(int D) { return 2 * D + 64; }
 constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)2 * kPrefixTokens * (key_row(D) + value_row(D)); }
 
 template <bool BF, bool F8, int D>
-__global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(AttendArgs) {
+__device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, const int index) {
   constexpr int TOK = kPrefixTokens, C = D / 8, DB = D / 32, QS = D / 16;
   constexpr int L = TOK * C / 256;  // chunks of a thread, of keys and of values
   constexpr int KR = key_row(D), VR = value_row(D);
   constexpr int CB = F8 ? 1 : 2;
-  extern __shared__ __align__(16) uint8_t lds[];
   int *const row_pos = reinterpret_cast<int *>(lds);        // [128] rows of T
   int *const bounds = reinterpret_cast<int *>(lds + 512);   // of each wave: smallest end, largest begin; then strays
   int64_t *const ring = reinterpret_cast<int64_t *>(lds + 1024) + (threadIdx.x >> 6) * 128;
   uint8_t *const keys = lds + kPrefixHead, *const values = keys + 2 * TOK * KR;
 
-  KernArgs *ap = kern_args();
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, half = lane >> 5;
@@ -104,22 +102,33 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
   const int sink_tiles = ap->window ? min((int)(((int64_t)sinks + TOK - 1) / TOK), low_tile) : 0;
   const int n = sink_tiles + all - low_tile;
   const int items = ap->pre_tiles * ap->c.H;
-  const int total = items * n;
-  const int per = max((total + ap->pre_workgroups - 1) / ap->pre_workgroups, 1);
-  if (blockIdx.x == 0 && tid == 0) {
-    ap->pre_plan[0] = n;
+  // Equal ranges of all items' granules; with workgroups for several parts of
+  // each item, as many for each, so that none walks two (of P workgroups for an
+  // item and the rest of them, at most 1 in P + 1 has nothing to do).
+  const int workgroups = ap->pre_workgroups, parts = (int)((uint32_t)workgroups / (uint32_t)items);
+  int per, padded = n;
+  if (parts >= 4 && n) {
+    per = (n + parts - 1) / parts;
+    padded = (n + per - 1) / per * per;
+  } else {
+    per = max((items * n + workgroups - 1) / workgroups, 1);
+  }
+  const int total = items * padded;
+  if (index == 0 && tid == 0) {
+    ap->pre_plan[0] = padded;
     ap->pre_plan[1] = per;
   }
+  if (index >= workgroups) return;
   // Workgroups of an XCD, which share its L2, walk neighbouring ranges.
-  int wg = blockIdx.x;
-  if (ap->pre_workgroups % 8 == 0) wg = (wg & 7) * (ap->pre_workgroups >> 3) + (wg >> 3);
+  int wg = index;
+  if (workgroups % 8 == 0) wg = (wg & 7) * (workgroups >> 3) + (wg >> 3);
   int cur = wg * per;
   const int end = min(cur + per, total);
 
   while (cur < end) {
-    const int item = (int)((uint32_t)cur / (uint32_t)n), first = cur - item * n;
+    const int item = (int)((uint32_t)cur / (uint32_t)padded), first = cur - item * padded;
     const int count = min(n - first, end - cur);
-    cur += count;
+    cur += min(padded - first, end - cur);
     const int h = (int)((uint32_t)item / (uint32_t)ap->pre_tiles), tile0 = item - h * ap->pre_tiles;
     const int r0 = tile0 * kPrefixRows, row = r0 + wave * 32 + c;
 
@@ -455,7 +464,7 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
     // ---- write: lane (c, half) has row c and d = 32 b + 8 (i / 4) + 4 half + i % 4
     l = pair_sum(l);
     if (row < R) {
-      const int part = (int)((uint32_t)(item * n + first) / (uint32_t)per) - (int)((uint32_t)(item * n) / (uint32_t)per);
+      const int part = (int)((uint32_t)(item * padded + first) / (uint32_t)per) - (int)((uint32_t)(item * padded) / (uint32_t)per);
       const int64_t to = ((int64_t)item * ap->pre_most + part) * kPrefixRows + wave * 32 + c;
       float *const o = ap->pre_part + to * D;
 #pragma unroll
@@ -472,21 +481,70 @@ __global__ __launch_bounds__(256, prefix_occupancy(D)) void prefix_kernel(Attend
   }
 }
 
+// The common tokens and the sequences' own in one launch.  A workgroup takes its
+// range of one, then its range of the other: the first half of them the own
+// tokens first, the second half the common ones, so that of the two workgroups
+// of a CU one is bound by the memory while the other is by the matrix units.
+// Counted from the other end, the workgroups of small calls have one of both.
+template <bool BF, bool F8, int D, int RT, bool SH>
+__global__ __launch_bounds__(256, 2) void shared_kernel(AttendArgs) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  KernArgs *ap = kern_args();
+  const bool prefix_first = 2 * blockIdx.x >= gridDim.x;
+#pragma unroll 1
+  for (int turn = 0; turn < 2; ++turn) {
+    if ((turn == 0) == prefix_first)
+      prefix_body<BF, F8, D>(reload(ap), lds, gridDim.x - 1 - blockIdx.x);
+    else
+      attend_body<BF, F8, D, RT, SH, true>(reload(ap), lds, blockIdx.x);
+    __syncthreads();
+  }
+}
+
+// At D = 256 either needs the registers of a CU's one workgroup for itself.
 template <bool BF, bool F8, int D>
-int launch_prefix_d(const AttendArgs &a, hipStream_t stream) {
-  constexpr size_t bytes = prefix_lds(D);
-  const auto kern = prefix_kernel<BF, F8, D>;
-  if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
-  hipLaunchKernelGGL(kern, dim3(a.pre_workgroups), dim3(256), bytes, stream, a);
-  return hipGetLastError() == hipSuccess ? QGEMV_OK : QGEMV_EHIP;
+__global__ __launch_bounds__(256, 1) void prefix_kernel(AttendArgs) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  prefix_body<BF, F8, D>(kern_args(), lds, blockIdx.x);
+}
+
+template <bool BF, bool F8, int D, int RT, bool SH>
+int launch_shared_rt(const AttendArgs &a, hipStream_t stream) {
+  constexpr size_t own = attend_lds(F8, D, RT, SH), common = prefix_lds(D);
+  if constexpr (D == 256) {
+    const auto first = prefix_kernel<BF, F8, D>;
+    if (!allow_max_dynamic_lds(reinterpret_cast<const void *>(first))) return QGEMV_EHIP;
+    hipLaunchKernelGGL(first, dim3(a.pre_workgroups), dim3(256), common, stream, a);
+    if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
+    const auto second = attend_kernel<BF, F8, D, RT, SH, attend_occupancy(F8, D, RT, SH), true>;
+    if (own > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(second))) return QGEMV_EHIP;
+    hipLaunchKernelGGL(second, dim3(a.workgroups), dim3(256), own, stream, a);
+  } else {
+    constexpr size_t bytes = own > common ? own : common;
+    const auto kern = shared_kernel<BF, F8, D, RT, SH>;
+    if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
+    hipLaunchKernelGGL(kern, dim3(a.grid), dim3(256), bytes, stream, a);
+  }
+  if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
+  return launch_join<BF, D, true>(a, stream);
+}
+
+template <bool BF, bool F8, int D, bool SH>
+int launch_shared_d(const AttendArgs &a, hipStream_t stream) {
+  if constexpr (D < 256)
+    if (a.rt == 3) return launch_shared_rt<BF, F8, D, 3, SH>(a, stream);
+  if constexpr (D == 64)
+    if (a.rt == 4) return launch_shared_rt<BF, F8, D, 4, SH>(a, stream);
+  return a.rt == 1 ? launch_shared_rt<BF, F8, D, 1, SH>(a, stream) : launch_shared_rt<BF, F8, D, 2, SH>(a, stream);
 }
 
 template <bool BF, bool F8>
 int launch_shared_t(const AttendArgs &a, hipStream_t stream) {
-  const int s = a.c.D == 64 ? launch_prefix_d<BF, F8, 64>(a, stream)
-                : a.c.D == 128 ? launch_prefix_d<BF, F8, 128>(a, stream)
-                               : launch_prefix_d<BF, F8, 256>(a, stream);
-  return s == QGEMV_OK ? launch_attend_t<BF, F8, true>(a, stream) : s;
+  switch (a.c.D) {
+    case 64: return a.shared ? launch_shared_d<BF, F8, 64, true>(a, stream) : launch_shared_d<BF, F8, 64, false>(a, stream);
+    case 128: return a.shared ? launch_shared_d<BF, F8, 128, true>(a, stream) : launch_shared_d<BF, F8, 128, false>(a, stream);
+  }
+  return a.shared ? launch_shared_d<BF, F8, 256, true>(a, stream) : launch_shared_d<BF, F8, 256, false>(a, stream);
 }
 
 }  // namespace qgemv
