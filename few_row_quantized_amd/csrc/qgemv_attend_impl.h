@@ -329,8 +329,9 @@ struct Split {
   int per0, per1, per2;  // granules of a workgroup
 };
 
-template <class Args>
-__device__ __forceinline__ Split split_of(Args &a, int total) {
+template <bool PRE, class Args>
+__device__ __forceinline__ Split split_of(Args &a, int total, int workgroups) {
+  if constexpr (PRE) return Split{1, workgroups, max((total + workgroups - 1) / workgroups, 1), 0, 0};
   const int ranks = a.ranks, n = a.rank_size;
   auto per = [&](int left, int share) {  // share 256ths of what is left, over n workgroups
     const int part = (left >> 8) * share + ((left & 255) * share >> 8);
@@ -368,12 +369,12 @@ __device__ __forceinline__ int split_owner(const Split &s, int granule) {
 // the first of them in sequence b, before which lie `base`.  False if there is
 // none.  Workgroup 0 writes the plan for the join.
 template <bool PRE, class Args>
-__device__ __forceinline__ bool attend_range(Args &a, int before, int wg, int *scan, int *b, int *base, int *cur, int *range1) {
+__device__ __forceinline__ bool attend_range(Args &a, int before, int wg, int workgroups, int *scan, int *b, int *base, int *cur, int *range1) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int B = a.B;
   int total = 0;
   int at = 0, end = 0;
-  auto place = [&]() { split_range(split_of(a, total), wg, &at, &end); };
+  auto place = [&]() { split_range(split_of<PRE>(a, total, workgroups), wg, &at, &end); };
   auto granules_of = [&](int s) {
     const SeqWork w = seq_work<PRE>(a, s, before);
     return w.items * w.granules;
@@ -432,6 +433,7 @@ __device__ __forceinline__ bool attend_range(Args &a, int before, int wg, int *s
     *b = __builtin_amdgcn_readfirstlane(scan[4]);
     *base = __builtin_amdgcn_readfirstlane(scan[5]);
   }
+  if (PRE && wg == 0 && threadIdx.x == 0) a.pre_plan[2] = workgroups;
   if (wg == 0 && threadIdx.x == 0) {
     a.plan[0] = total;
     a.plan[1] = 0;
@@ -443,7 +445,7 @@ __device__ __forceinline__ bool attend_range(Args &a, int before, int wg, int *s
 }
 
 template <bool BF, bool F8, int D, int RT, bool SH, bool PRE>
-__device__ __forceinline__ void attend_body(KernArgs *ap, uint8_t *const lds, const int wg) {
+__device__ __forceinline__ void attend_body(KernArgs *ap, uint8_t *const lds, const int wg, const int workgroups) {
   using T = Tile<F8, D>;
   constexpr int KL = T::KL, KC = T::KC, VH = T::VH, E = T::E, VW = T::VW, NE = VH * E;
   constexpr int CB = F8 ? 1 : 2;
@@ -469,7 +471,7 @@ __device__ __forceinline__ void attend_body(KernArgs *ap, uint8_t *const lds, co
   const bool joins = PRE || ap->joins;
   int b, base = 0, cur = 0, range1 = 1;
   if (joins) {
-    if (!attend_range<PRE>(*ap, before, wg, scan, &b, &base, &cur, &range1)) return;
+    if (!attend_range<PRE>(*ap, before, wg, workgroups, scan, &b, &base, &cur, &range1)) return;
   } else {
     b = wg / ap->seq_items;
   }
@@ -974,7 +976,7 @@ __device__ __forceinline__ void attend_body(KernArgs *ap, uint8_t *const lds, co
 template <bool BF, bool F8, int D, int RT, bool SH, int OCC, bool PRE = false>
 __global__ __launch_bounds__(256, OCC) void attend_kernel(AttendArgs) {
   extern __shared__ __align__(16) uint8_t lds[];
-  attend_body<BF, F8, D, RT, SH, PRE>(kern_args(), lds, blockIdx.x);
+  attend_body<BF, F8, D, RT, SH, PRE>(kern_args(), lds, blockIdx.x, gridDim.x);
 }
 
 // The parts of the common tokens (qgemv_prefix_impl.h): an item is 128 rows of a
@@ -1018,7 +1020,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   const SeqWork w = seq_work<PRE>(a, b, common_pages<PRE>(a) * a.c.page);
   const int groups = w.items ? w.groups : 0, h = hg / groups_max, group = hg - h * groups_max;
   if (group >= groups) return;
-  const Split split = split_of(a, a.plan[0]);
+  const Split split = split_of<PRE>(a, a.plan[0], PRE ? a.pre_plan[2] : 0);
   const PrefixPlan pre = PRE ? prefix_plan(a) : PrefixPlan{};
   const int first_row = w.row0 * a.G + group * item_rows;  // of all rows of the call
   const int g0 = a.plan[1 + b] + (h * groups + group) * w.granules, g1 = g0 + w.granules;

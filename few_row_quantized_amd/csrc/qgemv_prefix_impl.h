@@ -54,6 +54,7 @@ __device__ __forceinline__ int wave_least(int x) {
 
 constexpr int kPrefixRows = 128;   // of an item: 32 a wave
 constexpr int kPrefixTokens = 64;  // of a granule
+constexpr int kOrder = 1;
 constexpr int prefix_occupancy(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
 
 // LDS of a workgroup: positions of the rows and the reductions, then keys of two
@@ -65,11 +66,52 @@ constexpr int key_row(int D) { return 2 * D + 16; }
 constexpr int value_row(int D) { return 2 * D + 64; }
 constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)2 * kPrefixTokens * (key_row(D) + value_row(D)); }
 
+// The first token that a row's window can reach: of the sequence with the lowest
+// position.  (The workgroup's threads together; 4 words of LDS.)
+template <class Args>
+__device__ __forceinline__ int lowest_token(Args &a, int before, int *lds) {
+  if (!a.window) return 0;
+  int least = 0x7FFFFFFF;
+  for (int b = threadIdx.x; b < a.B; b += 256) {
+    const int s0 = min(max(a.start[b], 0), a.T), s1 = min(max(a.start[b + 1], s0), a.T);
+    const int len = min(max(a.len[b], 0), QGEMV_MAX_CONTEXT);
+    if (s1 > s0) least = min(least, len - (s1 - s0));
+  }
+  lds[threadIdx.x >> 6] = wave_least(least);
+  __syncthreads();
+  least = min(min(lds[0], lds[1]), min(lds[2], lds[3]));
+  return __builtin_amdgcn_readfirstlane(min(max(least - a.window + 1, 0), before));
+}
+
+// Granules of the sequences' own tokens.
+template <class Args>
+__device__ __forceinline__ int own_granules(Args &a, int before, int *lds) {
+  int sum = 0;
+  for (int b = threadIdx.x; b < a.B; b += 256) {
+    const SeqWork w = seq_work<true>(a, b, before);
+    sum += w.items * w.granules;
+  }
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x111, 0xF, 0xF, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x112, 0xF, 0xF, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x114, 0xF, 0xF, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x118, 0xF, 0xF, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x142, 0xA, 0xF, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x143, 0xC, 0xF, false);
+  lds[threadIdx.x >> 6] = __builtin_amdgcn_readlane(sum, 63);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(lds[0] + lds[1] + lds[2] + lds[3]);
+}
+
 template <bool BF, bool F8, int D>
-__device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, const int index) {
+__device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, const int index, const int workgroups) {
   constexpr int TOK = kPrefixTokens, C = D / 8, DB = D / 32, QS = D / 16;
   constexpr int L = TOK * C / 256;  // chunks of a thread, of keys and of values
   constexpr int KR = key_row(D), VR = value_row(D);
+  // Exponentials placed between matrix instructions by hand, part by part: left to
+  // itself the compiler takes registers past the limit at D = 128 (queries spilled,
+  // each reload a wait for all loads in flight); at D = 64, where there are enough,
+  // its own order is better (a window of 4096, 16 rows: 60 us, 65 by hand).
+  constexpr bool ORDER = kOrder && D == 128;
   constexpr int CB = F8 ? 1 : 2;
   int *const row_pos = reinterpret_cast<int *>(lds);        // [128] rows of T
   int *const bounds = reinterpret_cast<int *>(lds + 512);   // of each wave: smallest end, largest begin; then strays
@@ -83,21 +125,7 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
   const int G = ap->G, T = ap->T, R = T * G, B = ap->B;
   const int window = ap->window ? ap->window : 1 << 30, sinks = ap->sinks;
 
-  // The first token that a row's window can reach: of the sequence with the
-  // lowest position.
-  int low = 0;
-  if (ap->window) {
-    int least = 0x7FFFFFFF;
-    for (int b = tid; b < B; b += 256) {
-      const int s0 = min(max(ap->start[b], 0), T), s1 = min(max(ap->start[b + 1], s0), T);
-      const int len = min(max(ap->len[b], 0), QGEMV_MAX_CONTEXT);
-      if (s1 > s0) least = min(least, len - (s1 - s0));
-    }
-    bounds[wave] = wave_least(least);
-    __syncthreads();
-    least = min(min(bounds[0], bounds[1]), min(bounds[2], bounds[3]));
-    low = __builtin_amdgcn_readfirstlane(min(max(least - window + 1, 0), before));
-  }
+  const int low = lowest_token(*ap, before, bounds);
   const int all = (before + TOK - 1) / TOK, low_tile = low / TOK;
   const int sink_tiles = ap->window ? min((int)(((int64_t)sinks + TOK - 1) / TOK), low_tile) : 0;
   const int n = sink_tiles + all - low_tile;
@@ -105,7 +133,7 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
   // Equal ranges of all items' granules; with workgroups for several parts of
   // each item, as many for each, so that none walks two (of P workgroups for an
   // item and the rest of them, at most 1 in P + 1 has nothing to do).
-  const int workgroups = ap->pre_workgroups, parts = (int)((uint32_t)workgroups / (uint32_t)items);
+  const int parts = (int)((uint32_t)workgroups / (uint32_t)items);
   int per, padded = n;
   if (parts >= 4 && n) {
     per = (n + parts - 1) / parts;
@@ -208,15 +236,23 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     // A thread's share of a tile's keys, and of another's values, on their way: its
     // chunk of 8 values of every (256 / C)th token.
     u32x4_t kt[L], vt[L];
+    // (What follows from the thread alone is computed anew for each tile, not kept
+    // in registers.)
+    auto anew = [](int x) {
+      asm volatile("" : "+v"(x));
+      return x;
+    };
     typedef int64_t Places[L];
     auto look_up = [&](int tile, Places &to) {
+      const int64_t *const from = ring + (tile & 1) * 64 + anew(tid) / C;
 #pragma unroll
-      for (int i = 0; i < L; ++i) to[i] = ring[(tile & 1) * 64 + i * (256 / C) + tid / C];
+      for (int i = 0; i < L; ++i) to[i] = from[i * (256 / C)];
     };
     auto load_rows = [&](const uint8_t *from, const Places &at, u32x4_t (&to)[L]) {
+      const int within = anew(tid) % C * (8 * CB);
 #pragma unroll
       for (int i = 0; i < L; ++i) {
-        const uint8_t *const p = from + tid % C * (8 * CB) + at[i];
+        const uint8_t *const p = from + at[i] + within;
         if constexpr (F8) {
           const u32x2_t x = *reinterpret_cast<const u32x2_t *>(p);
           to[i][0] = x[0];
@@ -232,7 +268,8 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
                      e4m3_pair<BF, true>(x[1])};
     };
     auto store_keys = [&](int tile, const u32x4_t (&from)[L]) {
-      uint8_t *const to = keys + (tile & 1) * (TOK * KR) + tid / C * KR + tid % C * 16;
+      const int me = anew(tid);
+      uint8_t *const to = keys + (tile & 1) * (TOK * KR) + me / C * KR + me % C * 16;
 #pragma unroll
       for (int i = 0; i < L; ++i) *reinterpret_cast<u32x4_t *>(to + i * (256 / C) * KR) = widen(from[i]);
     };
@@ -240,12 +277,13 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     // are not there, and without NaNs and infinities (0 times one is not 0), which
     // are given to the rows that see them after the tiles.
     auto store_values = [&](int tile, bool edge, uint64_t present) {
-      uint8_t *const to = values + (tile & 1) * (TOK * VR) + tid / C * VR + tid % C * 16;
+      const int me = anew(tid);
+      uint8_t *const to = values + (tile & 1) * (TOK * VR) + me / C * VR + me % C * 16;
       if (edge) {
         uint32_t odd = 0;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-          const uint32_t ok = 0u - (uint32_t)(present >> (i * (256 / C) + tid / C) & 1);
+          const uint32_t ok = 0u - (uint32_t)(present >> (i * (256 / C) + me / C) & 1);
           u32x4_t v = widen(vt[i]);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -272,9 +310,9 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     // 4 half + i % 4.
     f32x16_t s[2];
     u32x4_t p[2][2];  // their weights, as operands of the second product
-    const uint8_t *const key0 = keys + c * KR + half * 16;
     auto products = [&](int tile, int b) {
-      const uint8_t *const from = key0 + (tile & 1) * (TOK * KR);
+      const int me = anew(lane);
+      const uint8_t *const from = keys + (tile & 1) * (TOK * KR) + (me & 31) * KR + (me >> 5) * 16;
       const f32x16_t none = {};
 #pragma unroll
       for (int st = 0; st < QS; ++st)
@@ -299,10 +337,11 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     };
     // Half a tile's values by their weights; a lane's operand is 8 tokens of one d,
     // turned by the LDS.
-    const uint8_t *const value0 = values + (4 * half + (lane & 15) / 4) * VR + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
     auto add = [&](int tile, int b) {
       typedef __attribute__((address_space(3))) s16x4_t LdsQuad;
-      uint8_t *const from = const_cast<uint8_t *>(value0) + (tile & 1) * (TOK * VR);
+      const int me = anew(lane);
+      uint8_t *const from = values + (tile & 1) * (TOK * VR) + (4 * (me >> 5) + (me & 15) / 4) * VR +
+                            (me >> 4 & 1) * 32 + (me & 3) * 8;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -317,8 +356,7 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     auto look = [&](int tile, uint64_t present) {
       const int tb = tile_base(tile);
       if (is_edge(tb, present)) {
-        int from = 4 * half;  // the lane's first token
-        asm volatile("" : "+v"(from));
+        const int from = 4 * anew(half);  // the lane's first token
         const uint64_t mine = present >> from;
         const int j0 = tb + from;
 #pragma unroll
@@ -400,25 +438,38 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
       look(t, there0);
     }
     do {
+      weigh(0);
+      add(t - 1, 1);
+      if constexpr (ORDER) {
+        __builtin_amdgcn_iglp_opt(2);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) asm volatile("" : "+v"(acc[d]));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) asm volatile("" : "+v"(p[0][u]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
       Places at2, at3;
       look_up(t + 2, at2);
       look_up(t + 3, at3);
-      weigh(0);
-      add(t - 1, 1);
       __syncthreads();
       // (past the last tile: keys and values of the first slot, which nothing reads)
       store_keys(t + 2, kt);
       store_values(t + 1, is_edge(tile_base(t + 1), there1), there1);
       load_rows(kbase, at3, kt);
       load_rows(vbase, at2, vt);
+      if constexpr (ORDER) __builtin_amdgcn_sched_barrier(0);
       products(t + 1, 0);
       weigh(1);
-      __builtin_amdgcn_sched_barrier(0);
-      products(t + 1, 1);
-      add(t, 0);
+      if constexpr (ORDER) {
+        __builtin_amdgcn_iglp_opt(2);
+        asm volatile("" : "+v"(s[0]));
+      }
       // (computed here, beside the products, not where it is used next)
 #pragma unroll
       for (int u = 0; u < 2; ++u) asm volatile("" : "+v"(p[1][u]));
+      if constexpr (ORDER) __builtin_amdgcn_sched_barrier(0);
+      products(t + 1, 1);
+      add(t, 0);
       ++t;
       look(t, there1);  // (past the last tile nothing is there)
       there1 = there2;
@@ -481,22 +532,47 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
   }
 }
 
-// The common tokens and the sequences' own in one launch.  A workgroup takes its
-// range of one, then its range of the other: the first half of them the own
-// tokens first, the second half the common ones, so that of the two workgroups
-// of a CU one is bound by the memory while the other is by the matrix units.
-// Counted from the other end, the workgroups of small calls have one of both.
+// The common tokens and the sequences' own in one launch.  Where both are short,
+// each workgroup has one of the two, so that what their walks begin and end with
+// is at the same time (24 sequences over 6001 tokens of E4M3, 0..2500 of their
+// own: 81 -> 68 us): as many for each as their granules cost, measured as times
+// of all workgroups: one of own tokens as much as kOwnCost common ones.  Where
+// they are long, a workgroup takes its range of one, then its range of the other:
+// the first half of them the own tokens first, the second half the common ones,
+// so that of the two workgroups of a CU one is bound by the memory while the
+// other is by the matrix units, and none ends early.
+constexpr int kOwnCost = 2;     // half common granules
+constexpr int kLongWalk = 48;   // of a workgroup, in common granules
+
 template <bool BF, bool F8, int D, int RT, bool SH>
 __global__ __launch_bounds__(256, 2) void shared_kernel(AttendArgs) {
   extern __shared__ __align__(16) uint8_t lds[];
   KernArgs *ap = kern_args();
-  const bool prefix_first = 2 * blockIdx.x >= gridDim.x;
+  const int block = blockIdx.x, grid = gridDim.x;
+  // (in small calls there are workgroups for the most that either can be cut in)
+  int common = ap->pre_workgroups, own = ap->workgroups;
+  if (common + own > grid) {
+    int *const words = reinterpret_cast<int *>(lds);
+    const int before = common_pages<true>(*ap) * ap->c.page;
+    const int low = lowest_token(*ap, before, words);
+    const int granules = (before - low + kPrefixTokens - 1) / kPrefixTokens;
+    const int64_t first = (int64_t)granules * ap->pre_tiles * ap->c.H;
+    const int64_t second = (int64_t)own_granules(*ap, before, words + 4) * kOwnCost / 2;
+    if (first + second < (int64_t)kLongWalk * grid && grid >= 16) {
+      const int share = (int)((uint32_t)(first * grid) / (uint32_t)(first + second + 1)) & ~7;
+      common = min(common, min(max(share, 8), grid - 8));
+      own = min(own, grid - common);
+    }
+    __syncthreads();
+  }
+  const bool one = common + own <= grid;
+  const bool prefix_first = one ? block >= own : 2 * block >= grid;
 #pragma unroll 1
-  for (int turn = 0; turn < 2; ++turn) {
+  for (int turn = 0; turn < (one ? 1 : 2); ++turn) {
     if ((turn == 0) == prefix_first)
-      prefix_body<BF, F8, D>(reload(ap), lds, gridDim.x - 1 - blockIdx.x);
+      prefix_body<BF, F8, D>(reload(ap), lds, one ? block - own : grid - 1 - block, common);
     else
-      attend_body<BF, F8, D, RT, SH, true>(reload(ap), lds, blockIdx.x);
+      attend_body<BF, F8, D, RT, SH, true>(reload(ap), lds, block, own);
     __syncthreads();
   }
 }
@@ -505,7 +581,7 @@ __global__ __launch_bounds__(256, 2) void shared_kernel(AttendArgs) {
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256, 1) void prefix_kernel(AttendArgs) {
   extern __shared__ __align__(16) uint8_t lds[];
-  prefix_body<BF, F8, D>(kern_args(), lds, blockIdx.x);
+  prefix_body<BF, F8, D>(kern_args(), lds, blockIdx.x, gridDim.x);
 }
 
 template <bool BF, bool F8, int D, int RT, bool SH>
