@@ -997,13 +997,14 @@ __device__ __forceinline__ PrefixPlan prefix_plan(Args &a) {
   return p;
 }
 
-// Where part `i` of a row is; below 0 if it has fewer.
+// Where a row's first part is, and how many it has; the next are a.pre_rows
+// further on.
 template <class Args>
-__device__ __forceinline__ int64_t prefix_part(Args &a, const PrefixPlan &p, int h, int row, int i) {
-  const int item = h * a.pre_tiles + row / a.pre_rows;
+__device__ __forceinline__ int64_t prefix_parts(Args &a, const PrefixPlan &p, int h, int row, int *count) {
+  const int tile = (int)((uint32_t)row / (uint32_t)a.pre_rows), item = h * a.pre_tiles + tile;
   const uint32_t g0 = (uint32_t)item * (uint32_t)p.n;
-  if (i > (int)((g0 + p.n - 1) / p.per - g0 / p.per)) return -1;
-  return ((int64_t)item * a.pre_most + i) * a.pre_rows + row % a.pre_rows;
+  *count = p.n ? (int)((g0 + p.n - 1) / (uint32_t)p.per - g0 / (uint32_t)p.per) + 1 : 0;
+  return (int64_t)item * a.pre_most * a.pre_rows + row - tile * a.pre_rows;
 }
 
 // Joins the parts of the items that several workgroups shared.  A team of D / 4
@@ -1039,18 +1040,23 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
     float m = kNegInf, l = 0.0f;
     f32x4_t acc = {0, 0, 0, 0};
     if (row < rows) {
+      int has = parts, prefix = 0;
+      int64_t prefix_at = 0;
+      if constexpr (PRE) {
+        prefix_at = prefix_parts(a, pre, h, first_row + row, &prefix);
+        has = own + prefix;
+      }
 #pragma unroll 4
-      for (int i = sub; i < parts; i += per_row) {
+      for (int i = sub; i < has; i += per_row) {
         int64_t at = (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * item_rows + row;
         const float *ml = a.ml, *part = a.part;
         if constexpr (PRE) {
+          // (selected, not branched to: the loads of several parts are on their way)
+          const bool common = i >= own;
           if (own == 1) at = (2 * (int64_t)a.workgroups + blockIdx.x) * item_rows + row;
-          if (i >= own) {
-            at = prefix_part(a, pre, h, first_row + row, i - own);
-            if (at < 0) continue;
-            ml = a.pre_ml;
-            part = a.pre_part;
-          }
+          at = common ? prefix_at + (int64_t)(i - own) * a.pre_rows : at;
+          ml = common ? a.pre_ml : ml;
+          part = common ? a.pre_part : part;
         }
         const float m2 = ml[at * 2], l2 = ml[at * 2 + 1];
         const f32x4_t y = *reinterpret_cast<const f32x4_t *>(part + at * D + d);
