@@ -7,12 +7,12 @@
 // of them): rows of one adapter, wherever they are among the T, make tiles of
 // 16, 32 or 64 and go through the matrix units together.  Two launches: the
 // first product with K cut over workgroups, whose partial sums the second adds
-// up in order.  Each wave finds the rows of its tile by itself, by ballots over
-// the adapters of all rows (512 at most in a call of the kernels).
+// up in order.  Each workgroup finds the rows of its tile by itself among the
+// adapters of all rows (512 at most in a call of the kernels).
 //
-// The sums of the first product enter the second as two parts, each in the
-// weights' type (hi + lo, 16 to 22 bits of the value); in fp16 a row is scaled
-// by a power of two first, so that its largest sum is near 2^14.
+// The sums of the first product enter the second in parts of the weights' type,
+// three in bf16 and two in fp16, which have all their 24 bits (fp16: 22 of the
+// row's largest, for which the row is scaled by a power of two first).
 
 #include <algorithm>
 #include <type_traits>
@@ -79,63 +79,169 @@ __device__ __forceinline__ int find_rows(const int32_t *adapter, int T, int n, b
   }
 }
 
+// The same by the whole workgroup for more rows, of at most kMapped adapters: a
+// bit for each row and adapter in LDS, whose counts give the tiles (adapters in
+// their own order).  64 adapters among 512 rows: one pass of some steps where the
+// ballots above take one for each adapter before the tile's.
+constexpr int kMapped = 256;
+
+__device__ int find_rows_mapped(const int32_t *adapter, int T, int n, bool rest, int tile, int size,
+                                uint32_t (*map)[kAdaptRows / 32], int *words, int *rows, int *which) {
+  constexpr int W = kAdaptRows / 32;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int total = n + 1;  // the last: rows without an adapter
+  int mine[kAdaptRows / 256];
+#pragma unroll
+  for (int i = 0; i < kAdaptRows / 256; ++i) {
+    const int t = i * 256 + tid;
+    mine[i] = t < T ? adapter[t] : -1;
+    mine[i] = (uint32_t)mine[i] < (uint32_t)n ? mine[i] : t < T && rest ? n : -1;
+  }
+  for (int i = tid; i < total * W; i += 256) (&map[0][0])[i] = 0;
+  if (tid == 0) words[4] = -1;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAdaptRows / 256; ++i) {
+    const int t = i * 256 + tid;
+    if (mine[i] >= 0) atomicOr(&map[mine[i]][t >> 5], 1u << (t & 31));
+  }
+  __syncthreads();
+  // thread a has adapter a, and thread 0 the last besides
+  int count = 0, last = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (tid < n) count += __popc(map[tid][i]);
+    last += __popc(map[n][i]);
+  }
+  const int tiles = (count + size - 1) / size;
+  int in = tiles;  // sums over the lanes up to each
+  in += __builtin_amdgcn_update_dpp(0, in, 0x111, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x112, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x114, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x118, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x142, 0xA, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x143, 0xC, 0xF, false);
+  if (lane == 63) words[wave] = in;
+  __syncthreads();
+  const int w0 = words[0], w1 = words[1], w2 = words[2], w3 = words[3], all = w0 + w1 + w2 + w3;
+  const int before = in - tiles + (wave > 0 ? w0 : 0) + (wave > 1 ? w1 : 0) + (wave > 2 ? w2 : 0);
+  if (tile >= before && tile < before + tiles) {
+    words[4] = tid;
+    words[5] = tile - before;
+    words[6] = count;
+  }
+  if (tid == 0 && tile >= all && tile < all + (last + size - 1) / size) {
+    words[4] = n;
+    words[5] = tile - all;
+    words[6] = last;
+  }
+  __syncthreads();
+  const int a = words[4], first = words[5] * size, rows_of = words[6];
+  if (a < 0) return 0;
+#pragma unroll
+  for (int i = 0; i < kAdaptRows / 256; ++i) {
+    if (mine[i] != a) continue;
+    const int t = i * 256 + tid;
+    int rank = -first;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const uint32_t below = k < (t >> 5) ? ~0u : k == (t >> 5) ? (1u << (t & 31)) - 1 : 0u;
+      rank += __popc(map[a][k] & below);
+    }
+    if (rank >= 0 && rank < size) rows[rank] = t;
+  }
+  __syncthreads();
+  *which = a == n ? -1 : a;
+  return min(rows_of - first, size);
+}
+
+// Either, with the rows where each wave finds them; `scratch` is free afterwards.
+constexpr size_t kMapBytes = (kMapped + 1) * (kAdaptRows / 8) + 32;
+
+template <int NC, int S>
+__device__ __forceinline__ int find(const AdaptArgs &a, bool rest, int lane, int wave, uint8_t *scratch, int *rows,
+                                    int *which) {
+  if constexpr (NC > 1) {
+    if (a.n <= kMapped)
+      return find_rows_mapped(a.adapter, a.T, a.n, rest, blockIdx.x, S,
+                              reinterpret_cast<uint32_t(*)[kAdaptRows / 32]>(scratch + 32),
+                              reinterpret_cast<int *>(scratch), rows, which);
+  }
+  return find_rows<NC>(a.adapter, a.T, a.n, rest, blockIdx.x, S, lane, rows + wave * S, which);
+}
+
 // First product: part[split][t][i] = sum over the split's k of A[i][k] x[t][k].
-// The waves of a workgroup cut its K once more and add up through LDS.
-template <bool BF, int NC, int RT>
+// A wave takes RK tiles of 16 ranks; the waves of a workgroup cut its K once more
+// and add up through LDS.
+template <bool BF, int NC, int RT, int RK>
 __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs a) {
-  __shared__ int rows[4][16 * RT];
-  __shared__ f32x4_t sums[3][RT][64];
+  __shared__ int all_rows[4 * 16 * RT];
+  __shared__ f32x4_t sums[3][RT * RK][64];
+  __shared__ __align__(16) uint8_t scratch[NC > 1 ? kMapBytes : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   int which = -1;
-  const int count =
-      __builtin_amdgcn_readfirstlane(find_rows<NC>(a.adapter, a.T, a.n, false, blockIdx.x, 16 * RT, lane, rows[wave], &which));
+  const int count = __builtin_amdgcn_readfirstlane(find<NC, 16 * RT>(a, false, lane, wave, scratch, all_rows, &which));
   if (count == 0) return;
+  const int *const rows = NC > 1 && a.n <= kMapped ? all_rows : all_rows + wave * (16 * RT);
   which = __builtin_amdgcn_readfirstlane(which);
   const int steps = (a.K + 31) / 32, waves = a.splits * 4;
   const int per = (steps + waves - 1) / waves;
   const int s0 = (blockIdx.y * 4 + wave) * per, s1 = min(s0 + per, steps);
-  const uint8_t *xr[RT];
+  const int r0 = blockIdx.z * (16 * RK);
+  const uint8_t *xr[RT], *ar[RK];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) xr[i] = a.x + (int64_t)rows[wave][min(i * 16 + c, count - 1)] * a.x_row * 2;
-  const int r0 = blockIdx.z * 16;
-  const uint8_t *const ar = a.a + ((int64_t)which * a.r + min(r0 + c, a.r - 1)) * a.K * 2;
-  f32x4_t acc[RT];
+  for (int i = 0; i < RT; ++i) xr[i] = a.x + (int64_t)rows[min(i * 16 + c, count - 1)] * a.x_row * 2;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
-  constexpr int U = 4;  // steps whose loads are on their way together
+  for (int i = 0; i < RK; ++i) ar[i] = a.a + ((int64_t)which * a.r + min(r0 + i * 16 + c, a.r - 1)) * a.K * 2;
+  f32x4_t acc[RT][RK];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < RK; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+  // steps whose loads are on their way together
+  constexpr int U = RT + RK <= 2 ? 8 : RT + RK <= 5 ? 4 : 2;
   for (int s = s0; s < s1; s += U) {
-    u32x4_t w[U], x[U][RT];
+    u32x4_t w[U][RK], x[U][RT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = (s + u) * 32 + g * 8;
       const bool in = (s + u < s1) & (k < a.K);
       const int64_t at = in ? 2 * (int64_t)k : 0;
       const uint32_t keep = in ? ~0u : 0u;
-      w[u] = *reinterpret_cast<const u32x4_t *>(ar + at) & keep;
+#pragma unroll
+      for (int j = 0; j < RK; ++j) w[u][j] = *reinterpret_cast<const u32x4_t *>(ar[j] + at) & keep;
 #pragma unroll
       for (int i = 0; i < RT; ++i) x[u][i] = *reinterpret_cast<const u32x4_t *>(xr[i] + at) & keep;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i] = mfma_16x16x32<BF>(w[u], x[u][i], acc[i]);  // lane (c, g): row c, ranks 4 g ..
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < RK; ++j)
+          acc[i][j] = mfma_16x16x32<BF>(w[u][j], x[u][i], acc[i][j]);  // lane (c, g): row c, ranks 4 g ..
   }
   if (wave > 0)
 #pragma unroll
-    for (int i = 0; i < RT; ++i) sums[wave - 1][i][lane] = acc[i];
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < RK; ++j) sums[wave - 1][i * RK + j][lane] = acc[i][j];
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int w = 0; w < 3; ++w)
+    for (int j = 0; j < RK; ++j) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][k] += sums[w][i][lane][k];
-    if (i * 16 + c < count && r0 + g * 4 < a.r)
-      *reinterpret_cast<f32x4_t *>(a.part + ((int64_t)blockIdx.y * a.T + rows[0][i * 16 + c]) * a.r + r0 + g * 4) = acc[i];
-  }
+      for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][j][k] += sums[w][i * RK + j][lane][k];
+      const int r = r0 + j * 16 + g * 4;
+      if (i * 16 + c < count && r < a.r)
+        *reinterpret_cast<f32x4_t *>(a.part + ((int64_t)blockIdx.y * a.T + rows[i * 16 + c]) * a.r + r) = acc[i][j];
+    }
 }
 
 typedef float f32x4_free_t __attribute__((ext_vector_type(4), aligned(4)));
@@ -146,23 +252,59 @@ template <bool BF, int NC, int RT, int STEPS>
 __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs a) {
   constexpr int S = 16 * RT, NB = STEPS > 2 ? 2 : 4;
   constexpr int W = STEPS * 32 + 8;  // values of a row in LDS: 16 bytes past whole banks
+  constexpr int PARTS = BF ? 3 : 2;
   extern __shared__ __align__(16) uint8_t lds[];  // rows of each wave's tile, what a row's sums are scaled by, the sums
-  int(*const rows)[S] = reinterpret_cast<int(*)[S]>(lds);
+  int *const all_rows = reinterpret_cast<int *>(lds);
   float *const back = reinterpret_cast<float *>(lds + 16 * S);
-  uint16_t *const hi = reinterpret_cast<uint16_t *>(lds + 20 * S), *const lo = hi + S * W;
+  uint16_t *const sums = reinterpret_cast<uint16_t *>(lds + 20 * S);  // [PARTS][S][W]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   int which = -1;
-  const int count = __builtin_amdgcn_readfirstlane(
-      find_rows<NC>(a.adapter, a.T, a.n, a.out != a.y, blockIdx.x, S, lane, rows[wave], &which));
+  const int count = __builtin_amdgcn_readfirstlane(find<NC, S>(a, a.out != a.y, lane, wave, lds + 20 * S, all_rows, &which));
   if (count == 0) return;
+  const int *const rows = NC > 1 && a.n <= kMapped ? all_rows : all_rows + wave * S;
   which = __builtin_amdgcn_readfirstlane(which);
+  // lane (c, g) has row c of each 16, columns n0 + 16 j + 4 g ..: of y, and of B
+  // the rows n0 + 16 j + c
+  const uint8_t *const b = a.b + (int64_t)max(which, 0) * a.N * a.r * 2;
+  const int blocks = (a.N + NB * 16 - 1) / (NB * 16);
+  f32x4_free_t y[RT][NB];
+  u32x4_t w[NB][STEPS];
+  auto load = [&](int n) {
+    const int n0 = n * (NB * 16);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const float *const p = a.y + rows[min(i * 16 + c, count - 1)] * a.y_row;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int col = n0 + j * 16 + g * 4;
+        if (col + 4 <= a.N) {
+          y[i][j] = *reinterpret_cast<const f32x4_free_t *>(p + col);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[i][j][k] = p[min(col + k, a.N - 1)];
+        }
+      }
+    }
+    if (which < 0) return;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int k = s * 32 + g * 8;
+        w[j][s] = *reinterpret_cast<const u32x4_t *>(
+            b + ((int64_t)min(n0 + j * 16 + c, a.N - 1) * a.r + (k < a.r ? k : 0)) * 2);
+      }
+  };
+  // the first columns, on their way while the sums are put together
+  int n = blockIdx.y * 4 + wave;
+  load(min(n, blocks - 1));
   if (which >= 0) {
     const float scale = a.scales ? a.scales[which] : 1.0f;
     // 16 lanes a row, which cut its ranks
     for (int i = threadIdx.x >> 4; i < S; i += 16) {
-      const float *const p = a.part + (int64_t)rows[wave][min(i, count - 1)] * a.r;
+      const float *const p = a.part + (int64_t)rows[min(i, count - 1)] * a.r;
       constexpr int Q = (STEPS + 1) / 2;  // fours of a lane
       f32x4_t v[Q];
       float most = 0.0f;
@@ -189,67 +331,47 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs a) {
 #pragma unroll
       for (int x = 0; x < Q; ++x) {
         const int k = (x * 16 + c) * 4;
-        float rest[4];
+        if constexpr (!BF)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float value = BF ? v[x][j] : __builtin_amdgcn_ldexpf(v[x][j], up);
-          const float top = BF ? (float)(__bf16)value : (float)(_Float16)value;
-          rest[j] = __builtin_isfinite(top) ? value - top : 0.0f;
-          v[x][j] = top;
-        }
-        if (k < STEPS * 32) {
-          *reinterpret_cast<uint2 *>(hi + i * W + k) = make_uint2(pair_of<BF>(v[x][0], v[x][1]), pair_of<BF>(v[x][2], v[x][3]));
-          *reinterpret_cast<uint2 *>(lo + i * W + k) = make_uint2(pair_of<BF>(rest[0], rest[1]), pair_of<BF>(rest[2], rest[3]));
+          for (int j = 0; j < 4; ++j) v[x][j] = __builtin_amdgcn_ldexpf(v[x][j], up);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+          float top[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            top[j] = BF ? (float)(__bf16)v[x][j] : (float)(_Float16)v[x][j];
+            v[x][j] = __builtin_isfinite(top[j]) ? v[x][j] - top[j] : 0.0f;
+          }
+          if (k < STEPS * 32)
+            *reinterpret_cast<uint2 *>(sums + (q * S + i) * W + k) = make_uint2(pair_of<BF>(top[0], top[1]), pair_of<BF>(top[2], top[3]));
         }
       }
       if (c == 0) back[i] = BF ? scale : __builtin_amdgcn_ldexpf(scale, -up);
     }
     __syncthreads();
   }
-  // lane (c, g) has row c of each 16, columns n0 + 16 j + 4 g ..
-  const uint8_t *const b = a.b + (int64_t)max(which, 0) * a.N * a.r * 2;
-  const int blocks = (a.N + NB * 16 - 1) / (NB * 16);
-  for (int n = blockIdx.y * 4 + wave; n < blocks; n += gridDim.y * 4) {
+  while (n < blocks) {
     const int n0 = n * (NB * 16);
-    f32x4_free_t y[RT][NB];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const float *const p = a.y + rows[wave][min(i * 16 + c, count - 1)] * a.y_row;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int col = n0 + j * 16 + g * 4;
-        if (col + 4 <= a.N) {
-          y[i][j] = *reinterpret_cast<const f32x4_free_t *>(p + col);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[i][j][k] = p[min(col + k, a.N - 1)];
-        }
-      }
-    }
     if (which >= 0) {
-      u32x4_t w[NB][STEPS];
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+      for (int s = 0; s < STEPS; ++s) {
+        const uint32_t keep = s * 32 + g * 8 < a.r ? ~0u : 0u;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          const int k = s * 32 + g * 8;
-          const uint32_t keep = k < a.r ? ~0u : 0u;
-          w[j][s] = *reinterpret_cast<const u32x4_t *>(b + ((int64_t)min(n0 + j * 16 + c, a.N - 1) * a.r + (k < a.r ? k : 0)) * 2) & keep;
-        }
+        for (int j = 0; j < NB; ++j) w[j][s] &= keep;
+      }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         f32x4_t acc[NB];
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          const int at = (i * 16 + c) * W + s * 32 + g * 8;
-          const u32x4_t h = *reinterpret_cast<const u32x4_t *>(hi + at), l = *reinterpret_cast<const u32x4_t *>(lo + at);
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-          for (int j = 0; j < NB; ++j) acc[j] = mfma_16x16x32<BF>(w[j][s], h, acc[j]);
+          for (int q = 0; q < PARTS; ++q) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t *>(sums + (q * S + i * 16 + c) * W + s * 32 + g * 8);
 #pragma unroll
-          for (int j = 0; j < NB; ++j) acc[j] = mfma_16x16x32<BF>(w[j][s], l, acc[j]);
-        }
+            for (int j = 0; j < NB; ++j) acc[j] = mfma_16x16x32<BF>(w[j][s], v, acc[j]);
+          }
         const float f = back[i * 16 + c];
 #pragma unroll
         for (int j = 0; j < NB; ++j)
@@ -260,7 +382,7 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs a) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       if (i * 16 + c >= count) continue;
-      float *const p = a.out + rows[wave][i * 16 + c] * a.out_row;
+      float *const p = a.out + rows[i * 16 + c] * a.out_row;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int col = n0 + j * 16 + g * 4;
@@ -273,12 +395,14 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs a) {
         }
       }
     }
+    n += gridDim.y * 4;
+    if (n < blocks) load(n);
   }
 }
 
 template <bool BF, int NC, int RT, int STEPS>
 int launch_adapt_up(const AdaptArgs &a, hipStream_t stream) {
-  constexpr size_t bytes = (size_t)16 * RT * (20 + 4 * (STEPS * 32 + 8));
+  constexpr size_t bytes = (size_t)16 * RT * 20 + std::max((size_t)16 * RT * 2 * (BF ? 3 : 2) * (STEPS * 32 + 8), NC > 1 ? kMapBytes : 0);
   constexpr int columns = STEPS > 2 ? 128 : 256;  // of a workgroup
   const auto kern = adapt_up_kernel<BF, NC, RT, STEPS>;
   if (bytes > 64 * 1024 && !allow_max_dynamic_lds(reinterpret_cast<const void *>(kern))) return QGEMV_EHIP;
@@ -289,7 +413,12 @@ int launch_adapt_up(const AdaptArgs &a, hipStream_t stream) {
 
 template <bool BF, int NC, int RT>
 int launch_adapt_rt(const AdaptArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT>), dim3(a.tiles, a.splits, (a.r + 15) / 16), dim3(256), 0, stream, a);
+  if (a.rk == 1)
+    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 1>), dim3(a.tiles, a.splits), dim3(256), 0, stream, a);
+  else if (a.rk == 2)
+    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 2>), dim3(a.tiles, a.splits), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 4>), dim3(a.tiles, a.splits, (a.r + 63) / 64), dim3(256), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
   return a.r <= 32 ? launch_adapt_up<BF, NC, RT, 1>(a, stream)
          : a.r <= 64 ? launch_adapt_up<BF, NC, RT, 2>(a, stream)
@@ -312,14 +441,18 @@ int launch_adapt_t(const AdaptArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// Workgroups of the first product for each CU, counted as if every tile were there.
+constexpr int kAdaptFill = 4;
+
 int64_t plan_adapt(AdaptArgs *a) {
   const int each = (a->T + a->n - 1) / a->n;  // rows of an adapter, where all have as many
   a->rt = each <= 16 ? 1 : each <= 32 ? 2 : 4;
   const int size = 16 * a->rt;
   // the most tiles: every adapter, and the rows without one, end in a part of one
   a->tiles = std::min(a->T, a->T / size + std::min(a->n + 1, a->T));
-  const int ranks = (a->r + 15) / 16, steps = (a->K + 31) / 32;
-  a->splits = std::max(1, std::min({kAdaptSplits, steps / 8, 4 * device_cu_count() / (a->tiles * ranks)}));
+  a->rk = a->r <= 16 ? 1 : a->r <= 32 ? 2 : 4;
+  const int ranks = (a->r + 16 * a->rk - 1) / (16 * a->rk), steps = (a->K + 31) / 32;
+  a->splits = std::max(1, std::min({kAdaptSplits, steps / 8, kAdaptFill * device_cu_count() / (a->tiles * ranks)}));
   // the most splits: so the size grows with T and r alone
   return (int64_t)4 * kAdaptSplits * a->T * a->r;
 }

@@ -115,6 +115,7 @@ struct AdaptArgs {
   int tiles;   // of rows: the most there can be
   int splits;  // of K
   int rt;      // 16-row tiles of a tile of rows
+  int rk;      // 16-rank tiles of a wave of the first product
 };
 
 struct VerifyArgs {

@@ -13,6 +13,11 @@
 // and in fp32 one in some thousand rows would be decided by rounding.  Without
 // a bias (and without sums over a group) the scores' order is the logits', and
 // nothing rounds at all.
+//
+// Bound by latency and, for thousands of rows, by what a step of the choice
+// costs: a lane sorts its choices once, as 64-bit keys in order, and a step
+// compares the lanes' first ones, by their upper halves in six instructions and by
+// their lower halves only where two lanes share the upper.  MEASURED
 
 #include "qgemv_device.h"
 #include "qgemv_kv.h"
@@ -49,11 +54,62 @@ __device__ __forceinline__ double wave_join(double x, double neutral, F f) {
   x = f(x, shifted<0x143, 0xC>(x, neutral));
   return read_lane(x, 63);
 }
-__device__ __forceinline__ double wave_max(double x) {
-  return wave_join(x, kNone, [](double a, double b) { return a > b ? a : b; });
-}
 __device__ __forceinline__ double wave_sum(double x) {
   return wave_join(x, 0.0, [](double a, double b) { return a + b; });
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false));
+  return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ float wave_max(float x) {  // in the order of unsigned numbers
+  const uint32_t v = __builtin_bit_cast(uint32_t, x);
+  const uint32_t m = wave_max(v >> 31 ? ~v : v | 0x80000000u);
+  return __builtin_bit_cast(float, m >> 31 ? m & 0x7FFFFFFFu : ~m);
+}
+
+// A choice as a number in the same order; 0 for one that is not there.
+__device__ __forceinline__ uint64_t key_of(double x) {
+  const uint64_t v = __builtin_bit_cast(uint64_t, x + 0.0);  // (-0 is 0)
+  return !(x > kNone) ? 0 : v >> 63 ? ~v : v | 1ull << 63;
+}
+// Its last 4 bits make room for the expert's place within its lane, the first
+// largest: choices count as equal within 2^-48 of their value.
+constexpr uint64_t kPlace = 15;
+__device__ __forceinline__ uint64_t placed(uint64_t key, int j) { return key ? (key & ~kPlace) | (kPlace - j) : 0; }
+
+// The largest first: Batcher's odd-even merge sort of V keys (V a power of two).
+template <int V>
+__device__ __forceinline__ void sort_keys(uint64_t (&key)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint64_t a = key[i + j], b = key[i + j + k];
+            key[i + j] = a > b ? a : b;
+            key[i + j + k] = a > b ? b : a;
+          }
+}
+
+// The value of the lane `distance` away, where lanes that lie closer together hold
+// the same already: 1, 2, 4 and 8 by DPP.
+__device__ __forceinline__ double across(double x, int distance) {
+  switch (distance) {
+    case 1: return shifted<0xB1, 0xF>(x, x);   // quad_perm 1 0 3 2
+    case 2: return shifted<0x4E, 0xF>(x, x);   // quad_perm 2 3 0 1
+    case 4: return shifted<0x141, 0xF>(x, x);  // row_half_mirror
+    case 8: return shifted<0x140, 0xF>(x, x);  // row_mirror
+  }
+  return __shfl_xor(x, distance);
 }
 
 template <int DT>
@@ -80,93 +136,109 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     x[j] = e0 + j < E ? logit<DT>(row, e0 + j) : -__builtin_inff();
     top = fmaxf(top, x[j]);  // (a NaN is passed over)
   }
-  // which experts are there: neither -inf nor NaN
-  double score[V], choice[V];
-  if (a.softmax) {
-    const double m = wave_max((double)top);
+  // Scores, a softmax's times their sum, where the choice or the weights need all
+  // of them.
+  const bool by_logit = !a.bias && a.best == 1;
+  const double m = a.softmax ? (double)wave_max(top) : 0.0;
+  double choice[V], total = 1.0;
+  if (!by_logit || (a.softmax && !a.renormalise)) {
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      score[j] = x[j] > -__builtin_inff() ? exp((double)x[j] - m) : 0.0;
-      sum += score[j];
+      choice[j] = a.softmax ? (x[j] > -__builtin_inff() ? exp((double)x[j] - m) : 0.0) : 1.0 / (1.0 + exp(-(double)x[j]));
+      sum += choice[j];
     }
-    sum = wave_sum(sum);
+    if (a.softmax) {
+      total = wave_sum(sum);
+      const double over = 1.0 / total;
 #pragma unroll
-    for (int j = 0; j < V; ++j) score[j] = score[j] / sum;
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) score[j] = 1.0 / (1.0 + exp(-(double)x[j]));
+      for (int j = 0; j < V; ++j) choice[j] *= over;
+    }
   }
-  const bool by_logit = !a.bias && a.best == 1;
+  // the choices' keys, of the experts that are there: neither -inf nor NaN
+  uint64_t key[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const bool there = x[j] > -__builtin_inff();
-    const double c = by_logit ? (double)x[j] : score[j] + (a.bias && e0 + j < E ? (double)a.bias[e0 + j] : 0.0);
-    choice[j] = there && c > kNone ? c : kNone;
+    const double c = by_logit ? (double)x[j] : choice[j] + (a.bias && e0 + j < E ? (double)a.bias[e0 + j] : 0.0);
+    choice[j] = x[j] > -__builtin_inff() && c > kNone ? c : kNone;
+    key[j] = key_of(choice[j]);
   }
 
   if (a.groups > 1) {
-    double *const all = choices + wave * (64 * V);
-#pragma unroll
-    for (int j = 0; j < V; ++j) all[e0 + j] = choice[j];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int size = E / a.groups;
-    // lane g has group g
+    const int size = E / a.groups, lanes = size / V;
+    // lane `at` of a group g has its value
     double first = kNone, second = kNone;
-    if (lane < a.groups) {
-      for (int i = 0; i < size; ++i) {
-        const double c = all[lane * size + i];
-        second = c > first ? first : c > second ? c : second;
-        first = c > first ? c : first;
+    auto take = [&](double c) {
+      second = c > first ? first : c > second ? c : second;
+      first = c > first ? c : first;
+    };
+    int at = 1;
+    if (lanes * V == size && (lanes & (lanes - 1)) == 0) {  // whole lanes, a power of two of them
+      at = lanes;
+#pragma unroll
+      for (int j = 0; j < V; ++j) take(choice[j]);
+      for (int over = 1; over < lanes; over <<= 1) {
+        const double f = across(first, over), s = across(second, over);
+        take(f);
+        take(s);
       }
+    } else {  // lane g reads group g
+      double *const all = choices + wave * (64 * V);
+#pragma unroll
+      for (int j = 0; j < V; ++j) all[e0 + j] = choice[j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (lane < a.groups)
+        for (int i = 0; i < size; ++i) take(all[lane * size + i]);
     }
     const double value = a.best == 2 && second > kNone ? first + second : first;
-    int before = 0;  // groups that come first
+    const uint64_t mine = key_of(value);
+    // lane g: how many groups come before it
+    const uint64_t its = __shfl(mine, min(lane * at, 63)), of_lane = lane < a.groups ? its : 0;
+    int before = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const double other = read_lane(value, g);
-      before += other > value || (other == value && g < lane);
+      const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(of_lane >> 32), g) << 32 |
+                             (uint32_t)__builtin_amdgcn_readlane((uint32_t)of_lane, g);
+      before += other > of_lane || (other == of_lane && g < lane);
     }
-    const uint64_t kept = __ballot(lane < a.groups && before < a.keep && value > kNone);
+    const uint64_t kept = __ballot(lane < a.groups && before < a.keep && of_lane);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int g = min((int)((uint32_t)(e0 + j) / (uint32_t)size), 63);
-      if (!(kept >> g & 1)) choice[j] = kNone;
+      if (!(kept >> g & 1)) key[j] = 0;
     }
   }
 
   // ---- the k of greatest choice, one after another; lane i keeps the i-th
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = placed(key[j], j);
+  sort_keys(key);
   int expert = -1;
-  double weight = 0.0;
   for (int i = 0; i < a.k; ++i) {
-    double best = choice[0], its = score[0];
-    int at = 0;
-#pragma unroll
-    for (int j = 1; j < V; ++j) {
-      const bool more = choice[j] > best;
-      best = more ? choice[j] : best;
-      its = more ? score[j] : its;
-      at = more ? j : at;
+    const uint32_t hi = (uint32_t)(key[0] >> 32), lo = (uint32_t)key[0];
+    const uint32_t most = wave_max(hi);
+    if (most == 0) break;  // none is left
+    uint64_t with = __ballot(hi == most);
+    if (with & (with - 1)) {
+      const uint32_t below = wave_max(hi == most ? lo >> 4 : 0u);
+      with = __ballot(hi == most && lo >> 4 == below);
     }
-    const double most = wave_max(best);
-    if (!(most > kNone)) break;  // none is left
-    const int from = (int)__ffsll((long long)__ballot(best == most)) - 1;
-    const int e = __builtin_amdgcn_readlane(e0 + at, from);
-    const double w = read_lane(its, from);
-    if (lane == i) {
-      expert = e;
-      weight = w;
-    }
+    const int from = (int)__ffsll((long long)with) - 1;
+    const int place = (int)kPlace - (int)(__builtin_amdgcn_readlane(lo, from) & (uint32_t)kPlace);
+    expert = lane == i ? from * V + place : expert;
+    // the lane's next
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (e0 + j == e) choice[j] = kNone;
+    for (int j = 0; j < V; ++j) key[j] = lane != from ? key[j] : j + 1 < V ? key[j + 1] : 0;
   }
-  if (a.renormalise) {
-    const double sum = wave_sum(weight);
-    weight = sum > 0.0 ? weight / sum : sum == 0.0 ? 0.0 : weight / sum;
+  double weight = 0.0;
+  if (lane < a.k && expert >= 0) {
+    const double v = (double)logit<DT>(row, expert);
+    weight = a.softmax ? exp(v - m) : 1.0 / (1.0 + exp(-v));
   }
+  if (a.renormalise) total = wave_sum(weight);
   if (lane < a.k) {
     a.experts[(int64_t)t * a.k + lane] = expert;
-    a.weights[(int64_t)t * a.k + lane] = (float)(weight * (double)a.scale);
+    a.weights[(int64_t)t * a.k + lane] =
+        expert < 0 || total == 0.0 ? 0.0f : (float)(weight / total * (double)a.scale);
   }
 }
 

@@ -516,8 +516,8 @@ int qgemv_route(const void *logits, int64_t row, int dtype, const float *bias, i
  *           enough for every smaller T and r; not shared by calls that may run
  *           at the same time.
  * x, a, b 16-byte aligned.  Products of 16-bit values are summed in fp32; the
- * rank's sums enter the second product as two 16-bit parts (a relative error of
- * 2^-17 of each in bf16, in fp16 2^-23 of the row's largest).  Deterministic, and
+ * rank's sums enter the second product in 16-bit parts that have their 24 bits
+ * (in fp16 22 bits of the row's largest).  Deterministic, and
  * a row's result does not depend on the other rows' values.  2^24 rows are
  * too many.
  */
