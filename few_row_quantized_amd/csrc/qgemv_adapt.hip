@@ -84,9 +84,10 @@ __device__ __forceinline__ int find_rows(const int32_t *adapter, int T, int n, b
 // their own order).  64 adapters among 512 rows: one pass of some steps where the
 // ballots above take one for each adapter before the tile's.
 constexpr int kMapped = 256;
+constexpr int kMapRow = kAdaptRows / 32 + 1;  // words of an adapter, one to spare: threads of neighbours in different banks
 
 __device__ int find_rows_mapped(const int32_t *adapter, int T, int n, bool rest, int tile, int size,
-                                uint32_t (*map)[kAdaptRows / 32], int *words, int *rows, int *which) {
+                                uint32_t (*map)[kMapRow], int *words, int *rows, int *which) {
   constexpr int W = kAdaptRows / 32;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int total = n + 1;  // the last: rows without an adapter
@@ -97,7 +98,7 @@ __device__ int find_rows_mapped(const int32_t *adapter, int T, int n, bool rest,
     mine[i] = t < T ? adapter[t] : -1;
     mine[i] = (uint32_t)mine[i] < (uint32_t)n ? mine[i] : t < T && rest ? n : -1;
   }
-  for (int i = tid; i < total * W; i += 256) (&map[0][0])[i] = 0;
+  for (int i = tid; i < total * kMapRow; i += 256) (&map[0][0])[i] = 0;
   if (tid == 0) words[4] = -1;
   __syncthreads();
 #pragma unroll
@@ -156,7 +157,7 @@ __device__ int find_rows_mapped(const int32_t *adapter, int T, int n, bool rest,
 }
 
 // Either, with the rows where each wave finds them; `scratch` is free afterwards.
-constexpr size_t kMapBytes = (kMapped + 1) * (kAdaptRows / 8) + 32;
+constexpr size_t kMapBytes = ((kMapped + 1) * kMapRow * 4 + 32 + 15) / 16 * 16;
 
 template <int NC, int S>
 __device__ __forceinline__ int find(const AdaptArgs &a, bool rest, int lane, int wave, uint8_t *scratch, int *rows,
@@ -164,7 +165,7 @@ __device__ __forceinline__ int find(const AdaptArgs &a, bool rest, int lane, int
   if constexpr (NC > 1) {
     if (a.n <= kMapped)
       return find_rows_mapped(a.adapter, a.T, a.n, rest, blockIdx.x, S,
-                              reinterpret_cast<uint32_t(*)[kAdaptRows / 32]>(scratch + 32),
+                              reinterpret_cast<uint32_t(*)[kMapRow]>(scratch + 32),
                               reinterpret_cast<int *>(scratch), rows, which);
   }
   return find_rows<NC>(a.adapter, a.T, a.n, rest, blockIdx.x, S, lane, rows + wave * S, which);
@@ -442,7 +443,7 @@ int launch_adapt_t(const AdaptArgs &a, hipStream_t stream) {
 }  // namespace
 
 // Workgroups of the first product for each CU, counted as if every tile were there.
-constexpr int kAdaptFill = 4;
+constexpr int kAdaptFill = 1;
 
 int64_t plan_adapt(AdaptArgs *a) {
   const int each = (a->T + a->n - 1) / a->n;  // rows of an adapter, where all have as many
