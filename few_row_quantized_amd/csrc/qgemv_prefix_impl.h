@@ -1,23 +1,42 @@
 // Attention of all sequences' rows over the tokens that they have in common.
 //
 // A batch whose sequences begin with the same pages reads them once: the rows
-// of all sequences, T G of them for a key-value head, are one product against
+// of all sequences, R = T G of them for a key-value head, are one product against
 // the common tokens,
 //
 //   m = max_j s_j,  l = sum_j 2^(s_j - m),  o = sum_j 2^(s_j - m) v_j,
 //   s_j = scale * k_scale[h] * log2(e) * (q . k_j),
 //
 // which is joined with what each sequence's own tokens give (qgemv_attend_impl.h,
-// PRE).  4 R D flops for 4 D bytes of cache, R in the hundreds or thousands: the
-// matrix units bound it, not the memory.
+// PRE).  4 R D flops for 4 D bytes of a token's keys and values, R in the hundreds
+// or thousands: the matrix units bound it, not the memory.
+//
+// A workgroup has 128 rows of a head, 32 a wave, and goes over granules of 64
+// tokens.  Scores are taken as S^T = K Q^T, which leaves a query row in a lane, so
+// that its maximum, its sum and its weights need no exchange but one with the lane
+// 32 away, and the weights are in registers as the second product, O^T = V^T P^T,
+// wants them; the queries stay in registers too.  Keys and values go through the
+// LDS, once for four waves.
+//
+// 64 sequences of up to 8 rows, 8 heads of 6 query heads over 16384 common tokens
+// of D = 128 and 500..2000 of their own, bf16: 306 us, where 190 GFLOP at the rate
+// of a product of 16384^3 would take 137.  What bounds it is waiting between two
+// products, for the LDS and for exponentials, with two waves of a SIMD: 256
+// registers of each hold 64 sums, 32 scores and 32 queries.  Without the
+// exponentials, the reads of the LDS or the loads, each by itself, it would take
+// less than a tenth off.
 #pragma once
+
+#include <type_traits>
 
 #include "qgemv_attend_impl.h"
 
 namespace qgemv {
 
+template <int N>
+using Const = std::integral_constant<int, N>;
+
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 template <bool BF>
 __device__ __forceinline__ f32x16_t mfma_32x32x16(u32x4_t a, u32x4_t b, f32x16_t c) {
@@ -54,7 +73,6 @@ __device__ __forceinline__ int wave_least(int x) {
 
 constexpr int kPrefixRows = 128;   // of an item: 32 a wave
 constexpr int kPrefixTokens = 64;  // of a granule
-constexpr int kOrder = 1;
 constexpr int prefix_occupancy(int D) { return D == 256 ? 1 : 2; }  // workgroups of a CU
 
 // LDS of a workgroup: positions of the rows and the reductions, then keys of two
@@ -65,6 +83,40 @@ constexpr int kPrefixHead = 1024 + 4096;  // the latter: each wave's places of t
 constexpr int key_row(int D) { return 2 * D + 16; }
 constexpr int value_row(int D) { return 2 * D + 64; }
 constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)2 * kPrefixTokens * (key_row(D) + value_row(D)); }
+
+// 16-bit caches at D = 128 are loaded straight to the LDS, 4 tokens and 1 KiB an
+// instruction, so rows lie together in fours with 16 bytes after them, and a row's
+// quarters of 64 bytes are exchanged by the token's place in its four: lanes read
+// different banks as above.  (The case above: 314 -> 306 us; a head of D = 128 over
+// 64 sequences of 1 row: 46.6 -> 43.1.)  Rows of D = 64 and D = 256 through
+// registers, as E4M3 has to be, which is widened on the way.
+constexpr int kFour = 4 * 256 + 16;
+
+// Operands of four matrix instructions, 8 tokens of one d a lane, out of rows of
+// values in the LDS: each of the reads turns 4 tokens by 16 d.  All are on their way
+// together, and waited for here: as builtins they were each waited for on their
+// own, and for loads from the memory to the LDS as well.
+template <int OFFSET, int EIGHT>
+__device__ __forceinline__ void read_turned(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, u32x4_t *to) {
+  uint64_t x0, y0, x1, y1, x2, y2, x3, y3;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x0), "=&v"(y0), "=&v"(x1), "=&v"(y1), "=&v"(x2), "=&v"(y2), "=&v"(x3), "=&v"(y3)
+      : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "i"(OFFSET), "i"(OFFSET + EIGHT)
+      : "memory");
+  to[0] = u32x4_t{(uint32_t)x0, (uint32_t)(x0 >> 32), (uint32_t)y0, (uint32_t)(y0 >> 32)};
+  to[1] = u32x4_t{(uint32_t)x1, (uint32_t)(x1 >> 32), (uint32_t)y1, (uint32_t)(y1 >> 32)};
+  to[2] = u32x4_t{(uint32_t)x2, (uint32_t)(x2 >> 32), (uint32_t)y2, (uint32_t)(y2 >> 32)};
+  to[3] = u32x4_t{(uint32_t)x3, (uint32_t)(x3 >> 32), (uint32_t)y3, (uint32_t)(y3 >> 32)};
+}
 
 // The first token that a row's window can reach: of the sequence with the lowest
 // position.  (The workgroup's threads together; 4 words of LDS.)
@@ -106,17 +158,19 @@ template <bool BF, bool F8, int D>
 __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, const int index, const int workgroups) {
   constexpr int TOK = kPrefixTokens, C = D / 8, DB = D / 32, QS = D / 16;
   constexpr int L = TOK * C / 256;  // chunks of a thread, of keys and of values
+  constexpr bool DIRECT = D == 128 && !F8;
   constexpr int KR = key_row(D), VR = value_row(D);
+  constexpr int KT = DIRECT ? TOK / 4 * kFour : TOK * KR, VT = DIRECT ? TOK / 4 * kFour : TOK * VR;  // bytes of a tile
   // Exponentials placed between matrix instructions by hand, part by part: left to
   // itself the compiler takes registers past the limit at D = 128 (queries spilled,
   // each reload a wait for all loads in flight); at D = 64, where there are enough,
   // its own order is better (a window of 4096, 16 rows: 60 us, 65 by hand).
-  constexpr bool ORDER = kOrder && D == 128;
+  constexpr bool ORDER = D == 128;
   constexpr int CB = F8 ? 1 : 2;
   int *const row_pos = reinterpret_cast<int *>(lds);        // [128] rows of T
   int *const bounds = reinterpret_cast<int *>(lds + 512);   // of each wave: smallest end, largest begin; then strays
   int64_t *const ring = reinterpret_cast<int64_t *>(lds + 1024) + (threadIdx.x >> 6) * 128;
-  uint8_t *const keys = lds + kPrefixHead, *const values = keys + 2 * TOK * KR;
+  uint8_t *const keys = lds + kPrefixHead, *const values = keys + 2 * KT;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -262,6 +316,34 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
         }
       }
     };
+    // the same straight to a tile's place in the LDS
+    auto fetch_rows = [&](const uint8_t *from, const Places &at, uint8_t *to) {
+      const int me = anew(lane), within = ((me & 15) ^ (me >> 4) * 4) * 16;
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(from + at[i] + within),
+                                         (__attribute__((address_space(3))) void *)(to + (i * 4 + wave) * kFour), 16, 0, 0);
+    };
+    // and the values of one that some row does not see some tokens of (as below)
+    auto clean_values = [&](int tile, uint64_t present) {
+      const int me = anew(tid);
+      u32x4_t *const at = reinterpret_cast<u32x4_t *>(values + (tile & 1) * VT + wave * kFour + (me & 63) * 16);
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const uint32_t ok = 0u - (uint32_t)(present >> (i * 16 + me / 16) & 1);
+        u32x4_t v = at[i * (4 * kFour / 16)];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          v[x] &= ok;
+          odd |= nonfinite_signs<BF, false>(v[x]);
+          v[x] &= ~nonfinite<BF, false>(v[x]);
+        }
+        at[i * (4 * kFour / 16)] = v;
+      }
+      if ((odd & kSigns<false>) != 0) bounds[8] = 1;
+      __syncthreads();
+    };
     auto widen = [](u32x4_t x) -> u32x4_t {
       if constexpr (!F8) return x;
       return u32x4_t{e4m3_pair<BF, false>(x[0]), e4m3_pair<BF, true>(x[0]), e4m3_pair<BF, false>(x[1]),
@@ -269,7 +351,7 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     };
     auto store_keys = [&](int tile, const u32x4_t (&from)[L]) {
       const int me = anew(tid);
-      uint8_t *const to = keys + (tile & 1) * (TOK * KR) + me / C * KR + me % C * 16;
+      uint8_t *const to = keys + (tile & 1) * KT + me / C * KR + me % C * 16;
 #pragma unroll
       for (int i = 0; i < L; ++i) *reinterpret_cast<u32x4_t *>(to + i * (256 / C) * KR) = widen(from[i]);
     };
@@ -278,7 +360,7 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     // are given to the rows that see them after the tiles.
     auto store_values = [&](int tile, bool edge, uint64_t present) {
       const int me = anew(tid);
-      uint8_t *const to = values + (tile & 1) * (TOK * VR) + me / C * VR + me % C * 16;
+      uint8_t *const to = values + (tile & 1) * VT + me / C * VR + me % C * 16;
       if (edge) {
         uint32_t odd = 0;
 #pragma unroll
@@ -312,11 +394,14 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     u32x4_t p[2][2];  // their weights, as operands of the second product
     auto products = [&](int tile, int b) {
       const int me = anew(lane);
-      const uint8_t *const from = keys + (tile & 1) * (TOK * KR) + (me & 31) * KR + (me >> 5) * 16;
+      const uint8_t *const from = keys + (tile & 1) * KT + (me >> 5) * 16 +
+                                  (DIRECT ? (me & 31) / 4 * kFour + (me & 3) * 256 : (me & 31) * KR);
       const f32x16_t none = {};
 #pragma unroll
-      for (int st = 0; st < QS; ++st)
-        s[b] = mfma_32x32x16<BF>(*reinterpret_cast<const u32x4_t *>(from + b * (32 * KR) + st * 32), qf[st], st ? s[b] : none);
+      for (int st = 0; st < QS; ++st) {
+        const int to = DIRECT ? b * (8 * kFour) + ((st / 2 ^ (me & 3)) * 64) + st % 2 * 32 : b * (32 * KR) + st * 32;
+        s[b] = mfma_32x32x16<BF>(*reinterpret_cast<const u32x4_t *>(from + to), qf[st], st ? s[b] : none);
+      }
     };
     // Weights leave fp32 for the matrix product: half a step of q's type each, as
     // in the attention over a sequence's own tokens.
@@ -337,20 +422,35 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     };
     // Half a tile's values by their weights; a lane's operand is 8 tokens of one d,
     // turned by the LDS.
-    auto add = [&](int tile, int b) {
-      typedef __attribute__((address_space(3))) s16x4_t LdsQuad;
+    auto add = [&](int tile, auto which) {
+      constexpr int b = decltype(which)::value;
       const int me = anew(lane);
-      uint8_t *const from = values + (tile & 1) * (TOK * VR) + (4 * (me >> 5) + (me & 15) / 4) * VR +
-                            (me >> 4 & 1) * 32 + (me & 3) * 8;
+      const int place = (me & 15) / 4;  // of the token in its four
+      const uint8_t *const from = values + (tile & 1) * VT + (me >> 4 & 1) * 32 + (me & 3) * 8 +
+                                  (DIRECT ? (me >> 5) * kFour + place * 256 : (4 * (me >> 5) + place) * VR);
+      const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)from;
+      constexpr int FIRST = DIRECT ? b * 8 * kFour : b * 32 * VR;
+      constexpr int NEXT = DIRECT ? 4 * kFour : 16 * VR, EIGHT = NEXT / 2;  // 16 tokens, 8 tokens
+      auto d_at = [&](int d) { return at + (DIRECT ? (d ^ place) * 64 : d * 64); };
+      if constexpr (DB == 2) {
+        u32x4_t v[4];
+        read_turned<FIRST, EIGHT>(d_at(0), d_at(1), d_at(0) + NEXT, d_at(1) + NEXT, v);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int i = 0; i < 4; ++i) acc[i & 1] = mfma_32x32x16<BF>(v[i], p[b][i >> 1], acc[i & 1]);
+      } else {
+        auto step = [&](auto part) {
+          constexpr int u = decltype(part)::value;
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          const int to = (b * 32 + u * 16) * VR + d * 64;
-          const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad *)(from + to)));
-          const uint2 y = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad *)(from + to + 8 * VR)));
-          acc[d] = mfma_32x32x16<BF>(u32x4_t{x.x, x.y, y.x, y.y}, p[b][u], acc[d]);
-        }
+          for (int d0 = 0; d0 < DB; d0 += 4) {
+            u32x4_t v[4];
+            read_turned<FIRST + u * NEXT, EIGHT>(d_at(d0), d_at(d0 + 1), d_at(d0 + 2), d_at(d0 + 3), v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[d0 + i] = mfma_32x32x16<BF>(v[i], p[b][u], acc[d0 + i]);
+          }
+        };
+        step(Const<0>{});
+        step(Const<1>{});
+      }
     };
     // Scores of a tile that have no part, and the reference of the weights.
     auto look = [&](int tile, uint64_t present) {
@@ -403,11 +503,35 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     // the values of t - 1 and t; registers bring the keys of t + 2 and the values
     // of t + 1.  One barrier a tile: after it, the keys of t and the values of
     // t - 1 have been read by all, and what was stored in the step before is there.
-    uint64_t there1, there2, there3;  // of t + 1, ..
-    {
+    uint64_t there0, there1, there2, there3;  // of t, t + 1, ..
+    if constexpr (DIRECT) {
+      Places at;
+      there0 = put(t, id);
+      look_up(t, at);
+      fetch_rows(kbase, at, keys + (t & 1) * KT);
+      fetch_rows(vbase, at, values + (t & 1) * VT);
+      there1 = put(t + 1, id_next);
+      look_up(t + 1, at);
+      fetch_rows(kbase, at, keys + (~t & 1) * KT);
+      id = load_id(t + 2);
+      id_next = load_id(t + 3);
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        *reinterpret_cast<u32x4_t *>(values + (~t & 1) * VT + (i * 4 + wave) * kFour + lane * 16) = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) p[1][u] = u32x4_t{0, 0, 0, 0};
+      there2 = put(t + 2, id);
+      id = id_next;
+      there3 = 0;
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+      __syncthreads();
+      products(t, 0);
+      products(t, 1);
+      look(t, there0);
+    } else {
       u32x4_t second[L];
       Places at;
-      const uint64_t there0 = put(t, id);
+      there0 = put(t, id);
       look_up(t, at);
       load_rows(kbase, at, kt);
       load_rows(vbase, at, vt);
@@ -439,7 +563,7 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     }
     do {
       weigh(0);
-      add(t - 1, 1);
+      add(t - 1, Const<1>{});
       if constexpr (ORDER) {
         __builtin_amdgcn_iglp_opt(2);
 #pragma unroll
@@ -450,13 +574,21 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
       }
       Places at2, at3;
       look_up(t + 2, at2);
-      look_up(t + 3, at3);
-      __syncthreads();
-      // (past the last tile: keys and values of the first slot, which nothing reads)
-      store_keys(t + 2, kt);
-      store_values(t + 1, is_edge(tile_base(t + 1), there1), there1);
-      load_rows(kbase, at3, kt);
-      load_rows(vbase, at2, vt);
+      look_up(t + (DIRECT ? 1 : 3), at3);
+      if constexpr (DIRECT) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the keys of t + 1 and the values of t are there
+        __syncthreads();
+        fetch_rows(kbase, at2, keys + (t & 1) * KT);
+        fetch_rows(vbase, at3, values + (~t & 1) * VT);
+        if (is_edge(tile_base(t), there0)) clean_values(t, there0);
+      } else {
+        __syncthreads();
+        // (past the last tile: keys and values of the first slot, which nothing reads)
+        store_keys(t + 2, kt);
+        store_values(t + 1, is_edge(tile_base(t + 1), there1), there1);
+        load_rows(kbase, at3, kt);
+        load_rows(vbase, at2, vt);
+      }
       if constexpr (ORDER) __builtin_amdgcn_sched_barrier(0);
       products(t + 1, 0);
       weigh(1);
@@ -469,15 +601,22 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
       for (int u = 0; u < 2; ++u) asm volatile("" : "+v"(p[1][u]));
       if constexpr (ORDER) __builtin_amdgcn_sched_barrier(0);
       products(t + 1, 1);
-      add(t, 0);
+      add(t, Const<0>{});
       ++t;
       look(t, there1);  // (past the last tile nothing is there)
+      there0 = there1;
       there1 = there2;
-      there2 = there3;
-      there3 = put(t + 3, id);
-      id = load_id(t + 4);
+      if constexpr (DIRECT) {
+        there2 = put(t + 2, id);
+        id = load_id(t + 3);
+      } else {
+        there2 = there3;
+        there3 = put(t + 3, id);
+        id = load_id(t + 4);
+      }
     } while (t < t_end);
-    add(t - 1, 1);
+    if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0x0F70);  // nothing on its way to the LDS any more
+    add(t - 1, Const<1>{});
 
     if (bounds[8]) {
       // The NaNs and infinities of the tiles above, to the rows that see their
