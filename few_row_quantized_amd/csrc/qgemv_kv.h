@@ -99,6 +99,7 @@ struct RouteArgs {
   int32_t *experts;   // [T][k]
   float *weights;     // [T][k]
   int T, E, k, dtype, groups, keep, best;
+  uint32_t over_size;  // floor(2^20 / (E / groups)) + 1: e * over_size >> 20 is e's group
   bool softmax, renormalise;
   float scale;
 };

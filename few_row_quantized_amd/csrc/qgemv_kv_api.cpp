@@ -312,6 +312,7 @@ int qgemv_route(const void *logits, int64_t row, int dtype, const float *bias, i
   a.groups = groups;
   a.keep = keep;
   a.best = groups > 1 ? best : 1;  // of one group nothing depends on it
+  a.over_size = (1u << 20) / (uint32_t)(E / groups) + 1;
   a.softmax = score == QGEMV_SOFTMAX;
   a.renormalise = renormalise != 0;
   a.scale = scale;
