@@ -135,13 +135,30 @@ __device__ __forceinline__ int lowest_token(Args &a, int before, int *lds) {
   return __builtin_amdgcn_readfirstlane(min(max(least - a.window + 1, 0), before));
 }
 
-// Granules of the sequences' own tokens.
+// What workgroups spend, in common granules (us of the cases that change most):
+// a granule of own tokens, in halves (1, 2, 3: 64 sequences of 4 rows over 6000
+// tokens of E4M3 and 0..2500 of their own 137, 104, 106; 16 of 16 rows, D = 64,
+// window 4096, 65, 62, 67);
+constexpr int kOwnCost = 2;
+// an item's start and end, in halves (0, 2, 4, 8: 64 of 8 rows over 4000 and
+// 25..100 of their own 211, 124, 99, 95; 24 of 4 over 6001 of E4M3 and 0..2500
+// 69, 69, 68, 75);
+constexpr int kItemCost = 4;
+// a second item in a range (with ranges always within an item, with ranges always
+// equal, with this: 32 of 4 rows, window 1024, 44, 51, 44; 64 of 8 over 16000 and
+// 25..100 237, 243, 237; for none but equal costs, 0: 244);
+constexpr int kRangeCost = 2;
+// and the walk of a workgroup from which both are long (32 and 72 as 48 within 1 %
+// but for 64 of 8 over 4000 and 500..2000: 141, 136, 137).
+constexpr int kLongWalk = 48;
+
+// What the sequences' own tokens cost, in halves of a common granule.
 template <class Args>
-__device__ __forceinline__ int own_granules(Args &a, int before, int *lds) {
+__device__ __forceinline__ int own_cost(Args &a, int before, int *lds) {
   int sum = 0;
   for (int b = threadIdx.x; b < a.B; b += 256) {
     const SeqWork w = seq_work<true>(a, b, before);
-    sum += w.items * w.granules;
+    sum += w.items * (w.granules * kOwnCost + kItemCost);
   }
   sum += __builtin_amdgcn_update_dpp(0, sum, 0x111, 0xF, 0xF, false);
   sum += __builtin_amdgcn_update_dpp(0, sum, 0x112, 0xF, 0xF, false);
@@ -184,16 +201,14 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
   const int sink_tiles = ap->window ? min((int)(((int64_t)sinks + TOK - 1) / TOK), low_tile) : 0;
   const int n = sink_tiles + all - low_tile;
   const int items = ap->pre_tiles * ap->c.H;
-  // Equal ranges of all items' granules; with workgroups for several parts of
-  // each item, as many for each, so that none walks two (of P workgroups for an
-  // item and the rest of them, at most 1 in P + 1 has nothing to do).
+  // Equal ranges of all items' granules; or as many workgroups for each item, so
+  // that none walks parts of two, where that makes ranges longer by less than a
+  // second start and end cost.
   const int parts = (int)((uint32_t)workgroups / (uint32_t)items);
-  int per, padded = n;
-  if (parts >= 4 && n) {
+  int per = max((items * n + workgroups - 1) / workgroups, 1), padded = n;
+  if (parts && n && (n + parts - 1) / parts <= per + kRangeCost) {
     per = (n + parts - 1) / parts;
     padded = (n + per - 1) / per * per;
-  } else {
-    per = max((items * n + workgroups - 1) / workgroups, 1);
   }
   const int total = items * padded;
   if (index == 0 && tid == 0) {
@@ -673,16 +688,15 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
 
 // The common tokens and the sequences' own in one launch.  Where both are short,
 // each workgroup has one of the two, so that what their walks begin and end with
-// is at the same time (24 sequences over 6001 tokens of E4M3, 0..2500 of their
-// own: 81 -> 68 us): as many for each as their granules cost, measured as times
-// of all workgroups: one of own tokens as much as kOwnCost common ones.  Where
-// they are long, a workgroup takes its range of one, then its range of the other:
-// the first half of them the own tokens first, the second half the common ones,
-// so that of the two workgroups of a CU one is bound by the memory while the
-// other is by the matrix units, and none ends early.
-constexpr int kOwnCost = 2;     // half common granules
-constexpr int kLongWalk = 48;   // of a workgroup, in common granules
-
+// is at the same time: as many for each as its cost is of all.  Where they are
+// long, a workgroup takes its range of one, then its range of the other: the first
+// half of them the own tokens first, the second half the common ones, so that of
+// the two workgroups of a CU one is bound by the memory while the other is by the
+// matrix units, and none ends early.  (Separate, in turn, us: 24 sequences of 4
+// rows over 6001 tokens of E4M3 and 0..2500 of their own 69 and 84; 32 of 4 over
+// 1000 and 500..2000 48 and 59; 64 of 8 over 16000 and 25..100 580 and 239; over
+// 16000 and 500..2000 312 and 290.  The border takes 64 of 8 over 4000 and 25..100
+// for short, where it loses: 98 and 91.)
 template <bool BF, bool F8, int D, int RT, bool SH>
 __global__ __launch_bounds__(256, 2) void shared_kernel(AttendArgs) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -696,7 +710,7 @@ __global__ __launch_bounds__(256, 2) void shared_kernel(AttendArgs) {
     const int low = lowest_token(*ap, before, words);
     const int granules = (before - low + kPrefixTokens - 1) / kPrefixTokens;
     const int64_t first = (int64_t)granules * ap->pre_tiles * ap->c.H;
-    const int64_t second = (int64_t)own_granules(*ap, before, words + 4) * kOwnCost / 2;
+    const int64_t second = own_cost(*ap, before, words + 4) / 2;
     if (first + second < (int64_t)kLongWalk * grid && grid >= 16) {
       const int share = (int)((uint32_t)(first * grid) / (uint32_t)(first + second + 1)) & ~7;
       common = min(common, min(max(share, 8), grid - 8));
