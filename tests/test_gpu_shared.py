@@ -94,6 +94,20 @@ def test_more_rows_than_a_tile():
     parity(p, 256, "2240 rows")
 
 
+@pytest.mark.parametrize("B,M,H,G,shared,own", [
+    (40, 8, 8, 6, 640, 60),    # 120 items: several workgroups for each, each within one
+    (60, 8, 8, 6, 448, 600),   # 176: common and own tokens in separate workgroups, and in turn
+    (48, 16, 8, 9, 384, 40),   # 432: one for each, or ranges over two
+    (64, 16, 8, 12, 128, 30),  # 768: more items than workgroups
+])
+@pytest.mark.parametrize("ct,D", [(BF, 128), (F8, 64)])
+def test_many_items(B, M, H, G, shared, own, ct, D):
+    rows = [M if b % 4 else 1 + b % M for b in range(B)]
+    lens = [shared + own] + [shared + max(rows[b], own * (b % 5) // 5) for b in range(1, B)]
+    p = problem(shared, rows, lens, H=H, G=G, D=D, page=32, dtype=ct, seed=B)
+    parity(p, shared, f"{B} sequences of {M} rows, {ct} D={D}")
+
+
 def test_missing_pages_in_the_prefix():
     p = problem(128, [2, 3, 1], [200, 180, 140], H=2, G=3, D=128, page=16, seed=5, poison=False)
     p.table[:, 2] = -1
