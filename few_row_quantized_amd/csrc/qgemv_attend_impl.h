@@ -905,12 +905,14 @@ __device__ __forceinline__ void attend_body(KernArgs *ap, uint8_t *const lds, co
           const float mn = fmaxf(m[r], m2);
           const float f1 = weight_of(m[r], mn), f2 = weight_of(m2, mn);
           m[r] = mn;
-          l[r] = l[r] * f1 + l2 * f2;
+          // (which product is rounded is written out: the compiler's choice changes
+          // with the code around it)
+          l[r] = __builtin_fmaf(l[r], f1, l2 * f2);
 #pragma unroll
           for (int e = 0; e < NE; ++e) {
             const f32x4_t y = give[((from * RT + r) * NE + e) * 64 + lane];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][e][i] = acc[r][e][i] * f1 + y[i] * f2;
+            for (int i = 0; i < 4; ++i) acc[r][e][i] = __builtin_fmaf(y[i], f2, acc[r][e][i] * f1);
           }
         }
       }
