@@ -19,7 +19,7 @@
 // LDS, once for four waves.
 //
 // 64 sequences of up to 8 rows, 8 heads of 6 query heads over 16384 common tokens
-// of D = 128 and 500..2000 of their own, bf16: 306 us, where 190 GFLOP at the rate
+// of D = 128 and 500..2000 of their own, bf16: 304 us, where 190 GFLOP at the rate
 // of a product of 16384^3 would take 137.  What bounds it is waiting between two
 // products, for the LDS and for exponentials, with two waves of a SIMD: 256
 // registers of each hold 64 sums, 32 scores and 32 queries.  Without the
@@ -87,8 +87,8 @@ constexpr size_t prefix_lds(int D) { return kPrefixHead + (size_t)2 * kPrefixTok
 // 16-bit caches at D = 128 are loaded straight to the LDS, 4 tokens and 1 KiB an
 // instruction, so rows lie together in fours with 16 bytes after them, and a row's
 // quarters of 64 bytes are exchanged by the token's place in its four: lanes read
-// different banks as above.  (The case above: 314 -> 306 us; a head of D = 128 over
-// 64 sequences of 1 row: 46.6 -> 43.1.)  Rows of D = 64 and D = 256 through
+// different banks as above.  (The case above, through registers 314, so 306 us; a head of D = 128 over
+// 64 sequences of 1 row 46.6 and 43.1.)  Rows of D = 64 and D = 256 through
 // registers, as E4M3 has to be, which is widened on the way.
 constexpr int kFour = 4 * 256 + 16;
 
