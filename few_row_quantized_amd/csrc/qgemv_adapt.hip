@@ -453,11 +453,11 @@ int launch_adapt_t(const AdaptArgs &a, hipStream_t stream) {
 constexpr int kAdaptFill = 1;
 
 int64_t plan_adapt(AdaptArgs *a) {
-  const int each = (a->T + a->n - 1) / a->n;  // rows of an adapter, where all have as many
+  const int each = (a->T - 1) / a->n + 1;  // rows of an adapter, where all have as many
   a->rt = each <= 16 ? 1 : each <= 32 ? 2 : 4;
   const int size = 16 * a->rt;
   // the most tiles: every adapter, and the rows without one, end in a part of one
-  a->tiles = std::min(a->T, a->T / size + std::min(a->n + 1, a->T));
+  a->tiles = std::min(a->T, a->T / size + std::min(a->n, a->T - 1) + 1);
   a->rk = a->r <= 16 ? 1 : a->r <= 32 ? 2 : 4;
   const int ranks = (a->r + 16 * a->rk - 1) / (16 * a->rk), steps = (a->K + 31) / 32;
   a->splits = std::max(1, std::min({kAdaptSplits, steps / 8, kAdaptFill * device_cu_count() / (a->tiles * ranks)}));

@@ -83,6 +83,11 @@ int64_t extent(int64_t T, int64_t row, int64_t heads, int64_t head, int64_t dim,
   return T < 1 ? 0 : ((T - 1) * row + (heads - 1) * head + dim) * bytes;
 }
 
+// Whether no two values of an operand lie in one place: rows apart, or heads.
+bool distinct(int64_t T, int64_t row, int64_t heads, int64_t head, int64_t dim) {
+  return T <= 1 || heads <= 1 || row >= (heads - 1) * head + dim || head >= (T - 1) * row + dim;
+}
+
 // What attention calls have in common, but for the workspace.
 int attend_args(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head, void *out, int64_t out_row,
                 int64_t out_head, int q_dtype, float *lse, const int32_t *start, const int32_t *len, int T, int M,
@@ -251,6 +256,7 @@ int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t 
   if (T == 0) return QGEMV_OK;
   if (T > kMaxWorkgroups || (q_heads + 2 * (int64_t)a.c.H) * a.c.D > kMaxRow) return QGEMV_EUNSUPPORTED;
   const int64_t b = elem_bytes(src_dtype);
+  if (!distinct(T, out_row, q_heads, out_head, a.c.D)) return QGEMV_EINVAL;
   // in place, value for value, or apart
   const bool in_place = out == q && out_dtype == src_dtype && out_row == q_row && out_head == q_head;
   if (!in_place && overlap(q, extent(T, q_row, q_heads, q_head, a.c.D, b), out,

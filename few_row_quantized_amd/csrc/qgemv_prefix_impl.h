@@ -154,21 +154,21 @@ constexpr int kLongWalk = 48;
 
 // What the sequences' own tokens cost, in halves of a common granule.
 template <class Args>
-__device__ __forceinline__ int own_cost(Args &a, int before, int *lds) {
-  int sum = 0;
+__device__ __forceinline__ int64_t own_cost(Args &a, int before, int *lds) {
+  uint32_t sum = 0;  // below 2^32 with 2^30 granules and 2^24 items
   for (int b = threadIdx.x; b < a.B; b += 256) {
     const SeqWork w = seq_work<true>(a, b, before);
-    sum += w.items * (w.granules * kOwnCost + kItemCost);
+    sum += (uint32_t)w.items * ((uint32_t)w.granules * kOwnCost + kItemCost);
   }
-  sum += __builtin_amdgcn_update_dpp(0, sum, 0x111, 0xF, 0xF, false);
-  sum += __builtin_amdgcn_update_dpp(0, sum, 0x112, 0xF, 0xF, false);
-  sum += __builtin_amdgcn_update_dpp(0, sum, 0x114, 0xF, 0xF, false);
-  sum += __builtin_amdgcn_update_dpp(0, sum, 0x118, 0xF, 0xF, false);
-  sum += __builtin_amdgcn_update_dpp(0, sum, 0x142, 0xA, 0xF, false);
-  sum += __builtin_amdgcn_update_dpp(0, sum, 0x143, 0xC, 0xF, false);
-  lds[threadIdx.x >> 6] = __builtin_amdgcn_readlane(sum, 63);
+  sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x111, 0xF, 0xF, false);
+  sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x112, 0xF, 0xF, false);
+  sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x114, 0xF, 0xF, false);
+  sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x118, 0xF, 0xF, false);
+  sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x142, 0xA, 0xF, false);
+  sum += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x143, 0xC, 0xF, false);
+  lds[threadIdx.x >> 6] = (int)__builtin_amdgcn_readlane(sum, 63);
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(lds[0] + lds[1] + lds[2] + lds[3]);
+  return (uint32_t)__builtin_amdgcn_readfirstlane(lds[0] + lds[1] + lds[2] + lds[3]);
 }
 
 template <bool BF, bool F8, int D>

@@ -443,8 +443,9 @@ int qgemv_kv_attend_shared(const qgemv_kv_cache *cache, const void *q, int64_t q
  * interleaved 2 i and 2 i + 1; a head's values from 2 * pairs on, and all of
  * new_v, stay.
  *   q       [T][q_heads][dim] of src_dtype; out the same of out_dtype
- *           (QGEMV_BF16 or QGEMV_F16): q itself (same type and strides), or
- *           apart from it (QGEMV_EINVAL).  Rows of no sequence are left
+ *           (QGEMV_BF16 or QGEMV_F16), its values all in places of their own:
+ *           q itself (same type and strides), or apart from it (QGEMV_EINVAL),
+ *           and apart from new_k and new_v.  Rows of no sequence are left
  *           unwritten.
  *   freq    fp32 [pairs], DEVICE; pairs a multiple of 8, at most dim / 2.
  *   position  int32 [axes][T], DEVICE, axes position_axis elements apart: the
@@ -483,7 +484,8 @@ int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t 
  *           logit of +inf leaves a row's softmax without values: weights NaN.
  *   bias    fp32 [E], DEVICE, or NULL.
  * Scores and choices are fp64; without a bias and with best = 1 the choice is
- * by the logits themselves, which their scores' order is.  Deterministic.
+ * by the logits themselves, which their scores' order is.  Choices count as
+ * equal within 2^-48 of their value.  Deterministic.
  * At most QGEMV_MAX_ROUTED experts, QGEMV_MAX_GROUPS groups, k of
  * QGEMV_MAX_CHOSEN (QGEMV_EUNSUPPORTED) and of the experts of `keep` groups
  * (QGEMV_EINVAL); 2^24 rows are too many.

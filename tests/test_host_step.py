@@ -72,6 +72,9 @@ def test_attend_shared_refusals(kw, want):
     # over the queries, but not value for value
     (dict(out=A), q.EINVAL), (dict(out=A + 16, src=q.BF16), q.EINVAL), (dict(out=A, src=q.F16), q.EINVAL),
     (dict(out=A, src=q.BF16, outr=6272), q.EINVAL),
+    # an output whose rows and heads lie over one another
+    (dict(outr=128), q.EINVAL), (dict(outr=6016), q.EINVAL), (dict(outr=256, outh=640), q.EINVAL),
+    (dict(out=A, src=q.BF16, outr=128, xr=128), q.EINVAL),
     (dict(T=0), q.OK), (dict(T=0, out=A), q.OK), (dict(T=0, pairs=12), q.EINVAL), (dict(T=1 << 24), q.EUNSUPPORTED),
     (dict(heads=1 << 23, xr=1 << 30, outr=1 << 30, out=1 << 60), q.EUNSUPPORTED),
 ])
