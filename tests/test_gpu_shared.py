@@ -265,3 +265,34 @@ def test_long_prefix_against_the_attention(qt, ct):
     rel = (a.double() - b.double()).norm() / a.double().norm()
     assert rel <= 2 * 2 * u, rel
     assert ((la - lb).abs() <= 1e-4).all()
+
+
+def test_pages_past_4_gib():
+    """Pages anywhere in a large cache give what the same pages close together
+    give, and rotated rows go to them."""
+    page, H, D, B, width = 64, 8, 128, 3, 7
+    g = torch.Generator(device="cuda").manual_seed(1)
+    near = [torch.randn(24, page, H, D, device="cuda", generator=g).to(BF) for _ in range(2)]
+    far = [torch.empty((1 << 15) + 600, page, H, D, device="cuda", dtype=BF) for _ in range(2)]  # 4.4e9 bytes each
+    places = torch.randperm(24, device="cuda", generator=g) * 24 + (1 << 15)
+    places[:4] = torch.tensor([0, 9, (1 << 14) + 1, (1 << 15) - 1], device="cuda")
+    for a, b in zip(near, far):
+        b[places] = a
+    table = torch.arange(B * width, device="cuda", dtype=torch.int32).reshape(B, width)
+    table[:, :4] = table[0, :4]
+    lens, start = torch.tensor([430, 300, 257], dtype=torch.int32, device="cuda"), torch.tensor([0, 4, 7, 8], dtype=torch.int32, device="cuda")
+    x = [torch.randn(8, h, D, device="cuda", generator=g) for h in (4 * H, H, H)]
+    freq = torch.logspace(0, -4, 64, device="cuda")
+    shared = torch.full((1,), 256, dtype=torch.int32, device="cuda")
+    results = []
+    for (k, v), ids in ((near, table), (far, places[table.long()].int())):
+        cache = q.KvCache(k, v, ids)
+        turned = q.append_rotated(cache, *x, start, lens, freq)
+        lse = torch.empty(8, 4 * H, device="cuda")
+        out = q.attend_shared(cache, turned, start, lens, 4, shared, lse=lse)
+        results.append((turned, out, lse))
+    torch.cuda.synchronize()
+    for a, b in zip(*results):
+        assert torch.equal(a, b) and torch.isfinite(a.float()).all()
+    for a, b in zip(near, far):
+        assert torch.equal(a, b[places])
