@@ -317,9 +317,16 @@ __global__ __launch_bounds__(256) void adapt_up_kernel(AdaptArgs a) {
 #pragma unroll
       for (int x = 0; x < Q; ++x) {
         const int k = (x * 16 + c) * 4;
+        // the most parts that there can be, on their way together
+        f32x4_t part[kAdaptSplits];
+#pragma unroll
+        for (int s = 0; s < kAdaptSplits; ++s)
+          part[s] = *reinterpret_cast<const f32x4_t *>(p + (int64_t)min(s, a.splits - 1) * a.T * a.r + (k < a.r ? k : 0));
         v[x] = f32x4_t{0, 0, 0, 0};
-        if (k < a.r)
-          for (int s = 0; s < a.splits; ++s) v[x] += *reinterpret_cast<const f32x4_t *>(p + (int64_t)s * a.T * a.r + k);
+#pragma unroll
+        for (int s = 0; s < kAdaptSplits; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[x][j] += s < a.splits && k < a.r ? part[s][j] : 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) most = fmaxf(most, __builtin_fabsf(v[x][j]));
       }
