@@ -84,6 +84,52 @@ __device__ __forceinline__ int find_rows(const int32_t *adapter, int T, int n, b
   }
 }
 
+// The same for up to 64 rows, a lane's row beside all: the rows that share its
+// adapter are those whose adapters agree in every bit, the first of them counts
+// their tiles.  (64 adapters of a row each: 24 -> MEASURED us, which a step for each
+// adapter before the tile's took.)
+template <int S>
+__device__ __forceinline__ int find_rows_wave(const int32_t *adapter, int T, int n, bool rest, int tile, int lane,
+                                              int *rows, int *which) {
+  const int mine = lane < T ? adapter[lane] : -1;
+  const bool has = (uint32_t)mine < (uint32_t)n;
+  const uint64_t none = __ballot(lane < T && !has);
+  uint64_t same = __ballot(has);
+  for (int bits = n - 1, bit = 0; bits >> bit; ++bit) {
+    const bool is = mine >> bit & 1;
+    const uint64_t with = __ballot(is);
+    same &= is ? with : ~with;
+  }
+  const bool leads = has && (int)__ffsll((long long)same) - 1 == lane;
+  const int tiles = leads ? (__popcll(same) + S - 1) / S : 0;
+  int in = tiles;  // sums over the lanes up to each
+  in += __builtin_amdgcn_update_dpp(0, in, 0x111, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x112, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x114, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x118, 0xF, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x142, 0xA, 0xF, false);
+  in += __builtin_amdgcn_update_dpp(0, in, 0x143, 0xC, 0xF, false);
+  const uint64_t hit = __ballot(leads && tile >= in - tiles && tile < in);
+  uint64_t mask = none;
+  int first = (tile - __builtin_amdgcn_readlane(in, 63)) * S;
+  *which = -1;
+  if (hit) {
+    const int from = (int)__ffsll((long long)hit) - 1;
+    *which = __builtin_amdgcn_readlane(mine, from);
+    mask = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(same >> 32), from) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)same, from);
+    first = (tile - __builtin_amdgcn_readlane(in - tiles, from)) * S;
+  } else if (!rest) {
+    return 0;
+  }
+  const int count = __popcll(mask) - first;
+  if (count <= 0) return 0;
+  const int at = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0)) - first;
+  if ((mask >> lane & 1) && at >= 0 && at < S) rows[at] = lane;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return min(count, S);
+}
+
 // The same by the whole workgroup for more rows, of at most kMapped adapters: a
 // bit for each row and adapter in LDS, whose counts give the tiles (adapters in
 // their own order).  64 adapters among 512 rows: one pass of some steps where the
@@ -173,7 +219,10 @@ __device__ __forceinline__ int find(const AdaptArgs &a, bool rest, int lane, int
                               reinterpret_cast<uint32_t(*)[kMapRow]>(scratch + 32),
                               reinterpret_cast<int *>(scratch), rows, which);
   }
-  return find_rows<NC>(a.adapter, a.T, a.n, rest, blockIdx.x, S, lane, rows + wave * S, which);
+  if constexpr (NC == 1)
+    return find_rows_wave<S>(a.adapter, a.T, a.n, rest, blockIdx.x, lane, rows + wave * S, which);
+  else
+    return find_rows<NC>(a.adapter, a.T, a.n, rest, blockIdx.x, S, lane, rows + wave * S, which);
 }
 
 // First product: part[split][t][i] = sum over the split's k of A[i][k] x[t][k].
@@ -426,12 +475,13 @@ int launch_adapt_up(const AdaptArgs &a, hipStream_t stream) {
 
 template <bool BF, int NC, int RT>
 int launch_adapt_rt(const AdaptArgs &a, hipStream_t stream) {
+  const dim3 grid(a.tiles, a.splits, (a.r + 16 * a.rk - 1) / (16 * a.rk)), block(256);
   if (a.rk == 1)
-    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 1>), dim3(a.tiles, a.splits), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 1>), grid, block, 0, stream, a);
   else if (a.rk == 2)
-    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 2>), dim3(a.tiles, a.splits), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 2>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 4>), dim3(a.tiles, a.splits, (a.r + 63) / 64), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 4>), grid, block, 0, stream, a);
   if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
   return a.r <= 32 ? launch_adapt_up<BF, NC, RT, 1>(a, stream)
          : a.r <= 64 ? launch_adapt_up<BF, NC, RT, 2>(a, stream)
@@ -462,10 +512,13 @@ constexpr int kAdaptFill = 1;
 int64_t plan_adapt(AdaptArgs *a) {
   const int each = (a->T - 1) / a->n + 1;  // rows of an adapter, where all have as many
   a->rt = each <= 16 ? 1 : each <= 32 ? 2 : 4;
-  const int size = 16 * a->rt;
   // the most tiles: every adapter, and the rows without one, end in a part of one
-  a->tiles = std::min(a->T, a->T / size + std::min(a->n, a->T - 1) + 1);
+  const auto tiles = [&] { return std::min(a->T, a->T / (16 * a->rt) + std::min(a->n, a->T - 1) + 1); };
+  const int columns = a->r <= 64 ? 256 : 128;  // of a workgroup of the second product
+  while (a->rt > 1 && tiles() * ((a->N + columns - 1) / columns) < device_cu_count()) a->rt /= 2;
+  a->tiles = tiles();
   a->rk = a->r <= 16 ? 1 : a->r <= 32 ? 2 : 4;
+  while (a->rk > 1 && a->tiles * ((a->r + 16 * a->rk - 1) / (16 * a->rk)) * kAdaptSplits < device_cu_count()) a->rk /= 2;
   const int ranks = (a->r + 16 * a->rk - 1) / (16 * a->rk), steps = (a->K + 31) / 32;
   a->splits = std::max(1, std::min({kAdaptSplits, steps / 8, kAdaptFill * device_cu_count() / (a->tiles * ranks)}));
   // the most splits: so the size grows with T and r alone
