@@ -15,7 +15,7 @@
 // row's largest, for which the row is scaled by a power of two first).
 //
 // Bound by memory where there is work, by latency where there is little.  On an
-// MI355X: 5 rows of one request, rank 16, 5120 to 6144: 4.0 + 6.0 us; 455 rows of
+// MI355X: 5 rows of one request, rank 16, 5120 to 6144: 4.0 + 5.0 us; 455 rows of
 // 64 requests, 32 adapters of rank 64, 5120 to 17408: 14 + 31 us, 26 and 125 MB
 // (B 71, y and out 32 each).
 
@@ -86,8 +86,8 @@ __device__ __forceinline__ int find_rows(const int32_t *adapter, int T, int n, b
 
 // The same for up to 64 rows, a lane's row beside all: the rows that share its
 // adapter are those whose adapters agree in every bit, the first of them counts
-// their tiles.  (64 adapters of a row each: 24 -> MEASURED us, which a step for each
-// adapter before the tile's took.)
+// their tiles.  (64 adapters of a row each: 13 us, 24 with a step for each
+// adapter before the tile's.)
 template <int S>
 __device__ __forceinline__ int find_rows_wave(const int32_t *adapter, int T, int n, bool rest, int tile, int lane,
                                               int *rows, int *which) {
@@ -515,9 +515,17 @@ int64_t plan_adapt(AdaptArgs *a) {
   // the most tiles: every adapter, and the rows without one, end in a part of one
   const auto tiles = [&] { return std::min(a->T, a->T / (16 * a->rt) + std::min(a->n, a->T - 1) + 1); };
   const int columns = a->r <= 64 ? 256 : 128;  // of a workgroup of the second product
-  while (a->rt > 1 && tiles() * ((a->N + columns - 1) / columns) < device_cu_count()) a->rt /= 2;
+  // Larger tiles read an adapter less often, smaller ones make more workgroups of
+  // the second product, which are wanted up to the four that a CU has (us, as the
+  // rows of an adapter say and so: 64 rows of one adapter of rank 16, 5120 to 6144,
+  // 16.8 and 8.9; of rank 128 to 17408 20.1 and 14.6; 512 rows of 8 of rank 64 to
+  // 6144 29 and 25, of one to 17408 35 and 31).
+  while (a->rt > 1 && tiles() * ((a->N + columns - 1) / columns) < 4 * device_cu_count()) a->rt /= 2;
   a->tiles = tiles();
   a->rk = a->r <= 16 ? 1 : a->r <= 32 ? 2 : 4;
+  // Fewer ranks a wave read x more often, and leave no CU without a workgroup of the
+  // first product (5 rows of rank 128, 17408 to 5120: 17.2 us with 4 tiles of ranks,
+  // 12.3 so; for two a CU 512 rows of 16 adapters of rank 64 lose, 35 and 41).
   while (a->rk > 1 && a->tiles * ((a->r + 16 * a->rk - 1) / (16 * a->rk)) * kAdaptSplits < device_cu_count()) a->rk /= 2;
   const int ranks = (a->r + 16 * a->rk - 1) / (16 * a->rk), steps = (a->K + 31) / 32;
   a->splits = std::max(1, std::min({kAdaptSplits, steps / 8, kAdaptFill * device_cu_count() / (a->tiles * ranks)}));

@@ -332,8 +332,8 @@ def adapters(T, n, r, K, N, dtype=BF, seed=0, spread=1.0):
 
 def check_adapt(out, y, x, a, b, adapter, scales, label):
     """The bound: K products summed in fp32 in parts of any order, K + 8 roundings;
-    the sums in two parts (2^-17 of each in bf16; in fp16 2^-23 of the row's
-    largest, with 2^-17 kept here for the sum over the rank); r products of both
+    the sums in parts (2^-24 of each in bf16; in fp16 2^-23 of the row's largest,
+    with 2^-17 kept here for both and the sum over the rank); r products of the
     parts; scale and the sum with y, 3 roundings."""
     d = lambda t: None if t is None else t.double().numpy()  # noqa: E731
     ref, down, up = oracle.adapt_reference(d(y), d(x), d(a), d(b), adapter.tolist(), d(scales))
@@ -352,6 +352,20 @@ def check_adapt(out, y, x, a, b, adapter, scales, label):
     (130, 90, 16, 128, 64), (512, 2, 16, 64, 48), (513, 3, 40, 72, 20), (1100, 5, 16, 64, 17), (3, 2, 256, 2048, 300),
     (90, 1, 256, 96, 65), (2, 300, 16, 8, 1)])
 def test_adapt(dtype, T, n, r, K, N):
+    say(f"adapt {dtype} T={T} n={n} r={r} K={K} N={N}")
+    y, x, a, b, adapter, scales = adapters(T, n, r, K, N, dtype, seed=T + r)
+    out = q.adapt(y.cuda(), x.cuda(), a.cuda(), b.cuda(), adapter.cuda(), scales=scales.cuda())
+    torch.cuda.synchronize()
+    check_adapt(out, y, x, a, b, adapter, scales, f"{dtype} T={T} n={n} r={r} K={K} N={N}")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,n,r,K,N", [
+    (512, 8, 16, 256, 16000), (64, 1, 72, 64, 44000), (64, 1, 200, 40, 44000),  # tiles of 64 rows
+    (64, 2, 72, 64, 27000), (512, 16, 40, 64, 10500), (200, 8, 16, 64, 20000),  # of 32
+    (512, 300, 24, 64, 40), (100, 500, 8, 64, 20), (512, 256, 48, 128, 30),  # many adapters
+    (300, 40, 256, 512, 70), (5, 8, 128, 4096, 64)])  # several tiles of ranks a wave, and one
+def test_adapt_tiles(dtype, T, n, r, K, N):
     say(f"adapt {dtype} T={T} n={n} r={r} K={K} N={N}")
     y, x, a, b, adapter, scales = adapters(T, n, r, K, N, dtype, seed=T + r)
     out = q.adapt(y.cuda(), x.cuda(), a.cuda(), b.cuda(), adapter.cuda(), scales=scales.cuda())
