@@ -227,12 +227,16 @@ __device__ __forceinline__ int find(const AdaptArgs &a, bool rest, int lane, int
 
 // First product: part[split][t][i] = sum over the split's k of A[i][k] x[t][k].
 // A wave takes RK tiles of 16 ranks; the waves of a workgroup cut its K once more
-// and add up through LDS.
+// and add up through LDS, where the bitmaps have been (64 rows by 64 ranks: 50 KB of
+// it, 67 with both side by side, past the 64 that a kernel has without asking).
 template <bool BF, int NC, int RT, int RK>
 __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs a) {
   __shared__ int all_rows[4 * 16 * RT];
-  __shared__ f32x4_t sums[3][RT * RK][64];
-  __shared__ __align__(16) uint8_t scratch[NC > 1 ? kMapBytes : 16];
+  constexpr size_t kSums = (size_t)3 * RT * RK * 64 * sizeof(f32x4_t);
+  __shared__ __align__(16) uint8_t scratch[NC > 1 && kMapBytes > kSums ? kMapBytes : kSums];
+  static_assert(sizeof(all_rows) + sizeof(scratch) <= 64 * 1024, "LDS that a kernel has without asking");
+  // (the search for the rows ends with a barrier)
+  f32x4_t(*const sums)[RT * RK][64] = reinterpret_cast<f32x4_t(*)[RT * RK][64]>(scratch);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;

@@ -65,3 +65,23 @@ def mfma_configuration(M: int, N: int, K: int, bits: int, gs: int, cus: int):
         if c is not None:
             return ("long_k",) + c
     return ("single_pass",)
+
+
+def adapt_plan(T: int, n: int, r: int, K: int, N: int, cus: int):
+    """Which kernels a qgemv_adapt call on T rows (512 at most, what is passed to
+    them together) runs, as plan_adapt chooses them: 64-row words of the search
+    (1: one wave's), 16-row tiles of a tile, 16-rank tiles of a wave of the first
+    product, 32-rank steps of the second."""
+    each = (T - 1) // n + 1
+    rt = 1 if each <= 16 else 2 if each <= 32 else 4
+    columns = 256 if r <= 64 else 128
+
+    def tiles():
+        return min(T, T // (16 * rt) + min(n, T - 1) + 1)
+
+    while rt > 1 and tiles() * -(-N // columns) < 4 * cus:
+        rt //= 2
+    rk = 1 if r <= 16 else 2 if r <= 32 else 4
+    while rk > 1 and tiles() * -(-r // (16 * rk)) * 8 < cus:
+        rk //= 2
+    return (1 if T <= 64 else 8), rt, rk, 1 if r <= 32 else 2 if r <= 64 else 4 if r <= 128 else 8

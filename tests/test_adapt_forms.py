@@ -1,0 +1,24 @@
+"""The shapes of the adapters' GPU tests against the plan (no GPU)."""
+import itertools
+
+from adapt_util import FORMS
+from kernel_config import adapt_plan
+
+CUS = 256  # of an MI355X
+
+
+def planned():
+    """Every form that a call can take, over sizes on both sides of each border."""
+    rows = [1, 2, 5, 8, 12, 16, 17, 24, 31, 32, 33, 48, 63, 64, 65, 96, 100, 128, 130, 192, 200, 256, 320, 384, 448, 511, 512]
+    adapters = [1, 2, 3, 4, 6, 7, 8, 10, 12, 16, 24, 32, 64, 100, 256, 257, 5000]
+    columns = [1, 256, 1000, 4096, 6144, 8192, 11000, 16384, 17408, 27000, 44000, 65536, 131072, 1 << 22]
+    return {adapt_plan(T, n, r, 4096, N, CUS)
+            for T, n, r, N in itertools.product(rows, adapters, range(8, 257, 16), columns)}
+
+
+def test_the_shapes_reach_every_form():
+    """The first product's kernels (all but the last number) and the second's
+    (all but the ranks of the first)."""
+    want, got = planned(), {adapt_plan(*s, CUS) for s in FORMS}
+    assert {p[:3] for p in want} == {p[:3] for p in got}
+    assert {(p[0], p[1], p[3]) for p in want} == {(p[0], p[1], p[3]) for p in got}
