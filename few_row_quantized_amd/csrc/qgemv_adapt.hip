@@ -303,6 +303,11 @@ __global__ __launch_bounds__(256) void adapt_down_kernel(AdaptArgs a) {
     }
 }
 
+// The most rank tiles of a wave of the first product: up to 64 rows make at most
+// six tiles of 32 rows and three of 64, with which more would leave CUs without a
+// workgroup (plan_adapt's rule on 256 CUs comes to this by itself).
+constexpr int adapt_ranks(bool many_rows, int rt) { return many_rows ? 4 : 4 / rt; }
+
 typedef float f32x4_free_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // Second product and the sum.  STEPS of 32 ranks; a wave takes NB tiles of 16
@@ -480,12 +485,14 @@ int launch_adapt_up(const AdaptArgs &a, hipStream_t stream) {
 template <bool BF, int NC, int RT>
 int launch_adapt_rt(const AdaptArgs &a, hipStream_t stream) {
   const dim3 grid(a.tiles, a.splits, (a.r + 16 * a.rk - 1) / (16 * a.rk)), block(256);
-  if (a.rk == 1)
+  constexpr int most = adapt_ranks(NC > 1, RT);
+  if (a.rk == 1) {
     hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 1>), grid, block, 0, stream, a);
-  else if (a.rk == 2)
-    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 2>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 4>), grid, block, 0, stream, a);
+  } else if (a.rk == 2) {
+    if constexpr (most >= 2) hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 2>), grid, block, 0, stream, a);
+  } else {
+    if constexpr (most >= 4) hipLaunchKernelGGL((adapt_down_kernel<BF, NC, RT, 4>), grid, block, 0, stream, a);
+  }
   if (hipGetLastError() != hipSuccess) return QGEMV_EHIP;
   return a.r <= 32 ? launch_adapt_up<BF, NC, RT, 1>(a, stream)
          : a.r <= 64 ? launch_adapt_up<BF, NC, RT, 2>(a, stream)
@@ -530,6 +537,7 @@ int64_t plan_adapt(AdaptArgs *a) {
   // Fewer ranks a wave read x more often, and leave no CU without a workgroup of the
   // first product (5 rows of rank 128, 17408 to 5120: 17.2 us with 4 tiles of ranks,
   // 12.3 so; for two a CU 512 rows of 16 adapters of rank 64 lose, 35 and 41).
+  a->rk = std::min(a->rk, adapt_ranks(a->T > 64, a->rt));
   while (a->rk > 1 && a->tiles * ((a->r + 16 * a->rk - 1) / (16 * a->rk)) * kAdaptSplits < device_cu_count()) a->rk /= 2;
   const int ranks = (a->r + 16 * a->rk - 1) / (16 * a->rk), steps = (a->K + 31) / 32;
   a->splits = std::max(1, std::min({kAdaptSplits, steps / 8, kAdaptFill * device_cu_count() / (a->tiles * ranks)}));

@@ -81,7 +81,7 @@ def adapt_plan(T: int, n: int, r: int, K: int, N: int, cus: int):
 
     while rt > 1 and tiles() * -(-N // columns) < 4 * cus:
         rt //= 2
-    rk = 1 if r <= 16 else 2 if r <= 32 else 4
+    rk = min(1 if r <= 16 else 2 if r <= 32 else 4, 4 // rt if T <= 64 else 4)
     while rk > 1 and tiles() * -(-r // (16 * rk)) * 8 < cus:
         rk //= 2
     return (1 if T <= 64 else 8), rt, rk, 1 if r <= 32 else 2 if r <= 64 else 4 if r <= 128 else 8

@@ -1,8 +1,11 @@
 """The shapes of the adapters' GPU tests against the plan (no GPU)."""
 import itertools
 
+from few_row_quantized_amd import qgemv as q
+
 from adapt_util import FORMS
 from kernel_config import adapt_plan
+from kernel_objects import instances
 
 CUS = 256  # of an MI355X
 
@@ -22,3 +25,12 @@ def test_the_shapes_reach_every_form():
     want, got = planned(), {adapt_plan(*s, CUS) for s in FORMS}
     assert {p[:3] for p in want} == {p[:3] for p in got}
     assert {(p[0], p[1], p[3]) for p in want} == {(p[0], p[1], p[3]) for p in got}
+
+
+def test_the_library_has_these_kernels_and_no_others():
+    want = planned()
+    for dtype in (0, 1):
+        assert ({i[1:] for i in instances(q.LIB_PATH, "adapt_down_kernel") if i[0] == dtype}
+                == {p[:3] for p in want})
+        assert ({i[1:] for i in instances(q.LIB_PATH, "adapt_up_kernel") if i[0] == dtype}
+                == {(p[0], p[1], p[3]) for p in want})
