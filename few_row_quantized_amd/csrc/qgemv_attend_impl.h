@@ -294,6 +294,12 @@ constexpr int attend_occupancy(bool f8, int D, int rt, bool sh) {
 // 32, or 64 where keys and values do not wait in registers.
 constexpr bool queries_in_lds(int D, int rt, bool sh) { return D * rt >= (sh ? 512 : 256); }
 
+// Whether one tile of rows a wave can be the plan's choice: not where rows are split
+// over the waves (sh) from 65 on, since those are two tiles a wave at least.
+constexpr bool one_tile(bool f8, int D, bool sh, bool after_prefix) {
+  return !sh || D == 256 || (D == 128 && (after_prefix || !f8));
+}
+
 constexpr size_t kLdsHead = 2048 + 64;  // token offsets and the scan
 constexpr size_t attend_lds(bool f8, int D, int rt, bool sh) {
   const size_t q = queries_in_lds(D, rt, sh) ? (size_t)(sh ? 4 : 1) * rt * D * 32 : 0;
@@ -1126,7 +1132,9 @@ int launch_attend_d(const AttendArgs &a, hipStream_t stream) {
     if (a.rt == 3) return launch_attend_rt<BF, F8, D, 3, SH>(a, stream);
     if (a.rt == 4) return launch_attend_rt<BF, F8, D, 4, SH>(a, stream);
   }
-  return a.rt == 1 ? launch_attend_rt<BF, F8, D, 1, SH>(a, stream) : launch_attend_rt<BF, F8, D, 2, SH>(a, stream);
+  if constexpr (one_tile(F8, D, SH, false))
+    if (a.rt == 1) return launch_attend_rt<BF, F8, D, 1, SH>(a, stream);
+  return launch_attend_rt<BF, F8, D, 2, SH>(a, stream);
 }
 
 template <bool BF, bool F8>

@@ -764,7 +764,9 @@ int launch_shared_d(const AttendArgs &a, hipStream_t stream) {
     if (a.rt == 3) return launch_shared_rt<BF, F8, D, 3, SH>(a, stream);
   if constexpr (D == 64)
     if (a.rt == 4) return launch_shared_rt<BF, F8, D, 4, SH>(a, stream);
-  return a.rt == 1 ? launch_shared_rt<BF, F8, D, 1, SH>(a, stream) : launch_shared_rt<BF, F8, D, 2, SH>(a, stream);
+  if constexpr (one_tile(F8, D, SH, true))
+    if (a.rt == 1) return launch_shared_rt<BF, F8, D, 1, SH>(a, stream);
+  return launch_shared_rt<BF, F8, D, 2, SH>(a, stream);
 }
 
 template <bool BF, bool F8>

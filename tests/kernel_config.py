@@ -85,3 +85,14 @@ def adapt_plan(T: int, n: int, r: int, K: int, N: int, cus: int):
     while rk > 1 and tiles() * -(-r // (16 * rk)) * 8 < cus:
         rk //= 2
     return (1 if T <= 64 else 8), rt, rk, 1 if r <= 32 else 2 if r <= 64 else 4 if r <= 128 else 8
+
+
+def attend_form(rows: int, dim: int, f8: bool, short_table: bool, after_prefix: bool):
+    """(whether rows are split over the waves, 16-row tiles of a wave) of an
+    attention call with `rows` rows times query heads on a key-value head, as
+    plan_attend chooses them; short_table: of up to 128 tokens."""
+    most = 2 if dim == 256 else 3 if after_prefix and dim == 128 else 4
+    split = rows > 16 * most or (rows > 48 and dim == 128 and not f8 and short_table)
+    waves = 4 if split else 1
+    groups = -(-rows // (waves * 16 * most))
+    return split, -(-rows // (groups * waves * 16))
