@@ -51,3 +51,20 @@ def reference(y, x, a, b, adapter, scales=None):
         if x.dtype == torch.float16:
             tol[rows] += abs(s) * 2.0 ** -23 * v.abs().amax(1, keepdim=True) * bi.abs().sum(0)
     return out, tol + 3 * 2.0 ** -24 * (y.double().abs() + out.abs())
+
+
+def whole_numbers(T, n, r, K, dtype, seed):
+    """y = 0, x, a, b, adapter and the rank's sums v [T, r], on the CPU: sums of
+    24 bits, whole numbers that fp32 adds up exactly in any order, of which b
+    takes one to each column."""
+    g = torch.Generator().manual_seed(seed)
+    lo = int((2 ** 23 / K) ** 0.5) + 1  # sums from 2^23 on ..
+    hi = int(((2 ** 24 - 1) / K) ** 0.5)  # .. to below 2^24
+    assert lo < hi <= 256  # which bf16 has all
+    x = torch.randint(lo, hi + 1, (T, K), generator=g)
+    a = torch.randint(lo, hi + 1, (n, r, K), generator=g)
+    adapter = torch.randint(0, n, (T,), generator=g, dtype=torch.int32)
+    v = torch.stack([a[int(i)] @ row for i, row in zip(adapter, x)])
+    assert int(v.min()) >= 2 ** 23 and int(v.max()) < 2 ** 24
+    b = torch.eye(r).expand(n, r, r).contiguous()
+    return torch.zeros(T, r), x.to(dtype), a.to(dtype), b.to(dtype), adapter, v

@@ -1,9 +1,11 @@
 """The shapes of the adapters' GPU tests against the plan (no GPU)."""
 import itertools
 
+import torch
+
 from few_row_quantized_amd import qgemv as q
 
-from adapt_util import FORMS
+from adapt_util import FORMS, whole_numbers
 from kernel_config import adapt_plan
 from kernel_objects import instances
 
@@ -34,3 +36,18 @@ def test_the_library_has_these_kernels_and_no_others():
                 == {p[:3] for p in want})
         assert ({i[1:] for i in instances(q.LIB_PATH, "adapt_up_kernel") if i[0] == dtype}
                 == {(p[0], p[1], p[3]) for p in want})
+
+
+def test_two_parts_would_not_hold_the_sums():
+    """That the GPU test of whole numbers sees a missing part: two parts of bf16
+    have 16 to 18 bits of 24, one of fp16 11 to 12."""
+    v = whole_numbers(20, 2, 16, 256, torch.bfloat16, 1)[-1].double()
+    first = v.bfloat16().double()
+    second = (v - first).bfloat16().double()
+    third = (v - first - second).bfloat16().double()
+    assert (first + second + third == v).all() and (first + second != v).double().mean() > 0.9
+    scaled = v * 2.0 ** -10  # the largest between 2^13 and 2^14
+    one = scaled.half().double()
+    two = one + (scaled - one).half().double()
+    assert ((scaled - two).abs() <= 2.0 ** -23 * scaled.amax(1, keepdim=True)).all()
+    assert not ((scaled - one).abs() <= 2.0 ** -23 * scaled.amax(1, keepdim=True)).all()
