@@ -172,14 +172,24 @@ int launch_append_src(const AppendArgs &a, hipStream_t stream) {
 // 256 sequences from fp32 into bf16 queries and an E4M3 cache, positions of three
 // axes, 164 MB, 30 us (5.3 TB/s, past what a large copy reaches).
 
-// cos and sin of position * freq.  The product of 31 and 24 bits is taken in
-// fp64, and turned into quarter turns there: positions reach millions of turns.
-// What is left is at most an eighth of a turn, where the series of sin and cos
-// end at their 9th and 10th power (next terms below 2^-29 and 2^-30).
+// cos and sin of position * freq, in quarter turns: positions reach billions of
+// them.  The product of 31 and 24 bits and that with 2 / pi, itself in two parts
+// (its first 53 bits and the next), are each a fp64 number and what it rounds
+// off, so that below 2^40 what is left over whole ones is off by its own fp64 step
+// alone.  (With the numbers alone, angles near 2^40 were off by 2^-13.)  It is at
+// most an eighth of a turn and 2^-12, where the series of sin and cos end at their
+// 9th and 10th power (next terms below 2^-29 and 2^-30).
 __device__ __forceinline__ float2 turn_of(int position, float freq) {
-  const double quarters = (double)position * (double)freq * 0.63661977236758134308;  // 2 / pi
-  const double whole = __builtin_rint(quarters);
-  const float x = (float)((quarters - whole) * 1.57079632679489661923);
+  constexpr double kQuarters = 0.63661977236758134308, kQuartersRest = -3.935735335036497e-17;  // 2 / pi
+  double whole, left;
+  {
+#pragma clang fp contract(off)  // (what a product rounds off is added below)
+    const double p = position, f = freq, angle = p * f, angle_rest = __builtin_fma(p, f, -angle);
+    const double quarters = angle * kQuarters, quarters_rest = __builtin_fma(angle, kQuarters, -quarters);
+    whole = __builtin_rint(quarters);
+    left = (quarters - whole) + (quarters_rest + __builtin_fma(angle_rest, kQuarters, angle * kQuartersRest));
+  }
+  const float x = (float)(left * 1.57079632679489661923);
   const float y = x * x;
   const float s = x + x * y * (-1.0f / 6 + y * (1.0f / 120 + y * (-1.0f / 5040 + y * (1.0f / 362880))));
   const float c = 1.0f + y * (-0.5f + y * (1.0f / 24 + y * (-1.0f / 720 + y * (1.0f / 40320 + y * (-1.0f / 3628800)))));

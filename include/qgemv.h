@@ -453,9 +453,9 @@ int qgemv_kv_attend_shared(const qgemv_kv_cache *cache, const void *q, int64_t q
  *           sequence.
  *   axis    int32 [pairs], DEVICE, limited to 0 .. axes - 1: the axis of each
  *           pair; NULL: the first.  NULL where position is.
- * Angles are fp64, cos and sin fp32 (within 2^-22), a rotated value is rounded
- * to fp32 and then once to its type.  Other arguments, requirements and
- * errors as qgemv_kv_append.
+ * cos and sin are fp32, within 2^-22 where |p(t, i) * freq[i]| < 2^40; a rotated
+ * value is rounded to fp32 and then once to its type.  Other arguments,
+ * requirements and errors as qgemv_kv_append.
  */
 int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t q_row, int64_t q_head, int q_heads,
                             void *out, int64_t out_row, int64_t out_head, int out_dtype, const void *new_k,

@@ -31,6 +31,7 @@ from .kv_oracle import (  # noqa: F401
 )
 from .step_oracle import (  # noqa: F401
     adapt_reference,
+    angle_reference,
     rotate_reference,
     route_reference,
 )

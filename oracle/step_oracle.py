@@ -12,7 +12,34 @@ import math
 
 import numpy as np
 
-__all__ = ["rotate_reference", "route_reference", "adapt_reference"]
+__all__ = ["angle_reference", "rotate_reference", "route_reference", "adapt_reference"]
+
+
+_BITS = 256  # after the point
+
+
+def _pi() -> int:
+    """pi in units of 2^-_BITS: 16 arctan(1/5) - 4 arctan(1/239)."""
+    def arctan_of_one_over(n):
+        term = total = (1 << (_BITS + 16)) // n
+        i, sign = 3, -1
+        while term:
+            term //= n * n
+            total += sign * (term // i)
+            i, sign = i + 2, -sign
+        return total
+    return (16 * arctan_of_one_over(5) - 4 * arctan_of_one_over(239)) >> 16
+
+
+_TURN = 2 * _pi()
+
+
+def angle_reference(position, freq) -> float:
+    """position * freq less whole turns, rounded once: the product and the turns
+    in whole numbers, since neither fits fp64 where positions are far."""
+    num, den = float(freq).as_integer_ratio()
+    angle = (int(position) * num << _BITS) // den
+    return math.ldexp(float(angle - (2 * angle + _TURN) // (2 * _TURN) * _TURN), -_BITS)
 
 
 def rotate_reference(x, position, freq, axes=None, interleaved=False):
@@ -23,7 +50,7 @@ def rotate_reference(x, position, freq, axes=None, interleaved=False):
     for t in range(x.shape[0]):
         for i in range(pairs):
             axis = 0 if axes is None else min(max(int(axes[i]), 0), len(position) - 1)
-            angle = math.fmod(float(int(position[axis][t])) * float(freq[i]), 2 * math.pi)
+            angle = angle_reference(position[axis][t], freq[i])
             c, s = math.cos(angle), math.sin(angle)
             p, q = (2 * i, 2 * i + 1) if interleaved else (i, pairs + i)
             a, b = np.array(x[t, :, p]), np.array(x[t, :, q])
