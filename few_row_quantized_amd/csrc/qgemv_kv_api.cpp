@@ -74,13 +74,21 @@ int attend_shape(const qgemv_kv_cache *c, int M, int q_heads, int T) {
   return q_heads / c->heads <= QGEMV_MAX_GROUP ? QGEMV_OK : QGEMV_EUNSUPPORTED;
 }
 
-// Whether two [T][heads][dim] operands of 2-byte elements lie in common memory.
+// Whether two operands lie in common memory, by where they begin and end.
 bool overlap(const void *p, int64_t p_bytes, const void *q, int64_t q_bytes) {
   const uint8_t *a = static_cast<const uint8_t *>(p), *b = static_cast<const uint8_t *>(q);
   return a < b + q_bytes && b < a + p_bytes;
 }
 int64_t extent(int64_t T, int64_t row, int64_t heads, int64_t head, int64_t dim, int64_t bytes) {
   return T < 1 ? 0 : ((T - 1) * row + (heads - 1) * head + dim) * bytes;
+}
+
+// Whether two operands of rows `row` bytes apart, of which they take so many bytes
+// each, are different columns of one buffer: no row of one meets any of the other.
+bool columns_apart(const void *p, int64_t p_bytes, const void *q, int64_t q_bytes, int64_t row) {
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) % row;
+  const int64_t from = d < 0 ? d + row : d;  // where q's columns begin in p's row
+  return from >= p_bytes && row - from >= q_bytes;
 }
 
 // Whether no two values of an operand lie in one place: rows apart, or heads.
@@ -259,8 +267,10 @@ int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t 
   if (!distinct(T, out_row, q_heads, out_head, a.c.D)) return QGEMV_EINVAL;
   // in place, value for value, or apart
   const bool in_place = out == q && out_dtype == src_dtype && out_row == q_row && out_head == q_head;
-  if (!in_place && overlap(q, extent(T, q_row, q_heads, q_head, a.c.D, b), out,
-                           extent(T, out_row, q_heads, out_head, a.c.D, 2)))
+  if (!in_place &&
+      overlap(q, extent(T, q_row, q_heads, q_head, a.c.D, b), out, extent(T, out_row, q_heads, out_head, a.c.D, 2)) &&
+      !(q_row * b == out_row * 2 && columns_apart(q, extent(1, q_row, q_heads, q_head, a.c.D, b), out,
+                                                  extent(1, out_row, q_heads, out_head, a.c.D, 2), q_row * b)))
     return QGEMV_EINVAL;
   a.nk = static_cast<const uint8_t *>(new_k);
   a.nv = static_cast<const uint8_t *>(new_v);
@@ -342,7 +352,9 @@ int qgemv_adapt(const float *y, int64_t y_row, float *out, int64_t out_row, cons
   if (!aligned(y, 4) || !aligned(out, 4) || !aligned(x, 16) || x_row % 8 || !aligned(a, 16) || !aligned(b, 16) ||
       !aligned(adapter, 4) || !aligned(scales, 4) || !aligned(workspace, 16))
     return QGEMV_EALIGN;
-  if (out == y ? out_row != y_row : overlap(y, extent(T, y_row, 1, 0, N, 4), out, extent(T, out_row, 1, 0, N, 4)))
+  if (out == y ? out_row != y_row
+               : overlap(y, extent(T, y_row, 1, 0, N, 4), out, extent(T, out_row, 1, 0, N, 4)) &&
+                     !(y_row == out_row && columns_apart(y, 4 * (int64_t)N, out, 4 * (int64_t)N, 4 * y_row)))
     return QGEMV_EINVAL;
   if (workspace_bytes < qgemv_adapt_workspace(T, r)) return QGEMV_EINVAL;
   if (T > kMaxWorkgroups) return QGEMV_EUNSUPPORTED;

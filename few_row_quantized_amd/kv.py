@@ -120,7 +120,8 @@ def append_rotated(cache: KvCache, q, new_k, new_v, start, len, freq, position=N
     int32 [A, T], the rows' positions on A axes, and axes int32 [pairs], the
     axis of each pair (the first unless given); without position a row's place
     in its sequence.  Returns the turned queries: out, else a tensor of the
-    cache's type (bfloat16 for an 8-bit cache).  out may be q itself."""
+    cache's type (bfloat16 for an 8-bit cache).  out may be q itself, or other
+    columns of its buffer."""
     if stream is not None and out is None and cache.k.is_cuda:
         with _allocating(stream, cache.device):
             return append_rotated(cache, q, new_k, new_v, start, len, freq, position, axes, interleaved)
@@ -211,7 +212,7 @@ def adapt(y, x, a, b, adapter, scales=None, out=None, workspace=None, stream=Non
     """y + scales * B (A x) of each row's adapter: y float32 [T, N], a product
     of x [T, K]; a [n, r, K] and b [n, N, r] of x's type (bfloat16 or float16);
     adapter int32 [T], none where outside [0, n); scales float32 [n].  Returns
-    out, else a new tensor; out may be y itself."""
+    out, else a new tensor; out may be y itself, or other columns of its buffer."""
     if stream is not None and (out is None or workspace is None) and y.is_cuda:
         with _allocating(stream, y.device):
             return adapt(y, x, a, b, adapter, scales, out, workspace)
