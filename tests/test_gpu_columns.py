@@ -30,8 +30,9 @@ def test_adapted_rows_beside_the_product(T, N, gap, first):
     want, tol = reference(y, x, a, b, adapter, scales)
     assert ((out.double() - want).abs() <= tol).all() and torch.equal(src, y)
     assert (wide[:, N:N + gap] == 5).all()
+    at = gap + 1 if first else N - 1  # so that they have one column in common
     with pytest.raises(q.QgemvError):
-        q.adapt(src, x, a, b, adapter, out=wide[:, 1:N + 1])
+        q.adapt(src, x, a, b, adapter, out=wide[:, at:at + N])
 
 
 @pytest.mark.parametrize("src", [BF, torch.float16])
