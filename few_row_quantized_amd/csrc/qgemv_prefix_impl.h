@@ -239,7 +239,8 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
 
     // ---- the first tiles' page ids and the queries, on their way while the
     // rows' positions are found.  The queries take the scale's sign (and are 0
-    // where it is 0), so that the largest product has the largest score.
+    // where it is 0, with a NaN where one is not finite), so that the largest
+    // product has the largest score.
     auto tile_base = [&](int tile) { return (tile < sink_tiles ? tile : tile - sink_tiles + low_tile) * TOK; };
     // the page id of a lane's token
     auto load_id = [&](int tile) -> int {
@@ -285,8 +286,15 @@ __device__ __forceinline__ void prefix_body(KernArgs *ap, uint8_t *const lds, co
     const float sc = signed_sc == 0.0f ? 1.0f : __builtin_fabsf(signed_sc);
     {
       const uint32_t flip = signed_sc < 0.0f ? 0x80008000u : 0u, keep = signed_sc == 0.0f ? 0u : ~0u;
+      uint32_t odd = 0;
 #pragma unroll
-      for (int s = 0; s < QS; ++s) qf[s] = (qf[s] ^ flip) & keep;
+      for (int s = 0; s < QS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          odd |= nonfinite_signs<BF, false>(qf[s][i]);
+          qf[s][i] = (qf[s][i] ^ flip) & keep;
+        }
+      qf[0][0] |= (odd & kSigns<false>) != 0 ? ~keep : 0u;
     }
 
     auto is_edge = [&](int tb, uint64_t present) {
