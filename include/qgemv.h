@@ -482,7 +482,8 @@ int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t 
  *           is, is not there: it has no part in the softmax (its logit) and is
  *           not chosen, nor is a group of such.  Where fewer than k are there,
  *           the list ends with -1 (which qgemv_gather skips) and weight 0.  A
- *           logit of +inf leaves a row's softmax without values: weights NaN.
+ *           logit of +inf leaves a row's softmax without values: weights NaN
+ *           where the logits choose (below), no expert where the scores do.
  *   bias    fp32 [E], DEVICE, or NULL.
  * Scores and choices are fp64; without a bias and with best = 1 the choice is
  * by the logits themselves, which their scores' order is.  Choices count as
