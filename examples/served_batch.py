@@ -73,7 +73,8 @@ class ServedBatch(verify_step.Generation):
         self.adapters, self.system = adapters, len(system)
         self.share = share
         page = kw.get("page", 16)
-        whole = len(system) // page if share else 0
+        # (a request's last token is its own: it is fed with the first step)
+        whole = min(len(system), len(system) + min(map(len, prompts)) - 1) // page if share and len(system) else 0
         self.common = torch.tensor([whole * page], dtype=torch.int32, device=model.device)
         self.pages = whole
         super().__init__(model, [list(system) + list(p) for p in prompts], **kw)
