@@ -267,10 +267,13 @@ int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t 
   if (!distinct(T, out_row, q_heads, out_head, a.c.D)) return QGEMV_EINVAL;
   // in place, value for value, or apart
   const bool in_place = out == q && out_dtype == src_dtype && out_row == q_row && out_head == q_head;
-  if (!in_place &&
-      overlap(q, extent(T, q_row, q_heads, q_head, a.c.D, b), out, extent(T, out_row, q_heads, out_head, a.c.D, 2)) &&
-      !(q_row * b == out_row * 2 && columns_apart(q, extent(1, q_row, q_heads, q_head, a.c.D, b), out,
-                                                  extent(1, out_row, q_heads, out_head, a.c.D, 2), q_row * b)))
+  auto meets_out = [&](const void *p, int64_t row, int64_t heads, int64_t head) {
+    return overlap(p, extent(T, row, heads, head, a.c.D, b), out, extent(T, out_row, q_heads, out_head, a.c.D, 2)) &&
+           !(row * b == out_row * 2 && columns_apart(p, extent(1, row, heads, head, a.c.D, b), out,
+                                                     extent(1, out_row, q_heads, out_head, a.c.D, 2), row * b));
+  };
+  if ((!in_place && meets_out(q, q_row, q_heads, q_head)) || meets_out(new_k, k_row, a.c.H, k_head) ||
+      meets_out(new_v, v_row, a.c.H, v_head))
     return QGEMV_EINVAL;
   a.nk = static_cast<const uint8_t *>(new_k);
   a.nv = static_cast<const uint8_t *>(new_v);

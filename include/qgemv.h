@@ -444,10 +444,10 @@ int qgemv_kv_attend_shared(const qgemv_kv_cache *cache, const void *q, int64_t q
  * new_v, stay.
  *   q       [T][q_heads][dim] of src_dtype; out the same of out_dtype
  *           (QGEMV_BF16 or QGEMV_F16), its values all in places of their own:
- *           q itself (same type and strides), or apart from it (before or after
- *           it, or other columns, first to last, of rows as many bytes apart;
- *           QGEMV_EINVAL), and apart from new_k and new_v.  Rows of no sequence
- *           are left unwritten.
+ *           q itself (same type and strides), or apart from it, and apart from
+ *           new_k and new_v: before or after them, or other columns, first to
+ *           last, of rows as many bytes apart (QGEMV_EINVAL).  Rows of no
+ *           sequence are left unwritten.
  *   freq    fp32 [pairs], DEVICE; pairs a multiple of 8, at most dim / 2.
  *   position  int32 [axes][T], DEVICE, axes position_axis elements apart: the
  *           rows' positions on each axis; NULL: one axis, a row's place in its

@@ -36,3 +36,15 @@ def test_adapters_output_in_rows_of_another_length():
 ])
 def test_rotated_queries_over_the_queries(kw):
     assert run_rotated(cache(), **kw) == q.EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=1 << 41),                                         # where the keys begin
+    dict(out=(1 << 41) + 256 * 1024, outr=6144),               # within them
+    dict(out=(1 << 42) - 128, outr=6144),                      # over the first value
+    dict(heads=8, out=(1 << 41) + 3 * 256, outr=4096, kr=4096, vr=4096, src=q.BF16, nv=(1 << 41) + 8 * 256, x=(1 << 41) + 16 * 256, xr=4096),
+])
+def test_rotated_queries_over_the_keys_and_values(kw):
+    args = dict(nk=1 << 41, nv=1 << 42, T=300)
+    args.update(kw)
+    assert run_rotated(cache(), **args) == q.EINVAL
