@@ -3,9 +3,10 @@
 //   out[t] = y[t] + scale[a] * B[a] (A[a] x[t]),  a = adapter[t]
 //
 // A [n][r][K] and B [n][N][r] are small beside the projection's own weights, and
-// each that is used is read once for all rows that have it (once for every 64
-// of them): rows of one adapter, wherever they are among the T, make tiles of
-// 16, 32 or 64 and go through the matrix units together.  Two launches: the
+// each that is used is read once for every tile of the rows that have it, and anew
+// for every 512 rows of a call: rows of one adapter, wherever they are among the
+// T, make tiles of 16, 32 or 64 and go through the matrix units together (of 16
+// where larger ones would leave CUs without work: plan_adapt).  Two launches: the
 // first product with K cut over workgroups, whose partial sums the second adds
 // up in order.  Each workgroup finds the rows of its tile by itself among the
 // adapters of all rows (512 at most in a call of the kernels).
@@ -15,9 +16,9 @@
 // row's largest, for which the row is scaled by a power of two first).
 //
 // Bound by memory where there is work, by latency where there is little.  On an
-// MI355X: 5 rows of one request, rank 16, 5120 to 6144: 4.0 + 5.0 us; 455 rows of
-// 64 requests, 32 adapters of rank 64, 5120 to 17408: 14 + 31 us, 26 and 125 MB
-// (B 71, y and out 32 each).
+// MI355X: 5 rows of one request, rank 16, 5120 to 6144: 4.2 + 4.4 us; 438 rows of
+// 64 requests, 31 adapters of rank 64, 5120 to 17408: 14 + 32 us for 25 MB (A 20,
+// x 5) and 130 MB (B 69, y and out 30.5 each); by the counters 31 and 151 past L2.
 
 #include <algorithm>
 #include <type_traits>
@@ -516,7 +517,7 @@ int launch_adapt_t(const AdaptArgs &a, hipStream_t stream) {
 }  // namespace
 
 // Workgroups of the first product for each CU, counted as if every tile were there
-// (2, 4 and 8: parts that the second product has to read as well; the 455 rows above
+// (2, 4 and 8: parts that the second product has to read as well; the 438 rows above
 // 41.3 us with 1, 44.5 with 8).
 constexpr int kAdaptFill = 1;
 
