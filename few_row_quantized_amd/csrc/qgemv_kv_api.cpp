@@ -268,9 +268,16 @@ int qgemv_kv_append_rotated(const qgemv_kv_cache *cache, const void *q, int64_t 
   // in place, value for value, or apart
   const bool in_place = out == q && out_dtype == src_dtype && out_row == q_row && out_head == q_head;
   auto meets_out = [&](const void *p, int64_t row, int64_t heads, int64_t head) {
-    return overlap(p, extent(T, row, heads, head, a.c.D, b), out, extent(T, out_row, q_heads, out_head, a.c.D, 2)) &&
-           !(row * b == out_row * 2 && columns_apart(p, extent(1, row, heads, head, a.c.D, b), out,
-                                                     extent(1, out_row, q_heads, out_head, a.c.D, 2), row * b));
+    if (!overlap(p, extent(T, row, heads, head, a.c.D, b), out, extent(T, out_row, q_heads, out_head, a.c.D, 2)))
+      return false;
+    // columns of rows, or of heads where those of all rows are equally far apart (a
+    // head's query, key and value side by side)
+    if (row * b == out_row * 2 && columns_apart(p, extent(1, row, heads, head, a.c.D, b), out,
+                                                extent(1, out_row, q_heads, out_head, a.c.D, 2), row * b))
+      return false;
+    const int64_t step = std::min(row, head), out_step = std::min(out_row, out_head);
+    return !(step * b == out_step * 2 && row % step == 0 && head % step == 0 && out_row % out_step == 0 &&
+             out_head % out_step == 0 && columns_apart(p, a.c.D * b, out, (int64_t)a.c.D * 2, step * b));
   };
   if ((!in_place && meets_out(q, q_row, q_heads, q_head)) || meets_out(new_k, k_row, a.c.H, k_head) ||
       meets_out(new_v, v_row, a.c.H, v_head))

@@ -446,8 +446,9 @@ int qgemv_kv_attend_shared(const qgemv_kv_cache *cache, const void *q, int64_t q
  *           (QGEMV_BF16 or QGEMV_F16), its values all in places of their own:
  *           q itself (same type and strides), or apart from it, and apart from
  *           new_k and new_v: before or after them, or other columns, first to
- *           last, of rows as many bytes apart (QGEMV_EINVAL).  Rows of no
- *           sequence are left unwritten.
+ *           last, of rows as many bytes apart, or of heads where those of all
+ *           rows are equally far apart (QGEMV_EINVAL).  Rows of no sequence are
+ *           left unwritten.
  *   freq    fp32 [pairs], DEVICE; pairs a multiple of 8, at most dim / 2.
  *   position  int32 [axes][T], DEVICE, axes position_axis elements apart: the
  *           rows' positions on each axis; NULL: one axis, a row's place in its

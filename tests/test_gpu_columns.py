@@ -35,6 +35,25 @@ def test_adapted_rows_beside_the_product(T, N, gap, first):
         q.adapt(src, x, a, b, adapter, out=wide[:, at:at + N])
 
 
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("parts", [3, 4])
+def test_rotated_queries_of_heads_side_by_side(parts, heads_first):
+    """A head's query, key and value one after another: turned in place, or to a
+    place of their own after them."""
+    p = KvProblem([2, 5], [9, 30], H=4, G=1, D=64, page=8, dtype=BF)
+    rows = torch.randn(p.T, 4, parts, 64, generator=torch.Generator().manual_seed(2)).bfloat16()
+    d, freq, x = KvDevice(p), frequencies(32), rows.cuda()
+    if heads_first:
+        x = x.transpose(0, 1).contiguous().transpose(0, 1)
+    out = q.append_rotated(d.cache, x[:, :, 0], x[:, :, 1], x[:, :, 2], d.start, d.len, freq.cuda(),
+                           out=x[:, :, 0 if parts == 3 else 3])
+    torch.cuda.synchronize()
+    check_rotated(p, d, rows[:, :, 0], rows[:, :, 1], rows[:, :, 2], freq, None, None, False, out, "side by side")
+    assert torch.equal(x[:, :, 1:3].cpu(), rows[:, :, 1:3])
+    with pytest.raises(q.QgemvError):
+        q.append_rotated(d.cache, x[:, :, 0], x[:, :, 1], x[:, :, 2], d.start, d.len, freq.cuda(), out=x[:, :, 1])
+
+
 @pytest.mark.parametrize("src", [BF, torch.float16])
 def test_rotated_queries_beside_the_queries(src):
     """Queries, keys, values and the turned queries in one buffer."""

@@ -29,13 +29,16 @@ def test_adapters_output_in_rows_of_another_length():
     dict(heads=8, x=A + 7 * 256, xr=4096, out=A, outr=4096, src=q.BF16),
     # past the row's end, into the next one's queries
     dict(heads=8, x=A, xr=4096, out=A + 25 * 256, outr=4096, src=q.BF16),
-    # heads in turn, which take the whole row's columns
-    dict(heads=8, x=A, xr=2048, xh=256, out=A + 256, outr=2048, outh=256, src=q.BF16),
+    # heads in turn, which overlap by half
+    dict(heads=8, x=A, xr=2048, xh=256, out=A + 128, outr=2048, outh=256, src=q.BF16),
+    # heads of other lengths, and rows that do not hold whole ones
+    dict(heads=8, x=A, xr=2048, xh=256, out=A + 256, outr=2048, outh=128, src=q.BF16),
+    dict(heads=8, x=A, xr=2176, xh=256, out=A + 256, outr=2176, outh=256, src=q.BF16),
     # rows of other lengths in bytes
     dict(heads=8, x=A, xr=4096, out=A + 8 * 512, outr=4096, src=q.F32),
 ])
 def test_rotated_queries_over_the_queries(kw):
-    assert run_rotated(cache(), **kw) == q.EINVAL
+    assert run_rotated(cache(), nk=1 << 50, nv=1 << 51, **kw) == q.EINVAL
 
 
 @pytest.mark.parametrize("kw", [
